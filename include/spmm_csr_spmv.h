@@ -532,6 +532,109 @@ int bsr_spmm(int64_t mb, int64_t kb, int32_t bs, int64_t nnzb,
              float alpha, float beta, float* C, int64_t ldc,
              void* work, size_t work_bytes, void* stream);
 
+/* --------------------------------------------------------- mixture of experts: routing
+ * The routing of T tokens to slots experts each is a sparse T x S matrix, and
+ * its sort by expert is the COO -> CSR step with expert ids as rows: count,
+ * prefix sum, stable placement.  Slot f = t * slots + j is the j-th choice of
+ * token t; n = T * slots.
+ *
+ * moe_sort: ids[n] (device; the expert of every slot) ->
+ *   offsets[num_experts + 1]  first place of every expert; offsets[num_experts]
+ *                             is the number of routed slots
+ *   src[n]  the slot at every place; -1 at the places from offsets[num_experts] on
+ *   pos[n]  the place of every slot; -1 where it is routed nowhere
+ * A slot whose id is outside [0, num_experts) is routed nowhere (a padding
+ * token, a slot over an expert's capacity).  Slots of one expert keep their
+ * order, so the result is unique and bit-exact.  num_experts in
+ * [1, SP_MOE_MAX_EXPERTS]; n may be 0.  work: moe_sort_bufsize() bytes (0 for
+ * small n: then NULL is fine), 4-byte aligned; its contents on entry do not
+ * matter; calls that share it must not overlap.
+ *
+ * moe_dispatch: Xs[pos[f]] = X[f / slots], a copy: X is T x H (rows ldx
+ * apart), Xs S x H (rows lds apart).  A place outside [0, S) is skipped; rows
+ * of Xs that no slot names keep their contents.  Its gradient, dX[t] = the
+ * sum of dXs[pos[t, j]] over j, is moe_combine without weights.
+ *
+ * moe_combine: Y[t] = sum_j weights[t, j] Ys[pos[t, j]], summed in fp32 in
+ * order of j and rounded once; weights (fp32, T x slots) may be NULL: all
+ * ones.  A slot with a place outside [0, S) contributes nothing (its weight
+ * is not read); a token without any gets zeros.  0 * Inf in a routed slot is
+ * NaN, as the formula says.
+ *
+ * moe_combine_backward: from dY (T x H): dYs[pos[t, j]] = weights[t, j] dY[t]
+ * (rounded once; rows that no slot names keep their contents) and
+ * dweights[t, j] = <dY[t], Ys[pos[t, j]]> (fp32, in a fixed order; 0 where the
+ * slot is routed nowhere).  dYs must not overlap dY or Ys.
+ *
+ * dtype: SP_F32, SP_BF16 or SP_F16, for all rows of a call; rows need the
+ * element's alignment only, any row length and any distance >= H.  The
+ * outputs must not overlap the inputs.  If two slots name the same place, the
+ * row written there is one of the two's or a mixture.  None of these calls
+ * allocates or synchronises; all are deterministic and can be captured.
+ * Errors: SP_ERR_NULL, SP_ERR_SIZE (T * slots, H, S or n above INT32_MAX, a row
+ * distance below H), SP_ERR_UNSUPPORTED (dtype, num_experts, alignment),
+ * SP_ERR_WORKSPACE, SP_ERR_HIP.
+ */
+enum { SP_F32 = 0, SP_BF16 = 1, SP_F16 = 2 }; /* element types */
+enum { SP_MOE_MAX_EXPERTS = 1024 };
+
+int moe_sort_bufsize(int64_t n, int32_t num_experts, size_t* bytes);
+int moe_sort(int64_t n, int32_t num_experts, const int32_t* ids, int32_t* offsets, int32_t* src, int32_t* pos,
+             void* work, size_t work_bytes, void* stream);
+int moe_dispatch(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* X, int64_t ldx,
+                 const int32_t* pos, void* Xs, int64_t lds, void* stream);
+int moe_combine(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* Ys, int64_t lds,
+                const int32_t* pos, const float* weights, void* Y, int64_t ldy, void* stream);
+int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* dY, int64_t ldy,
+                         const void* Ys, int64_t lds, const int32_t* pos, const float* weights, void* dYs,
+                         int64_t ldd, float* dweights, void* stream);
+
+/* --------------------------------------------------------- 8-bit integer products
+ * quantize_rows_i8: every row of X (rows x K, dtype as above, rows ldx apart)
+ * to int8 codes with one fp32 scale: a = max |x|, scale = a / 127,
+ * q = rint(127 x / a), ties to even, |q| <= 127; |q scale - x| <= a / 254 up to
+ * rounding.  A row with a < 2^-119 (its scale would be a denormal) becomes
+ * zeros with scale 0; a row that holds an Inf or a NaN becomes zeros with
+ * scale NaN, so that every product with it is NaN.  q rows are ldq bytes
+ * apart; the bytes between K and ldq keep their contents.
+ *
+ * gemm_i8: C[m, n] = a_scale[m] b_scale[n] sum_k A[m, k] B[n, k], with A M x K
+ * and B N x K, K-contiguous rows (the layout of a linear layer's weight), a
+ * scale per row of A (token) and per row of B (output channel).  The sums are
+ * exact int32 (K <= SP_I8_MAX_K); the float of a sum times a_scale times
+ * b_scale is rounded once to c_type.  K == 0 gives the empty sum.
+ *
+ * moe_gemm_i8: one matrix B[e] (N x K, strideb bytes apart) and b_scale[e]
+ * (b_scale is num_experts x N, contiguous) per expert, applied to the rows
+ * sorted by expert: for p in [offsets[e], offsets[e + 1])
+ *   C[p, n] = a_scale[r] b_scale[e, n] sum_k A[r, k] B[e, n, k]
+ * with r = p (src NULL) or r = src[p] / slots (src from moe_sort: A then holds
+ * the tokens' rows, and no dispatched copy of them is needed).  C is S x N.
+ * A row of C behind offsets[num_experts], or whose r is outside [0, a_rows),
+ * keeps its contents.  Offsets are read on the device and not validated: they
+ * are clamped to [0, S], a descending pair is an empty expert, and rows that
+ * two experts claim are unspecified.
+ *
+ * Alignment: none needed for A and B (C and the scales: the element's).  When
+ * A, B, lda, ldb (and strideb) are multiples of 16 bytes the fast kernels
+ * run; they read the rows in 16-byte pieces, so that up to 15 bytes behind a
+ * row's last (K rounded up to 16) are read and ignored, also behind the last
+ * row: within its 16-byte piece, never past it.
+ * None of these calls allocates or synchronises; all are deterministic.
+ * Errors: SP_ERR_NULL, SP_ERR_SIZE, SP_ERR_UNSUPPORTED (types, K, num_experts,
+ * alignment), SP_ERR_HIP.
+ */
+enum { SP_I8_MAX_K = 131071 };
+
+int quantize_rows_i8(int64_t rows, int64_t K, int32_t dtype, const void* X, int64_t ldx, int8_t* q, int64_t ldq,
+                     float* scale, void* stream);
+int gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B,
+            int64_t ldb, const float* b_scale, int32_t c_type, void* C, int64_t ldc, void* stream);
+int moe_gemm_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
+                const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
+                int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t c_type, void* C, int64_t ldc,
+                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

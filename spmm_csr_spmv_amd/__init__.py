@@ -4,8 +4,10 @@ Python binding of libspmm_csr_spmv.so (C ABI in include/spmm_csr_spmv.h):
 CSR SpMV y = alpha A x + beta y, its transpose through a one-time CSC,
 CSR SpMM C = alpha A B + beta C, BSR SpMM on MFMA (bf16 in, fp32
 accumulate), CSR -> BSR with a fill-ratio gate, BSR SpMV, windowed rows
-(WCSR) with a windowed SpMM on MFMA, and a tuning cache.  All
-arithmetic runs in the library's HIP kernels; this package only marshals
+(WCSR) with a windowed SpMM on MFMA, and a tuning cache; for mixtures of
+experts the sort of tokens by expert, their rows moved there and back with
+weights and gradients, and int8 products with a scale per token and channel,
+over one matrix or one per expert.  All arithmetic runs in the library's HIP kernels; this package only marshals
 torch tensors into the C calls.  There is no CPU fallback:
 without the built library every call raises.
 """
@@ -42,4 +44,13 @@ from ._binding import (  # noqa: F401
     tune_cache_size,
     tune_cache_store,
     sp_dispatch_key,
+)
+from ._moe import (  # noqa: F401
+    gemm_i8,
+    moe_combine,
+    moe_combine_backward,
+    moe_dispatch,
+    moe_gemm_i8,
+    moe_sort,
+    quantize_rows_i8,
 )

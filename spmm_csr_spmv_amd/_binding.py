@@ -33,7 +33,8 @@ EXPORTS = ("sp_status_string", "sp_version", "csr_build_from_coo_bufsize", "csr_
            "sp_tune_cache_size", "sp_autotune_workspace_size", "sp_autotune_spmv", "csr_to_wcsr_bufsize",
            "csr_to_wcsr_analyze", "csr_to_wcsr_fill", "wcsr_spmm", "sp_plan_view_create",
            "csr_build_from_coo_noalloc", "bsr_spmv_rowwise", "wcsr_tasks_bufsize", "wcsr_tasks_build",
-           "wcsr_spmm_tasks_bufsize", "wcsr_spmm_tasks")
+           "wcsr_spmm_tasks_bufsize", "wcsr_spmm_tasks", "moe_sort_bufsize", "moe_sort", "moe_dispatch", "moe_combine",
+           "moe_combine_backward", "quantize_rows_i8", "gemm_i8", "moe_gemm_i8")
 
 
 class SparseError(RuntimeError):
@@ -135,6 +136,15 @@ def lib():
         L.sp_autotune_spmv.argtypes = [_i64, _i64, _i64, _p, _p, _p, _opt, _i32, _p, _p, _i32, ctypes.c_uint64, _p,
                                        _sz, ctypes.POINTER(_i32), ctypes.POINTER(_f), _p]
         L.bsr_spmm.argtypes = [_i64, _i64, _i32, _i64, _p, _p, _p, _i32, _p, _i64, _f, _f, _p, _i64, _p, _sz, _p]
+        L.moe_sort_bufsize.argtypes = [_i64, _i32, ctypes.POINTER(_sz)]
+        L.moe_sort.argtypes = [_i64, _i32, _p, _p, _p, _p, _p, _sz, _p]
+        L.moe_dispatch.argtypes = [_i64, _i32, _i64, _i64, _i32, _p, _i64, _p, _p, _i64, _p]
+        L.moe_combine.argtypes = [_i64, _i32, _i64, _i64, _i32, _p, _i64, _p, _p, _p, _i64, _p]
+        L.moe_combine_backward.argtypes = [_i64, _i32, _i64, _i64, _i32, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _p]
+        L.quantize_rows_i8.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _p]
+        L.gemm_i8.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _i32, _p, _i64, _p]
+        L.moe_gemm_i8.argtypes = [_i64, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i32, _p, _i64, _i64, _p, _p, _i32, _p,
+                                  _i64, _p]
         for name in EXPORTS:
             if name not in ("sp_status_string", "sp_version"):
                 getattr(L, name).restype = ctypes.c_int

@@ -1,0 +1,299 @@
+"""ctypes binding of the mixture-of-experts entry points -- argument marshalling only.
+
+Like the rest of the package: the functions have the names of the C calls, check
+types, shapes, devices and strides, allocate what is not given, and raise
+SparseError on a non-zero status.  Row tensors may have any row distance as long
+as their last dimension is contiguous and rows do not overlap.  Everything is
+enqueued on `stream` (default: the current stream of the tensors' device), nothing
+synchronises, and nothing here is recorded for autograd: gradients are calls of
+their own (moe_combine for moe_dispatch's, moe_combine_backward for moe_combine's).
+"""
+import contextlib
+import ctypes
+import functools
+
+import torch
+
+from ._binding import SP_OK, SparseError, _on, _sz, lib
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _check(fn, code):
+    if code != SP_OK:
+        raise SparseError(fn, code, lib())
+
+
+def _type(t, name):
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    return code
+
+
+def _want(t, dtype, dim, name, device=None):
+    """Checks type, number of dimensions and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise TypeError("%s must be a device tensor" % name)
+    if t.dim() != dim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the others on %s" % (name, t.device, device))
+
+
+def _whole(t, dtype, dim, name, device=None):
+    """_want, and contiguous."""
+    _want(t, dtype, dim, name, device)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _rows(t, name):
+    """Row distance of a 2-D tensor with contiguous, disjoint rows."""
+    rows, cols = t.shape
+    ld = t.stride(0)
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and ld < cols:
+        raise ValueError("%s must have a contiguous last dimension and rows that do not overlap" % name)
+    return max(ld, cols, 1)
+
+
+def _apart(out, name, *inputs):
+    """Refuses an output whose bytes overlap an input's (row gaps count as used)."""
+    if out.numel() == 0:
+        return
+    lo = out.data_ptr()
+    hi = lo + (sum((n - 1) * st for n, st in zip(out.shape, out.stride())) + 1) * out.element_size()
+    for t in inputs:
+        if t is None or t.numel() == 0:
+            continue
+        b = t.data_ptr()
+        if b < hi and lo < b + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size():
+            raise ValueError("%s overlaps an input" % name)
+
+
+def _device(t):
+    """The tensor's device as the current one while the library launches."""
+    if t.get_device() == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _raw(stream, t):
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    if stream.device != t.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _sort_bytes(n, num_experts):
+    size = _sz()
+    _check("moe_sort_bufsize", lib().moe_sort_bufsize(n, num_experts, ctypes.byref(size)))
+    return size.value
+
+
+def moe_sort(ids, num_experts, work=None, stream=None):
+    """Stable sort of the slots ids (int32, any shape) by expert: (offsets int32
+    [num_experts + 1], src int32 [n], pos int32 of ids' shape).  src[p] is the slot
+    at place p (-1 from place offsets[-1] on), pos[f] the place of slot f; a slot
+    whose id is outside [0, num_experts) is routed nowhere, its pos is -1.  `work` is
+    a uint8 device tensor of moe_sort_bufsize bytes (allocated when None)."""
+    _whole(ids, torch.int32, ids.dim(), "ids")
+    n, num_experts = ids.numel(), int(num_experts)
+    need = _sort_bytes(n, num_experts)
+    with _device(ids), _on(stream):
+        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
+        src = torch.empty(n, dtype=torch.int32, device=ids.device)
+        pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+        if work is None:
+            work = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+        elif work.device != ids.device or not work.is_contiguous():
+            raise ValueError("work must be a contiguous tensor on %s" % ids.device)
+        nbytes = work.numel() * work.element_size() if work is not None else 0
+        _check("moe_sort", lib().moe_sort(n, num_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(),
+                                          pos.data_ptr(), work.data_ptr() if nbytes else None, nbytes,
+                                          _raw(stream, ids)))
+    return offsets, src, pos
+
+
+def moe_dispatch(X, pos, S=None, out=None, stream=None):
+    """out[pos[t, j]] = X[t]: the rows of X (T x H) at their places, out S x H.  pos is
+    int32 T x slots (moe_sort); S defaults to T * slots.  Rows that no slot names keep
+    their contents (they are undefined where out is allocated here)."""
+    code = _type(X, "X")
+    _want(X, X.dtype, 2, "X")
+    _whole(pos, torch.int32, 2, "pos", X.device)
+    T, H = X.shape
+    if pos.shape[0] != T or pos.shape[1] < 1:
+        raise ValueError("pos must be T x slots, slots at least 1")
+    with _device(X), _on(stream):
+        if out is None:
+            out = torch.empty(pos.numel() if S is None else int(S), H, dtype=X.dtype, device=X.device)
+        else:
+            _want(out, X.dtype, 2, "out", X.device)
+            if out.shape[1] != H or (S is not None and out.shape[0] != S):
+                raise ValueError("out must be S x H")
+            _apart(out, "out", X, pos)
+        _check("moe_dispatch", lib().moe_dispatch(T, pos.shape[1], H, out.shape[0], code, X.data_ptr(),
+                                                  _rows(X, "X"), pos.data_ptr(), out.data_ptr(), _rows(out, "out"),
+                                                  _raw(stream, X)))
+    return out
+
+
+def moe_combine(Ys, pos, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] Ys[pos[t, j]] (T x H); weights float32 T x slots, or
+    None for all ones (then it is also the gradient of moe_dispatch)."""
+    code = _type(Ys, "Ys")
+    _want(Ys, Ys.dtype, 2, "Ys")
+    _whole(pos, torch.int32, 2, "pos", Ys.device)
+    if pos.shape[1] < 1:
+        raise ValueError("pos must be T x slots, slots at least 1")
+    if weights is not None:
+        _whole(weights, torch.float32, 2, "weights", Ys.device)
+        if weights.shape != pos.shape:
+            raise ValueError("weights must have pos's shape")
+    (T, slots), (S, H) = pos.shape, Ys.shape
+    with _device(Ys), _on(stream):
+        if out is None:
+            out = torch.empty(T, H, dtype=Ys.dtype, device=Ys.device)
+        else:
+            _want(out, Ys.dtype, 2, "out", Ys.device)
+            if tuple(out.shape) != (T, H):
+                raise ValueError("out must be T x H")
+            _apart(out, "out", Ys, pos, weights)
+        _check("moe_combine", lib().moe_combine(T, slots, H, S, code, Ys.data_ptr(), _rows(Ys, "Ys"), pos.data_ptr(),
+                                                weights.data_ptr() if weights is not None else None, out.data_ptr(),
+                                                _rows(out, "out"), _raw(stream, Ys)))
+    return out
+
+
+def moe_combine_backward(dY, Ys, pos, weights, dYs=None, dweights=None, stream=None):
+    """Gradient of moe_combine: (dYs, dweights) with dYs[pos[t, j]] = weights[t, j] dY[t] (S x H;
+    rows that no slot names keep their contents, undefined where dYs is allocated here)
+    and dweights[t, j] = <dY[t], Ys[pos[t, j]]>, 0 where the slot is routed nowhere."""
+    code = _type(Ys, "Ys")
+    _want(Ys, Ys.dtype, 2, "Ys")
+    _want(dY, Ys.dtype, 2, "dY", Ys.device)
+    _whole(pos, torch.int32, 2, "pos", Ys.device)
+    _whole(weights, torch.float32, 2, "weights", Ys.device)
+    (T, slots), (S, H) = pos.shape, Ys.shape
+    if slots < 1 or weights.shape != pos.shape or tuple(dY.shape) != (T, H):
+        raise ValueError("dY must be T x H, pos and weights T x slots, slots at least 1")
+    with _device(Ys), _on(stream):
+        if dYs is None:
+            dYs = torch.empty(S, H, dtype=Ys.dtype, device=Ys.device)
+        else:
+            _want(dYs, Ys.dtype, 2, "dYs", Ys.device)
+            if dYs.shape != Ys.shape:
+                raise ValueError("dYs must be S x H")
+            _apart(dYs, "dYs", dY, Ys, pos, weights)
+        if dweights is None:
+            dweights = torch.empty(T, slots, dtype=torch.float32, device=Ys.device)
+        else:
+            _whole(dweights, torch.float32, 2, "dweights", Ys.device)
+            if dweights.shape != pos.shape:
+                raise ValueError("dweights must have pos's shape")
+            _apart(dweights, "dweights", dY, Ys, pos, weights, dYs)
+        _check("moe_combine_backward",
+               lib().moe_combine_backward(T, slots, H, S, code, dY.data_ptr(), _rows(dY, "dY"), Ys.data_ptr(),
+                                          _rows(Ys, "Ys"), pos.data_ptr(), weights.data_ptr(), dYs.data_ptr(),
+                                          _rows(dYs, "dYs"), dweights.data_ptr(), _raw(stream, Ys)))
+    return dYs, dweights
+
+
+def quantize_rows_i8(X, q=None, scale=None, stream=None):
+    """Rows of X (rows x K) as int8 codes and one float32 scale each: (q, scale), X about
+    q * scale[:, None].  A q allocated here has its rows a multiple of 16 bytes apart, as
+    the fast kernels of the products want them."""
+    code = _type(X, "X")
+    _want(X, X.dtype, 2, "X")
+    rows, K = X.shape
+    with _device(X), _on(stream):
+        if q is None:
+            q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.int8, device=X.device)[:, :K]
+        else:
+            _want(q, torch.int8, 2, "q", X.device)
+            if q.shape != X.shape:
+                raise ValueError("q must have X's shape")
+            _apart(q, "q", X)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        else:
+            _whole(scale, torch.float32, 1, "scale", X.device)
+            if scale.shape[0] != rows:
+                raise ValueError("scale must have one entry per row")
+            _apart(scale, "scale", X, q)
+        _check("quantize_rows_i8", lib().quantize_rows_i8(rows, K, code, X.data_ptr(), _rows(X, "X"), q.data_ptr(),
+                                                          _rows(q, "q"), scale.data_ptr(), _raw(stream, X)))
+    return q, scale
+
+
+def _codes(A, a_scale):
+    _want(A, torch.int8, 2, "A")
+    _whole(a_scale, torch.float32, 1, "a_scale", A.device)
+    if a_scale.shape[0] != A.shape[0]:
+        raise ValueError("a_scale must have one entry per row of A")
+
+
+def _product_out(out, dtype, rows, N, A, *inputs):
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % (dtype,))
+        return torch.empty(rows, N, dtype=dtype, device=A.device)
+    _type(out, "out")
+    _want(out, out.dtype, 2, "out", A.device)
+    if tuple(out.shape) != (rows, N):
+        raise ValueError("out must be %d x %d" % (rows, N))
+    _apart(out, "out", A, *inputs)
+    return out
+
+
+def gemm_i8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None):
+    """out[m, n] = a_scale[m] b_scale[n] sum_k A[m, k] B[n, k]: A int8 M x K, B int8 N x K, scales
+    float32; out in `dtype` (float32, bfloat16 or float16) when it is allocated here."""
+    _codes(A, a_scale)
+    _want(B, torch.int8, 2, "B", A.device)
+    _whole(b_scale, torch.float32, 1, "b_scale", A.device)
+    (M, K), N = A.shape, B.shape[0]
+    if B.shape[1] != K or b_scale.shape[0] != N:
+        raise ValueError("B must be N x K and b_scale have one entry per row of B")
+    with _device(A), _on(stream):
+        out = _product_out(out, dtype, M, N, A, B, a_scale, b_scale)
+        _check("gemm_i8", lib().gemm_i8(M, N, K, A.data_ptr(), _rows(A, "A"), a_scale.data_ptr(), B.data_ptr(),
+                                        _rows(B, "B"), b_scale.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
+                                        _rows(out, "out"), _raw(stream, A)))
+    return out
+
+
+def moe_gemm_i8(A, a_scale, B, b_scale, offsets, src=None, slots=1, out=None, dtype=torch.bfloat16, stream=None):
+    """The product with one matrix per expert: B int8 E x N x K, b_scale float32 E x N, offsets
+    int32 [E + 1] (moe_sort).  Row p of out in expert e's range is the product of A's row p, or
+    with src (moe_sort's, and its slots per token) of A's row src[p] // slots.  Rows behind the
+    last expert's keep their contents (undefined where out is allocated here)."""
+    _codes(A, a_scale)
+    _want(B, torch.int8, 3, "B", A.device)
+    _whole(b_scale, torch.float32, 2, "b_scale", A.device)
+    _whole(offsets, torch.int32, 1, "offsets", A.device)
+    (rows, K), (E, N, _) = A.shape, B.shape
+    if B.shape[2] != K or tuple(b_scale.shape) != (E, N) or offsets.shape[0] != E + 1:
+        raise ValueError("B must be E x N x K, b_scale E x N and offsets E + 1")
+    if src is not None:
+        _whole(src, torch.int32, 1, "src", A.device)
+    S = rows if src is None else src.shape[0]
+    if K > 1 and B.stride(2) != 1 or N > 1 and B.stride(1) < K:
+        raise ValueError("B must have a contiguous last dimension and rows that do not overlap")
+    ldb = max(B.stride(1), K, 1)
+    strideb = B.stride(0) if K > 0 else N * ldb
+    with _device(A), _on(stream):
+        out = _product_out(out, dtype, S, N, A, B, a_scale, b_scale, offsets, src)
+        _check("moe_gemm_i8",
+               lib().moe_gemm_i8(S, E, N, K, A.data_ptr(), rows, _rows(A, "A"), a_scale.data_ptr(),
+                                 src.data_ptr() if src is not None else None, int(slots), B.data_ptr(), ldb, strideb,
+                                 b_scale.data_ptr(), offsets.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
+                                 _rows(out, "out"), _raw(stream, A)))
+    return out
