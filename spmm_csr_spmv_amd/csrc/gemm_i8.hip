@@ -36,6 +36,15 @@ struct GemmArgs {
     int64_t m_tiles, n_tiles; // m_tiles is an upper bound when offsets are given
 };
 
+// Tile i of the rows [a, b): as many tiles as BM asks for, of equal height in units of 64 rows.
+template <int BM>
+__device__ __forceinline__ void cut(int64_t a, int64_t b, int64_t i, int64_t& lo, int64_t& hi) {
+    const int64_t tiles = (b - a + BM - 1) / BM;
+    const int64_t height = BM <= 64 ? BM : (b - a + 64 * tiles - 1) / (64 * max(tiles, (int64_t)1)) * 64;
+    lo = a + i * height;
+    hi = min(lo + height, b);
+}
+
 // Row tile number `tile` of the launch: expert e, rows [lo, hi) of its range,
 // at most BM of them.  Every wave of a workgroup finds it by itself: the
 // experts' tile counts, 64 at a time, a prefix sum over the lanes, and the
@@ -45,9 +54,8 @@ template <int BM>
 __device__ __forceinline__ bool find_tile(const GemmArgs& g, int64_t tile, int lane, int& e, int64_t& lo, int64_t& hi) {
     if (!g.offsets) {
         e = 0;
-        lo = tile * BM;
-        hi = min(lo + BM, g.S);
-        return lo < g.S;
+        cut<BM>(0, g.S, tile, lo, hi);
+        return tile * BM < g.S;
     }
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
@@ -68,8 +76,7 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& g, int64_t tile, int l
             const int l = __builtin_ctzll(past);
             e = e0 + l;
             const int first = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
-            lo = (int64_t)__builtin_amdgcn_readlane(a, l) + (tile - first) * BM;
-            hi = min(lo + BM, (int64_t)__builtin_amdgcn_readlane(b, l));
+            cut<BM>(__builtin_amdgcn_readlane(a, l), __builtin_amdgcn_readlane(b, l), tile - first, lo, hi);
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -158,9 +165,230 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Large products: tiles of up to 256 rows x 256 columns, eight waves.
+//
+// K advances in steps of 128 bytes, double-buffered in LDS: while the matrix
+// cores work on one step, global_load_lds brings the next (16 bytes per lane
+// straight into LDS; 8 lanes read a whole 128-byte line of a row).  Chunk c of
+// a row lies at c ^ (row % 8), so that the operand reads of 8 neighbouring
+// rows cover all banks.
+//
+// Wave (wm, wn) owns columns 64 wn .. 64 wn + 63 and every second 32-row
+// block: rows 32 (2 i + wm), i < F.  F = 1 .. 4 is the tile's height in units
+// of 64 rows: a short tile (an expert's last) runs fewer MFMAs and loads fewer
+// rows, instead of multiplying rows nobody stores.  An expert's rows are cut
+// into tiles of equal height rather than full ones and a rest.
+//
+// B is the first MFMA operand, so that a lane's four consecutive sums lie in
+// one row of C; the sums go through LDS once more to be stored as whole lines.
+constexpr int kBig = 256;             // rows and columns of a tile
+constexpr int kBigK = 128;            // bytes of K a step
+constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// One wave's share of a step's copies: F blocks of 64 rows of A, 256 rows of B.
+template <int F>
+__device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const int8_t* const (&pa)[4],
+                                         const int8_t* const (&pb)[4], int64_t k, int w) {
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+        __builtin_amdgcn_global_load_lds((const void*)(pa[j] + k), (lds_void*)(la + (j * 8 + w) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_global_load_lds((const void*)(pb[j] + k), (lds_void*)(lb + (j * 8 + w) * 1024), 16, 0, 0);
+}
+
+// MFMA operands of 32 bytes of K: piece ks of a step.
+template <int F>
+struct BigOps {
+    i32x4 a[F], b[2];
+    __device__ __forceinline__ void read(const int8_t* la, const int8_t* lb, int ks, int wm, int wn, int l) {
+        const int r = l & 31, c = ((2 * ks + (l >> 5)) ^ (r & 7)) << 4;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) b[u] = *reinterpret_cast<const i32x4*>(lb + (64 * wn + 32 * u + r) * kBigK + c);
+#pragma unroll
+        for (int i = 0; i < F; ++i) a[i] = *reinterpret_cast<const i32x4*>(la + (32 * (2 * i + wm) + r) * kBigK + c);
+    }
+    __device__ __forceinline__ void multiply(i32x16 (&acc)[F][2]) const {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) acc[i][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[u], a[i], acc[i][u], 0, 0, 0);
+    }
+};
+
+// Zeroes the bytes from K on in the last step's rows of A (what B holds there is then multiplied by zero).
+template <int F>
+__device__ __forceinline__ void big_mask(int8_t* la, int left, int tid) {
+    for (int i = tid; i < F * 64 * 8; i += 512) {
+        const int row = i >> 3, k = (((i & 7) ^ (row & 7)) << 4);
+        if (k + 16 <= left) continue;
+        i32x4* at = reinterpret_cast<i32x4*>(la + i * 16);
+        i32x4 v = *at;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int keep = left - (k + 4 * d);  // bytes of this word
+            v[d] = keep >= 4 ? v[d] : keep <= 0 ? 0 : v[d] & ((1 << (8 * keep)) - 1);
+        }
+        *at = v;
+    }
+}
+
+template <class D, int F>
+__device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0, int8_t* a0,
+                                         int8_t* b0, int8_t* a1, int8_t* b1, int32_t* lrow, int tid, int w, int l) {
+    typedef typename D::T T;
+    const int wm = w & 1, wn = w >> 1;
+    // the rows this lane copies: 64 j + 8 w + l / 8, chunk (l % 8) ^ (row % 8)
+    const int crow = 8 * w + (l >> 3), chunk = ((l & 7) ^ (crow & 7)) << 4;
+    const int8_t *pa[4], *pb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t p = lo + 64 * j + crow;
+        const int64_t r = j < F && p < hi ? a_row(g, p) : -1;
+        pa[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
+        if (j < F && (l & 7) == 0) lrow[64 * j + crow] = (int32_t)r;
+        pb[j] = g.B + e * g.strideb + min(n0 + 64 * j + crow, g.N - 1) * g.ldb;
+    }
+    const int64_t last = (g.K - 1) & ~(int64_t)15;  // chunks behind it are read from there and masked
+    const int steps = (int)((g.K + kBigK - 1) / kBigK);
+    const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
+
+    i32x16 acc[F][2];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][u][r] = 0;
+
+    // The operands of piece ks + 1 are read while the MFMAs of piece ks run.  The
+    // barrier that ends a step stands before its last piece's MFMAs, when all of
+    // the step's operands are in registers: the copies of step s + 2 and the
+    // first operand reads of step s + 1 are then issued under those MFMAs.
+    BigOps<F> x0, x1;
+    big_copy<F>(a0, b0, pa, pb, min((int64_t)chunk, last), w);
+    __syncthreads();
+    if (steps == 1 && left < kBigK) {
+        big_mask<F>(a0, left, tid);
+        __syncthreads();
+    }
+    if (steps > 1) big_copy<F>(a1, b1, pa, pb, min((int64_t)kBigK + chunk, last), w);
+    x0.read(a0, b0, 0, wm, wn, l);
+#define SPX_STEP(s, la, lb, na, nb)                                                                             \
+    {                                                                                                            \
+        x1.read(la, lb, 1, wm, wn, l);                                                                           \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x0.multiply(acc);                                                                                        \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x0.read(la, lb, 2, wm, wn, l);                                                                           \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x1.multiply(acc);                                                                                        \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x1.read(la, lb, 3, wm, wn, l);                                                                           \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x0.multiply(acc);                                                                                        \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        __syncthreads();                                                                                         \
+        if ((s) + 2 < steps) big_copy<F>(la, lb, pa, pb, min((int64_t)((s) + 2) * kBigK + chunk, last), w);       \
+        if ((s) + 1 < steps) {                                                                                   \
+            if ((s) + 2 == steps && left < kBigK) {                                                              \
+                big_mask<F>(na, left, tid);                                                                      \
+                __syncthreads();                                                                                 \
+            }                                                                                                    \
+            x0.read(na, nb, 0, wm, wn, l);                                                                       \
+        }                                                                                                        \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        x1.multiply(acc);                                                                                        \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+    }
+    for (int s = 0; s < steps; s += 2) {
+        SPX_STEP(s, a0, b0, a1, b1);
+        if (s + 1 < steps) SPX_STEP(s + 1, a1, b1, a0, b0);
+    }
+#undef SPX_STEP
+
+    // Sums of one 32-row block at a time through this wave's part of LDS
+    // (8.5 KB each, three to a buffer), then 8 consecutive columns a
+    // lane, 8 rows an instruction.  D layout of the 32 x 32 MFMA: lane l,
+    // register r -> first operand's row 8 (r/4) + 4 (l/32) + r%4 (a column of
+    // C), second operand's row l%32 (a row of C).
+    int32_t* mine = reinterpret_cast<int32_t*>(w < 3 ? b0 : w < 6 ? b1 : a0) + (w % 3) * (32 * kBigRow);
+    const int64_t n = n0 + 64 * wn + 8 * (l & 7);
+    float sb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sb[i] = g.b_scale[e * g.N + min(n + i, g.N - 1)];
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 v = {acc[i][u][4 * q], acc[i][u][4 * q + 1], acc[i][u][4 * q + 2], acc[i][u][4 * q + 3]};
+                *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
+            }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = 8 * q + (l >> 3), tr = 32 * (2 * i + wm) + row;
+            const i32x4 v0 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7));
+            const i32x4 v1 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7) + 4);
+            const int r = lrow[tr];
+            if (r < 0 || n >= g.N) continue;
+            const float sa = g.a_scale[r];
+            T* c = (T*)g.C + (lo + tr) * g.ldc + n;
+            constexpr int N = Chunk<T>::N;
+            typename Chunk<T>::V o[8 / N];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
+#pragma unroll
+            for (int x = 0; x < 8 / N; ++x)
+                if (n + x * N < g.N) chunk_store(c + x * N, g.N - n - x * N, o[x]);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <class D>
+__global__ __launch_bounds__(512) void gemm_i8_big(GemmArgs g) {
+    __shared__ __attribute__((aligned(1024))) int8_t a0[kBig * kBigK], a1[kBig * kBigK], b0[kBig * kBigK], b1[kBig * kBigK];
+    __shared__ int32_t lrow[kBig];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    // neighbouring tiles on one XCD, four row tiles to a column tile
+    const int v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
+    const int64_t group = 4 * g.n_tiles, first = v / group * 4;
+    const int64_t high = min(g.m_tiles - first, (int64_t)4);
+    const int64_t m = first + v % group % high, nt = v % group / high;
+    int e;
+    int64_t lo, hi;
+    if (!find_tile<kBig>(g, m, l, e, lo, hi)) return;
+    switch ((hi - lo + 63) >> 6) {
+        case 1: big_tile<D, 1>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
+        case 2: big_tile<D, 2>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
+        case 3: big_tile<D, 3>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
+        default: big_tile<D, 4>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
+    }
+}
+
+bool aligned16(const GemmArgs& g) {
+    return ((uintptr_t)g.A | (uintptr_t)g.B | (uintptr_t)g.lda | (uintptr_t)g.ldb | (uintptr_t)(g.E > 1 ? g.strideb : 0)) % 16 == 0;
+}
+
+template <class D>
+int launch_big(GemmArgs g, hipStream_t s) {
+    g.m_tiles = g.offsets ? g.S / kBig + std::min<int64_t>(g.E, g.S) : (g.S + kBig - 1) / kBig;
+    g.n_tiles = (g.N + kBig - 1) / kBig;
+    hipLaunchKernelGGL((gemm_i8_big<D>), dim3((unsigned)(g.m_tiles * g.n_tiles)), dim3(512), 0, s, g);
+    return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
+}
+
 template <class D>
 int gemm_t(GemmArgs g, hipStream_t s) {
     constexpr int64_t BM = 64, BN = 64;
+    const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
+    if (g.K > 0 && g.a_rows > 0 && aligned16(g) && g.S >= 32 * groups) return launch_big<D>(g, s);
     g.m_tiles = g.offsets ? g.S / BM + std::min<int64_t>(g.E, g.S) : (g.S + BM - 1) / BM;
     g.n_tiles = (g.N + BN - 1) / BN;
     const int64_t grid = std::min<int64_t>(g.m_tiles * g.n_tiles, 1 << 22);
