@@ -33,16 +33,17 @@ struct GemmArgs {
     int32_t E;
     void* C;
     int64_t ldc;
-    int64_t m_tiles, n_tiles; // m_tiles is an upper bound when offsets are given
+    uint32_t m_tiles, n_tiles; // m_tiles is an upper bound when offsets are given; the product fits 31 bits
 };
 
 // Tile i of the rows [a, b): as many tiles as BM asks for, of equal height in units of 64 rows.
 template <int BM>
-__device__ __forceinline__ void cut(int64_t a, int64_t b, int64_t i, int64_t& lo, int64_t& hi) {
-    const int64_t tiles = (b - a + BM - 1) / BM;
-    const int64_t height = BM <= 64 ? BM : (b - a + 64 * tiles - 1) / (64 * max(tiles, (int64_t)1)) * 64;
+__device__ __forceinline__ void cut(int a, int b, int i, int64_t& lo, int64_t& hi) {
+    const uint32_t rows = b - a, tiles = (rows + (BM - 1)) / BM;
+    const uint32_t units = (rows + 63) / 64;  // 32-bit divisions: a 64-bit one takes hundreds of instructions
+    const int64_t height = BM <= 64 ? BM : (units + tiles - 1) / max(tiles, 1u) * 64;
     lo = a + i * height;
-    hi = min(lo + height, b);
+    hi = min(lo + height, (int64_t)b);
 }
 
 // Row tile number `tile` of the launch: expert e, rows [lo, hi) of its range,
@@ -51,20 +52,20 @@ __device__ __forceinline__ void cut(int64_t a, int64_t b, int64_t i, int64_t& lo
 // first lane past `tile`.  false: there are fewer tiles than that.  Offsets
 // outside [0, S] are clamped, a descending pair is an empty expert.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const GemmArgs& g, int64_t tile, int lane, int& e, int64_t& lo, int64_t& hi) {
+__device__ __forceinline__ bool find_tile(const GemmArgs& g, int tile, int lane, int& e, int64_t& lo, int64_t& hi) {
     if (!g.offsets) {
         e = 0;
-        cut<BM>(0, g.S, tile, lo, hi);
-        return tile * BM < g.S;
+        cut<BM>(0, (int)g.S, tile, lo, hi);
+        return (int64_t)tile * BM < g.S;
     }
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
         int a = 0, b = 0;
         if (e0 + lane < g.E) {
-            a = (int)min(max((int64_t)g.offsets[e0 + lane], (int64_t)0), g.S);
-            b = max(a, (int)min(max((int64_t)g.offsets[e0 + lane + 1], (int64_t)0), g.S));
+            a = min(max(g.offsets[e0 + lane], 0), (int)g.S);
+            b = max(a, min(max(g.offsets[e0 + lane + 1], 0), (int)g.S));
         }
-        const int mine = (b - a + (BM - 1)) / BM;
+        const int mine = (int)(((uint32_t)(b - a) + (BM - 1)) / BM);
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -123,12 +124,12 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
     const int row = tid >> 2, chunk = tid & 3;  // what this thread stages
     const int wm = 32 * (w >> 1), wn = 32 * (w & 1);
-    const int64_t tiles = g.m_tiles * g.n_tiles;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const uint32_t tiles = g.m_tiles * g.n_tiles;
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int e;
         int64_t lo, hi;
-        if (!find_tile<BM>(g, t / g.n_tiles, l, e, lo, hi)) continue;
-        const int64_t n0 = t % g.n_tiles * BN;
+        if (!find_tile<BM>(g, (int)(t / g.n_tiles), l, e, lo, hi)) continue;
+        const int64_t n0 = (int64_t)(t % g.n_tiles) * BN;
         const int64_t ar = lo + row < hi ? a_row(g, lo + row) : -1;
         const int8_t* pa = g.A + max(ar, (int64_t)0) * g.lda;
         const int8_t* pb = g.B + e * g.strideb + (n0 + row) * g.ldb;
@@ -171,8 +172,10 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
 // K advances in steps of 128 bytes, double-buffered in LDS: while the matrix
 // cores work on one step, global_load_lds brings the next (16 bytes per lane
 // straight into LDS; 8 lanes read a whole 128-byte line of a row).  Chunk c of
-// a row lies at c ^ (row % 8), so that the operand reads of 8 neighbouring
-// rows cover all banks.
+// a row lies at c ^ (row / 2 % 8): a 16-byte operand read serves 16 lanes, 256
+// bytes, at a time, and 16 rows at one c then lie in 16 different places of
+// 256 bytes (with row % 8 rows r and r + 8 met in one place: half of all LDS
+// cycles were conflicts).
 //
 // Wave (wm, wn) owns columns 64 wn .. 64 wn + 63 and every second 32-row
 // block: rows 32 (2 i + wm), i < F.  F = 1 .. 4 is the tile's height in units
@@ -188,16 +191,19 @@ constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// One wave's share of a step's copies: F blocks of 64 rows of A, 256 rows of B.
-template <int F>
+__device__ __forceinline__ int big_swizzle(int row) { return (row >> 1) & 7; }
+
+// One wave's share of a step's copies: F blocks of 64 rows of A, then 4 of B;
+// copies [from, to) of the F + 4.
+template <int F, int FROM, int TO>
 __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const int8_t* const (&pa)[4],
                                          const int8_t* const (&pb)[4], int64_t k, int w) {
 #pragma unroll
-    for (int j = 0; j < F; ++j)
-        __builtin_amdgcn_global_load_lds((const void*)(pa[j] + k), (lds_void*)(la + (j * 8 + w) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        __builtin_amdgcn_global_load_lds((const void*)(pb[j] + k), (lds_void*)(lb + (j * 8 + w) * 1024), 16, 0, 0);
+    for (int j = FROM; j < TO; ++j) {
+        const int8_t* src = (j < F ? pa[j & 3] : pb[(j - F) & 3]) + k;
+        int8_t* dst = (j < F ? la + j * 8192 : lb + (j - F) * 8192) + w * 1024;
+        __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+    }
 }
 
 // MFMA operands of 32 bytes of K: piece ks of a step.
@@ -205,25 +211,59 @@ template <int F>
 struct BigOps {
     i32x4 a[F], b[2];
     __device__ __forceinline__ void read(const int8_t* la, const int8_t* lb, int ks, int wm, int wn, int l) {
-        const int r = l & 31, c = ((2 * ks + (l >> 5)) ^ (r & 7)) << 4;
+        const int r = l & 31, c = ((2 * ks + (l >> 5)) ^ big_swizzle(r)) << 4;
 #pragma unroll
         for (int u = 0; u < 2; ++u) b[u] = *reinterpret_cast<const i32x4*>(lb + (64 * wn + 32 * u + r) * kBigK + c);
 #pragma unroll
         for (int i = 0; i < F; ++i) a[i] = *reinterpret_cast<const i32x4*>(la + (32 * (2 * i + wm) + r) * kBigK + c);
     }
-    __device__ __forceinline__ void multiply(i32x16 (&acc)[F][2]) const {
+    __device__ __forceinline__ void multiply(i32x16 (&acc)[F][2], int i0 = 0, int i1 = F) const {
 #pragma unroll
         for (int i = 0; i < F; ++i)
+            if (i >= i0 && i < i1)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) acc[i][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[u], a[i], acc[i][u], 0, 0, 0);
+                for (int u = 0; u < 2; ++u)
+                    acc[i][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[u], a[i], acc[i][u], 0, 0, 0);
+    }
+    // The same with copies [FROM, FROM + F) .. of a later step between the MFMAs.
+    template <int FROM, int TO>
+    __device__ __forceinline__ void multiply_and_copy(i32x16 (&acc)[F][2], int8_t* la, int8_t* lb,
+                                                      const int8_t* const (&pa)[4], const int8_t* const (&pb)[4],
+                                                      int64_t k, int w) const {
+        constexpr int N = TO - FROM;
+        big_copy<F, FROM, FROM + (N * 1 + F - 1) / F>(la, lb, pa, pb, k, w);
+        multiply(acc, 0, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (F > 1) {
+            big_copy<F, FROM + (N * 1 + F - 1) / F, FROM + (N * 2 + F - 1) / F>(la, lb, pa, pb, k, w);
+            multiply(acc, 1, 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (F > 2) {
+            big_copy<F, FROM + (N * 2 + F - 1) / F, FROM + (N * 3 + F - 1) / F>(la, lb, pa, pb, k, w);
+            multiply(acc, 2, 3);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (F > 3) {
+            big_copy<F, FROM + (N * 3 + F - 1) / F, FROM + (N * 4 + F - 1) / F>(la, lb, pa, pb, k, w);
+            multiply(acc, 3, 4);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 };
+
+// Waits for the operand reads in flight.  Placed before the next reads are
+// issued: left to the compiler, the wait comes after them and takes them in.
+__device__ __forceinline__ void big_operands_here() {
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0, the others untouched
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // Zeroes the bytes from K on in the last step's rows of A (what B holds there is then multiplied by zero).
 template <int F>
 __device__ __forceinline__ void big_mask(int8_t* la, int left, int tid) {
     for (int i = tid; i < F * 64 * 8; i += 512) {
-        const int row = i >> 3, k = (((i & 7) ^ (row & 7)) << 4);
+        const int row = i >> 3, k = ((i & 7) ^ big_swizzle(row)) << 4;
         if (k + 16 <= left) continue;
         i32x4* at = reinterpret_cast<i32x4*>(la + i * 16);
         i32x4 v = *at;
@@ -238,20 +278,25 @@ __device__ __forceinline__ void big_mask(int8_t* la, int left, int tid) {
 
 template <class D, int F>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0, int8_t* a0,
-                                         int8_t* b0, int8_t* a1, int8_t* b1, int32_t* lrow, int tid, int w, int l) {
+                                         int8_t* b0, int8_t* a1, int8_t* b1, int32_t* lrow, float* lscale, int tid, int w,
+                                         int l) {
     typedef typename D::T T;
     const int wm = w & 1, wn = w >> 1;
-    // the rows this lane copies: 64 j + 8 w + l / 8, chunk (l % 8) ^ (row % 8)
-    const int crow = 8 * w + (l >> 3), chunk = ((l & 7) ^ (crow & 7)) << 4;
+    // the rows this lane copies: 64 j + 8 w + l / 8, chunk (l % 8) ^ big_swizzle(row)
+    const int crow = 8 * w + (l >> 3), chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
     const int8_t *pa[4], *pb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t p = lo + 64 * j + crow;
         const int64_t r = j < F && p < hi ? a_row(g, p) : -1;
         pa[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
-        if (j < F && (l & 7) == 0) lrow[64 * j + crow] = (int32_t)r;
+        if (j < F && (l & 7) == 0) {
+            lrow[64 * j + crow] = (int32_t)r;
+            lscale[64 * j + crow] = g.a_scale[max(r, (int64_t)0)];
+        }
         pb[j] = g.B + e * g.strideb + min(n0 + 64 * j + crow, g.N - 1) * g.ldb;
     }
+    if (tid < kBig) lscale[kBig + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
     const int64_t last = (g.K - 1) & ~(int64_t)15;  // chunks behind it are read from there and masked
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
@@ -269,45 +314,51 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     // the step's operands are in registers: the copies of step s + 2 and the
     // first operand reads of step s + 1 are then issued under those MFMAs.
     BigOps<F> x0, x1;
-    big_copy<F>(a0, b0, pa, pb, min((int64_t)chunk, last), w);
+    constexpr int kCopies = F + 4, kHalf = kCopies / 2;
+    big_copy<F, 0, kCopies>(a0, b0, pa, pb, min((int64_t)chunk, last), w);
     __syncthreads();
     if (steps == 1 && left < kBigK) {
         big_mask<F>(a0, left, tid);
         __syncthreads();
     }
-    if (steps > 1) big_copy<F>(a1, b1, pa, pb, min((int64_t)kBigK + chunk, last), w);
+    big_copy<F, 0, kHalf>(a1, b1, pa, pb, min((int64_t)kBigK + chunk, last), w);
     x0.read(a0, b0, 0, wm, wn, l);
 #define SPX_STEP(s, la, lb, na, nb)                                                                             \
     {                                                                                                            \
+        big_operands_here();                                                                                     \
         x1.read(la, lb, 1, wm, wn, l);                                                                           \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x0.multiply(acc);                                                                                        \
+        x0.template multiply_and_copy<kHalf, kCopies>(acc, na, nb, pa, pb,                                       \
+                                             min((int64_t)((s) + 1) * kBigK + chunk, last), w);                  \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
+        big_operands_here();                                                                                     \
         x0.read(la, lb, 2, wm, wn, l);                                                                           \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
         x1.multiply(acc);                                                                                        \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
+        big_operands_here();                                                                                     \
         x1.read(la, lb, 3, wm, wn, l);                                                                           \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
         x0.multiply(acc);                                                                                        \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
         __syncthreads();                                                                                         \
-        if ((s) + 2 < steps) big_copy<F>(la, lb, pa, pb, min((int64_t)((s) + 2) * kBigK + chunk, last), w);       \
-        if ((s) + 1 < steps) {                                                                                   \
-            if ((s) + 2 == steps && left < kBigK) {                                                              \
-                big_mask<F>(na, left, tid);                                                                      \
-                __syncthreads();                                                                                 \
-            }                                                                                                    \
-            x0.read(na, nb, 0, wm, wn, l);                                                                       \
+        if ((s) + 2 == steps && left < kBigK) {                                                                  \
+            big_mask<F>(na, left, tid);                                                                          \
+            __syncthreads();                                                                                     \
         }                                                                                                        \
+        x0.read(na, nb, 0, wm, wn, l);                                                                           \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x1.multiply(acc);                                                                                        \
+        x1.template multiply_and_copy<0, kHalf>(acc, la, lb, pa, pb,                                             \
+                                       min((int64_t)((s) + 2) * kBigK + chunk, last), w);                        \
         __builtin_amdgcn_sched_barrier(0);                                                                       \
     }
-    for (int s = 0; s < steps; s += 2) {
+    int s = 0;
+    for (; s + 2 <= steps; s += 2) {
         SPX_STEP(s, a0, b0, a1, b1);
-        if (s + 1 < steps) SPX_STEP(s + 1, a1, b1, a0, b0);
+        SPX_STEP(s + 1, a1, b1, a0, b0);
     }
+    if (s < steps) SPX_STEP(s, a0, b0, a1, b1);
+    __syncthreads();  // the copies behind the last step have landed too
 #undef SPX_STEP
 
     // Sums of one 32-row block at a time through this wave's part of LDS
@@ -319,7 +370,7 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     const int64_t n = n0 + 64 * wn + 8 * (l & 7);
     float sb[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sb[i] = g.b_scale[e * g.N + min(n + i, g.N - 1)];
+    for (int i = 0; i < 8; ++i) sb[i] = lscale[kBig + 64 * wn + 8 * (l & 7) + i];
 #pragma unroll
     for (int i = 0; i < F; ++i) {
 #pragma unroll
@@ -330,14 +381,14 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
                 *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
             }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {  // rolled: straight-line code here is fetched once and costs more than it saves
             const int row = 8 * q + (l >> 3), tr = 32 * (2 * i + wm) + row;
             const i32x4 v0 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7));
             const i32x4 v1 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7) + 4);
             const int r = lrow[tr];
             if (r < 0 || n >= g.N) continue;
-            const float sa = g.a_scale[r];
+            const float sa = lscale[tr];
             T* c = (T*)g.C + (lo + tr) * g.ldc + n;
             constexpr int N = Chunk<T>::N;
             typename Chunk<T>::V o[8 / N];
@@ -354,21 +405,22 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
 template <class D>
 __global__ __launch_bounds__(512) void gemm_i8_big(GemmArgs g) {
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBig * kBigK], a1[kBig * kBigK], b0[kBig * kBigK], b1[kBig * kBigK];
-    __shared__ int32_t lrow[kBig];
+    __shared__ int32_t lrow[kBig];       // row of A of every row of the tile, or -1
+    __shared__ float lscale[2 * kBig];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     // neighbouring tiles on one XCD, four row tiles to a column tile
     const int v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
-    const int64_t group = 4 * g.n_tiles, first = v / group * 4;
-    const int64_t high = min(g.m_tiles - first, (int64_t)4);
-    const int64_t m = first + v % group % high, nt = v % group / high;
+    const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
+    const uint32_t high = min(g.m_tiles - first, 4u);
+    const int64_t nt = in / high;
     int e;
     int64_t lo, hi;
-    if (!find_tile<kBig>(g, m, l, e, lo, hi)) return;
+    if (!find_tile<kBig>(g, (int)(first + in % high), l, e, lo, hi)) return;
     switch ((hi - lo + 63) >> 6) {
-        case 1: big_tile<D, 1>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
-        case 2: big_tile<D, 2>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
-        case 3: big_tile<D, 3>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
-        default: big_tile<D, 4>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, tid, w, l); break;
+        case 1: big_tile<D, 1>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
+        case 2: big_tile<D, 2>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
+        case 3: big_tile<D, 3>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
+        default: big_tile<D, 4>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
     }
 }
 
@@ -376,10 +428,17 @@ bool aligned16(const GemmArgs& g) {
     return ((uintptr_t)g.A | (uintptr_t)g.B | (uintptr_t)g.lda | (uintptr_t)g.ldb | (uintptr_t)(g.E > 1 ? g.strideb : 0)) % 16 == 0;
 }
 
+// Tile counts of the launch; false if there are 2^31 or more.
+bool set_tiles(GemmArgs& g, int64_t bm, int64_t bn) {
+    const int64_t m = g.offsets ? g.S / bm + std::min<int64_t>(g.E, g.S) : (g.S + bm - 1) / bm, n = (g.N + bn - 1) / bn;
+    g.m_tiles = (uint32_t)m;
+    g.n_tiles = (uint32_t)n;
+    return m * n < (int64_t)1 << 31;
+}
+
 template <class D>
 int launch_big(GemmArgs g, hipStream_t s) {
-    g.m_tiles = g.offsets ? g.S / kBig + std::min<int64_t>(g.E, g.S) : (g.S + kBig - 1) / kBig;
-    g.n_tiles = (g.N + kBig - 1) / kBig;
+    set_tiles(g, kBig, kBig);
     hipLaunchKernelGGL((gemm_i8_big<D>), dim3((unsigned)(g.m_tiles * g.n_tiles)), dim3(512), 0, s, g);
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
@@ -388,10 +447,11 @@ template <class D>
 int gemm_t(GemmArgs g, hipStream_t s) {
     constexpr int64_t BM = 64, BN = 64;
     const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
-    if (g.K > 0 && g.a_rows > 0 && aligned16(g) && g.S >= 32 * groups) return launch_big<D>(g, s);
-    g.m_tiles = g.offsets ? g.S / BM + std::min<int64_t>(g.E, g.S) : (g.S + BM - 1) / BM;
-    g.n_tiles = (g.N + BN - 1) / BN;
-    const int64_t grid = std::min<int64_t>(g.m_tiles * g.n_tiles, 1 << 22);
+    if (g.K > 0 && g.a_rows > 0 && aligned16(g) && g.S >= 32 * groups && set_tiles(g, kBig, kBig) &&
+        g.m_tiles * g.n_tiles < 1 << 22)
+        return launch_big<D>(g, s);
+    if (!set_tiles(g, BM, BN)) return SP_ERR_SIZE;
+    const uint32_t grid = std::min<uint32_t>(g.m_tiles * g.n_tiles, 1 << 22);
     hipLaunchKernelGGL((gemm_i8_plain<D>), dim3((unsigned)grid), dim3(256), 0, s, g);
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }

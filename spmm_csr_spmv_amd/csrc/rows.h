@@ -51,7 +51,7 @@ __device__ __forceinline__ void chunk_store(T* p, int64_t len, typename Chunk<T>
         *reinterpret_cast<typename Chunk<T>::U*>(p) = v;
     } else {
 #pragma unroll
-        for (int i = 0; i < Chunk<T>::N; ++i)
+        for (int i = 0; i < Chunk<T>::N - 1; ++i)
             if (i < len) p[i] = v[i];
     }
 }
