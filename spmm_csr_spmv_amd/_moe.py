@@ -8,7 +8,6 @@ enqueued on `stream` (default: the current stream of the tensors' device), nothi
 synchronises, and nothing here is recorded for autograd: gradients are calls of
 their own (moe_combine for moe_dispatch's, moe_combine_backward for moe_combine's).
 """
-import contextlib
 import ctypes
 import functools
 
@@ -32,7 +31,7 @@ def _type(t, name):
 
 
 def _want(t, dtype, dim, name, device=None):
-    """Checks type, number of dimensions and device."""
+    """Checks type, number of dimensions and device (a number; None: any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     if t.dtype is not dtype:
@@ -41,8 +40,8 @@ def _want(t, dtype, dim, name, device=None):
         raise TypeError("%s must be a device tensor" % name)
     if t.dim() != dim:
         raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the others on %s" % (name, t.device, device))
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s is on device %d, the others on %d" % (name, t.get_device(), device))
 
 
 def _whole(t, dtype, dim, name, device=None):
@@ -55,39 +54,40 @@ def _whole(t, dtype, dim, name, device=None):
 def _rows(t, name):
     """Row distance of a 2-D tensor with contiguous, disjoint rows."""
     rows, cols = t.shape
-    ld = t.stride(0)
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and ld < cols:
+    ld, step = t.stride()
+    if cols > 1 and step != 1 or rows > 1 and ld < cols:
         raise ValueError("%s must have a contiguous last dimension and rows that do not overlap" % name)
     return max(ld, cols, 1)
 
 
+def _span(t):
+    """First byte and the one behind the last (row gaps count as used)."""
+    n = t.numel()
+    if n and not t.is_contiguous():
+        n = sum((s - 1) * d for s, d in zip(t.shape, t.stride())) + 1
+    p = t.data_ptr()
+    return p, p + n * t.element_size()
+
+
 def _apart(out, name, *inputs):
-    """Refuses an output whose bytes overlap an input's (row gaps count as used)."""
-    if out.numel() == 0:
-        return
-    lo = out.data_ptr()
-    hi = lo + (sum((n - 1) * st for n, st in zip(out.shape, out.stride())) + 1) * out.element_size()
+    """Refuses an output whose bytes overlap an input's."""
+    lo, hi = _span(out)
     for t in inputs:
-        if t is None or t.numel() == 0:
-            continue
-        b = t.data_ptr()
-        if b < hi and lo < b + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size():
-            raise ValueError("%s overlaps an input" % name)
+        if t is not None:
+            b, e = _span(t)
+            if b < hi and lo < e:
+                raise ValueError("%s overlaps an input" % name)
 
 
-def _device(t):
-    """The tensor's device as the current one while the library launches."""
-    if t.get_device() == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
-
-
-def _raw(stream, t):
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    if stream.device != t.device:
+def _call(body, t, stream, *args):
+    """body(raw stream, *args) with t's device current and allocations on the stream."""
+    device = t.get_device()
+    if stream is None and device == torch._C._cuda_getDevice():
+        return body(torch._C._cuda_getCurrentRawStream(device), *args)
+    if stream is not None and stream.device.index != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
-    return stream.cuda_stream
+    with torch.cuda.device(device), _on(stream):
+        return body(torch._C._cuda_getCurrentRawStream(device), *args)
 
 
 @functools.lru_cache(maxsize=256)
@@ -106,18 +106,20 @@ def moe_sort(ids, num_experts, work=None, stream=None):
     _whole(ids, torch.int32, ids.dim(), "ids")
     n, num_experts = ids.numel(), int(num_experts)
     need = _sort_bytes(n, num_experts)
-    with _device(ids), _on(stream):
-        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
-        src = torch.empty(n, dtype=torch.int32, device=ids.device)
-        pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
-        if work is None:
-            work = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-        elif work.device != ids.device or not work.is_contiguous():
-            raise ValueError("work must be a contiguous tensor on %s" % ids.device)
-        nbytes = work.numel() * work.element_size() if work is not None else 0
-        _check("moe_sort", lib().moe_sort(n, num_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(),
-                                          pos.data_ptr(), work.data_ptr() if nbytes else None, nbytes,
-                                          _raw(stream, ids)))
+    return _call(_sort, ids, stream, ids, n, num_experts, need, work)
+
+
+def _sort(raw, ids, n, num_experts, need, work):
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
+    src = torch.empty(n, dtype=torch.int32, device=ids.device)
+    pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    elif work.device != ids.device or not work.is_contiguous():
+        raise ValueError("work must be a contiguous tensor on %s" % ids.device)
+    nbytes = work.numel() * work.element_size() if work is not None else 0
+    _check("moe_sort", lib().moe_sort(n, num_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(),
+                                      pos.data_ptr(), work.data_ptr() if nbytes else None, nbytes, raw))
     return offsets, src, pos
 
 
@@ -127,21 +129,24 @@ def moe_dispatch(X, pos, S=None, out=None, stream=None):
     their contents (they are undefined where out is allocated here)."""
     code = _type(X, "X")
     _want(X, X.dtype, 2, "X")
-    _whole(pos, torch.int32, 2, "pos", X.device)
+    _whole(pos, torch.int32, 2, "pos", X.get_device())
     T, H = X.shape
     if pos.shape[0] != T or pos.shape[1] < 1:
         raise ValueError("pos must be T x slots, slots at least 1")
-    with _device(X), _on(stream):
-        if out is None:
-            out = torch.empty(pos.numel() if S is None else int(S), H, dtype=X.dtype, device=X.device)
-        else:
-            _want(out, X.dtype, 2, "out", X.device)
-            if out.shape[1] != H or (S is not None and out.shape[0] != S):
-                raise ValueError("out must be S x H")
-            _apart(out, "out", X, pos)
-        _check("moe_dispatch", lib().moe_dispatch(T, pos.shape[1], H, out.shape[0], code, X.data_ptr(),
-                                                  _rows(X, "X"), pos.data_ptr(), out.data_ptr(), _rows(out, "out"),
-                                                  _raw(stream, X)))
+    return _call(_dispatch, X, stream, code, X, pos, S, out)
+
+
+def _dispatch(raw, code, X, pos, S, out):
+    T, H = X.shape
+    if out is None:
+        out = torch.empty(pos.numel() if S is None else int(S), H, dtype=X.dtype, device=X.device)
+    else:
+        _want(out, X.dtype, 2, "out", X.get_device())
+        if out.shape[1] != H or (S is not None and out.shape[0] != S):
+            raise ValueError("out must be S x H")
+        _apart(out, "out", X, pos)
+    _check("moe_dispatch", lib().moe_dispatch(T, pos.shape[1], H, out.shape[0], code, X.data_ptr(),
+                                              _rows(X, "X"), pos.data_ptr(), out.data_ptr(), _rows(out, "out"), raw))
     return out
 
 
@@ -150,25 +155,28 @@ def moe_combine(Ys, pos, weights=None, out=None, stream=None):
     None for all ones (then it is also the gradient of moe_dispatch)."""
     code = _type(Ys, "Ys")
     _want(Ys, Ys.dtype, 2, "Ys")
-    _whole(pos, torch.int32, 2, "pos", Ys.device)
+    _whole(pos, torch.int32, 2, "pos", Ys.get_device())
     if pos.shape[1] < 1:
         raise ValueError("pos must be T x slots, slots at least 1")
     if weights is not None:
-        _whole(weights, torch.float32, 2, "weights", Ys.device)
+        _whole(weights, torch.float32, 2, "weights", Ys.get_device())
         if weights.shape != pos.shape:
             raise ValueError("weights must have pos's shape")
+    return _call(_combine, Ys, stream, code, Ys, pos, weights, out)
+
+
+def _combine(raw, code, Ys, pos, weights, out):
     (T, slots), (S, H) = pos.shape, Ys.shape
-    with _device(Ys), _on(stream):
-        if out is None:
-            out = torch.empty(T, H, dtype=Ys.dtype, device=Ys.device)
-        else:
-            _want(out, Ys.dtype, 2, "out", Ys.device)
-            if tuple(out.shape) != (T, H):
-                raise ValueError("out must be T x H")
-            _apart(out, "out", Ys, pos, weights)
-        _check("moe_combine", lib().moe_combine(T, slots, H, S, code, Ys.data_ptr(), _rows(Ys, "Ys"), pos.data_ptr(),
-                                                weights.data_ptr() if weights is not None else None, out.data_ptr(),
-                                                _rows(out, "out"), _raw(stream, Ys)))
+    if out is None:
+        out = torch.empty(T, H, dtype=Ys.dtype, device=Ys.device)
+    else:
+        _want(out, Ys.dtype, 2, "out", Ys.get_device())
+        if tuple(out.shape) != (T, H):
+            raise ValueError("out must be T x H")
+        _apart(out, "out", Ys, pos, weights)
+    _check("moe_combine", lib().moe_combine(T, slots, H, S, code, Ys.data_ptr(), _rows(Ys, "Ys"), pos.data_ptr(),
+                                            weights.data_ptr() if weights is not None else None, out.data_ptr(),
+                                            _rows(out, "out"), raw))
     return out
 
 
@@ -178,31 +186,35 @@ def moe_combine_backward(dY, Ys, pos, weights, dYs=None, dweights=None, stream=N
     and dweights[t, j] = <dY[t], Ys[pos[t, j]]>, 0 where the slot is routed nowhere."""
     code = _type(Ys, "Ys")
     _want(Ys, Ys.dtype, 2, "Ys")
-    _want(dY, Ys.dtype, 2, "dY", Ys.device)
-    _whole(pos, torch.int32, 2, "pos", Ys.device)
-    _whole(weights, torch.float32, 2, "weights", Ys.device)
+    _want(dY, Ys.dtype, 2, "dY", Ys.get_device())
+    _whole(pos, torch.int32, 2, "pos", Ys.get_device())
+    _whole(weights, torch.float32, 2, "weights", Ys.get_device())
     (T, slots), (S, H) = pos.shape, Ys.shape
     if slots < 1 or weights.shape != pos.shape or tuple(dY.shape) != (T, H):
         raise ValueError("dY must be T x H, pos and weights T x slots, slots at least 1")
-    with _device(Ys), _on(stream):
-        if dYs is None:
-            dYs = torch.empty(S, H, dtype=Ys.dtype, device=Ys.device)
-        else:
-            _want(dYs, Ys.dtype, 2, "dYs", Ys.device)
-            if dYs.shape != Ys.shape:
-                raise ValueError("dYs must be S x H")
-            _apart(dYs, "dYs", dY, Ys, pos, weights)
-        if dweights is None:
-            dweights = torch.empty(T, slots, dtype=torch.float32, device=Ys.device)
-        else:
-            _whole(dweights, torch.float32, 2, "dweights", Ys.device)
-            if dweights.shape != pos.shape:
-                raise ValueError("dweights must have pos's shape")
-            _apart(dweights, "dweights", dY, Ys, pos, weights, dYs)
-        _check("moe_combine_backward",
-               lib().moe_combine_backward(T, slots, H, S, code, dY.data_ptr(), _rows(dY, "dY"), Ys.data_ptr(),
-                                          _rows(Ys, "Ys"), pos.data_ptr(), weights.data_ptr(), dYs.data_ptr(),
-                                          _rows(dYs, "dYs"), dweights.data_ptr(), _raw(stream, Ys)))
+    return _call(_combine_backward, Ys, stream, code, dY, Ys, pos, weights, dYs, dweights)
+
+
+def _combine_backward(raw, code, dY, Ys, pos, weights, dYs, dweights):
+    (T, slots), (S, H) = pos.shape, Ys.shape
+    if dYs is None:
+        dYs = torch.empty(S, H, dtype=Ys.dtype, device=Ys.device)
+    else:
+        _want(dYs, Ys.dtype, 2, "dYs", Ys.get_device())
+        if dYs.shape != Ys.shape:
+            raise ValueError("dYs must be S x H")
+        _apart(dYs, "dYs", dY, Ys, pos, weights)
+    if dweights is None:
+        dweights = torch.empty(T, slots, dtype=torch.float32, device=Ys.device)
+    else:
+        _whole(dweights, torch.float32, 2, "dweights", Ys.get_device())
+        if dweights.shape != pos.shape:
+            raise ValueError("dweights must have pos's shape")
+        _apart(dweights, "dweights", dY, Ys, pos, weights, dYs)
+    _check("moe_combine_backward",
+           lib().moe_combine_backward(T, slots, H, S, code, dY.data_ptr(), _rows(dY, "dY"), Ys.data_ptr(),
+                                      _rows(Ys, "Ys"), pos.data_ptr(), weights.data_ptr(), dYs.data_ptr(),
+                                      _rows(dYs, "dYs"), dweights.data_ptr(), raw))
     return dYs, dweights
 
 
@@ -212,30 +224,35 @@ def quantize_rows_i8(X, q=None, scale=None, stream=None):
     the fast kernels of the products want them."""
     code = _type(X, "X")
     _want(X, X.dtype, 2, "X")
+    return _call(_quantize, X, stream, code, X, q, scale)
+
+
+def _quantize(raw, code, X, q, scale):
     rows, K = X.shape
-    with _device(X), _on(stream):
-        if q is None:
-            q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.int8, device=X.device)[:, :K]
-        else:
-            _want(q, torch.int8, 2, "q", X.device)
-            if q.shape != X.shape:
-                raise ValueError("q must have X's shape")
-            _apart(q, "q", X)
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-        else:
-            _whole(scale, torch.float32, 1, "scale", X.device)
-            if scale.shape[0] != rows:
-                raise ValueError("scale must have one entry per row")
-            _apart(scale, "scale", X, q)
-        _check("quantize_rows_i8", lib().quantize_rows_i8(rows, K, code, X.data_ptr(), _rows(X, "X"), q.data_ptr(),
-                                                          _rows(q, "q"), scale.data_ptr(), _raw(stream, X)))
+    if q is None:
+        q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.int8, device=X.device)
+        if q.shape[1] != K:
+            q = q[:, :K]
+    else:
+        _want(q, torch.int8, 2, "q", X.get_device())
+        if q.shape != X.shape:
+            raise ValueError("q must have X's shape")
+        _apart(q, "q", X)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+    else:
+        _whole(scale, torch.float32, 1, "scale", X.get_device())
+        if scale.shape[0] != rows:
+            raise ValueError("scale must have one entry per row")
+        _apart(scale, "scale", X, q)
+    _check("quantize_rows_i8", lib().quantize_rows_i8(rows, K, code, X.data_ptr(), _rows(X, "X"), q.data_ptr(),
+                                                      _rows(q, "q"), scale.data_ptr(), raw))
     return q, scale
 
 
 def _codes(A, a_scale):
     _want(A, torch.int8, 2, "A")
-    _whole(a_scale, torch.float32, 1, "a_scale", A.device)
+    _whole(a_scale, torch.float32, 1, "a_scale", A.get_device())
     if a_scale.shape[0] != A.shape[0]:
         raise ValueError("a_scale must have one entry per row of A")
 
@@ -246,7 +263,7 @@ def _product_out(out, dtype, rows, N, A, *inputs):
             raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % (dtype,))
         return torch.empty(rows, N, dtype=dtype, device=A.device)
     _type(out, "out")
-    _want(out, out.dtype, 2, "out", A.device)
+    _want(out, out.dtype, 2, "out", A.get_device())
     if tuple(out.shape) != (rows, N):
         raise ValueError("out must be %d x %d" % (rows, N))
     _apart(out, "out", A, *inputs)
@@ -257,16 +274,20 @@ def gemm_i8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None)
     """out[m, n] = a_scale[m] b_scale[n] sum_k A[m, k] B[n, k]: A int8 M x K, B int8 N x K, scales
     float32; out in `dtype` (float32, bfloat16 or float16) when it is allocated here."""
     _codes(A, a_scale)
-    _want(B, torch.int8, 2, "B", A.device)
-    _whole(b_scale, torch.float32, 1, "b_scale", A.device)
+    _want(B, torch.int8, 2, "B", A.get_device())
+    _whole(b_scale, torch.float32, 1, "b_scale", A.get_device())
     (M, K), N = A.shape, B.shape[0]
     if B.shape[1] != K or b_scale.shape[0] != N:
         raise ValueError("B must be N x K and b_scale have one entry per row of B")
-    with _device(A), _on(stream):
-        out = _product_out(out, dtype, M, N, A, B, a_scale, b_scale)
-        _check("gemm_i8", lib().gemm_i8(M, N, K, A.data_ptr(), _rows(A, "A"), a_scale.data_ptr(), B.data_ptr(),
-                                        _rows(B, "B"), b_scale.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
-                                        _rows(out, "out"), _raw(stream, A)))
+    return _call(_gemm, A, stream, A, a_scale, B, b_scale, out, dtype)
+
+
+def _gemm(raw, A, a_scale, B, b_scale, out, dtype):
+    (M, K), N = A.shape, B.shape[0]
+    out = _product_out(out, dtype, M, N, A, B, a_scale, b_scale)
+    _check("gemm_i8", lib().gemm_i8(M, N, K, A.data_ptr(), _rows(A, "A"), a_scale.data_ptr(), B.data_ptr(),
+                                    _rows(B, "B"), b_scale.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
+                                    _rows(out, "out"), raw))
     return out
 
 
@@ -276,24 +297,29 @@ def moe_gemm_i8(A, a_scale, B, b_scale, offsets, src=None, slots=1, out=None, dt
     with src (moe_sort's, and its slots per token) of A's row src[p] // slots.  Rows behind the
     last expert's keep their contents (undefined where out is allocated here)."""
     _codes(A, a_scale)
-    _want(B, torch.int8, 3, "B", A.device)
-    _whole(b_scale, torch.float32, 2, "b_scale", A.device)
-    _whole(offsets, torch.int32, 1, "offsets", A.device)
+    _want(B, torch.int8, 3, "B", A.get_device())
+    _whole(b_scale, torch.float32, 2, "b_scale", A.get_device())
+    _whole(offsets, torch.int32, 1, "offsets", A.get_device())
     (rows, K), (E, N, _) = A.shape, B.shape
     if B.shape[2] != K or tuple(b_scale.shape) != (E, N) or offsets.shape[0] != E + 1:
         raise ValueError("B must be E x N x K, b_scale E x N and offsets E + 1")
     if src is not None:
-        _whole(src, torch.int32, 1, "src", A.device)
+        _whole(src, torch.int32, 1, "src", A.get_device())
     S = rows if src is None else src.shape[0]
     if K > 1 and B.stride(2) != 1 or N > 1 and B.stride(1) < K:
         raise ValueError("B must have a contiguous last dimension and rows that do not overlap")
     ldb = max(B.stride(1), K, 1)
     strideb = B.stride(0) if K > 0 else N * ldb
-    with _device(A), _on(stream):
-        out = _product_out(out, dtype, S, N, A, B, a_scale, b_scale, offsets, src)
-        _check("moe_gemm_i8",
-               lib().moe_gemm_i8(S, E, N, K, A.data_ptr(), rows, _rows(A, "A"), a_scale.data_ptr(),
-                                 src.data_ptr() if src is not None else None, int(slots), B.data_ptr(), ldb, strideb,
-                                 b_scale.data_ptr(), offsets.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
-                                 _rows(out, "out"), _raw(stream, A)))
+    return _call(_moe_gemm, A, stream, A, a_scale, B, b_scale, offsets, src, slots, out, dtype, ldb, strideb)
+
+
+def _moe_gemm(raw, A, a_scale, B, b_scale, offsets, src, slots, out, dtype, ldb, strideb):
+    (rows, K), (E, N, _) = A.shape, B.shape
+    S = rows if src is None else src.shape[0]
+    out = _product_out(out, dtype, S, N, A, B, a_scale, b_scale, offsets, src)
+    _check("moe_gemm_i8",
+           lib().moe_gemm_i8(S, E, N, K, A.data_ptr(), rows, _rows(A, "A"), a_scale.data_ptr(),
+                             src.data_ptr() if src is not None else None, int(slots), B.data_ptr(), ldb, strideb,
+                             b_scale.data_ptr(), offsets.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
+                             _rows(out, "out"), raw))
     return out

@@ -167,7 +167,8 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
 }
 
 // ---------------------------------------------------------------------------
-// Large products: tiles of up to 256 rows x 256 columns, eight waves.
+// Many rows: tiles of up to 64 WN rows x 64 WN columns by 2 WN waves, WN = 4
+// (256 x 256, one workgroup a CU) or 2 (128 x 128, two).
 //
 // K advances in steps of 128 bytes, double-buffered in LDS: while the matrix
 // cores work on one step, global_load_lds brings the next (16 bytes per lane
@@ -178,14 +179,13 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
 // cycles were conflicts).
 //
 // Wave (wm, wn) owns columns 64 wn .. 64 wn + 63 and every second 32-row
-// block: rows 32 (2 i + wm), i < F.  F = 1 .. 4 is the tile's height in units
+// block: rows 32 (2 i + wm), i < F.  F = 1 .. WN is the tile's height in units
 // of 64 rows: a short tile (an expert's last) runs fewer MFMAs and loads fewer
 // rows, instead of multiplying rows nobody stores.  An expert's rows are cut
 // into tiles of equal height rather than full ones and a rest.
 //
 // B is the first MFMA operand, so that a lane's four consecutive sums lie in
 // one row of C; the sums go through LDS once more to be stored as whole lines.
-constexpr int kBig = 256;             // rows and columns of a tile
 constexpr int kBigK = 128;            // bytes of K a step
 constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
 
@@ -193,15 +193,24 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 __device__ __forceinline__ int big_swizzle(int row) { return (row >> 1) & 7; }
 
-// One wave's share of a step's copies: F blocks of 64 rows of A, then 4 of B;
-// copies [from, to) of the F + 4.
-template <int F, int FROM, int TO>
+// Copy instructions a wave issues for a step: 16 WN rows each over the workgroup.
+template <int WN, int F>
+struct BigShape {
+    static constexpr int kRows = 16 * WN;            // rows that one instruction of every wave covers
+    static constexpr int kA = 64 * F / kRows;        // for the rows of A
+    static constexpr int kB = 64 * WN / kRows;       // for the rows of B
+    static constexpr int kCopies = kA + kB;
+};
+
+// Copies [FROM, TO) of the step's, in the order A, B.
+template <int WN, int F, int FROM, int TO>
 __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const int8_t* const (&pa)[4],
                                          const int8_t* const (&pb)[4], int64_t k, int w) {
+    using S = BigShape<WN, F>;
 #pragma unroll
     for (int j = FROM; j < TO; ++j) {
-        const int8_t* src = (j < F ? pa[j & 3] : pb[(j - F) & 3]) + k;
-        int8_t* dst = (j < F ? la + j * 8192 : lb + (j - F) * 8192) + w * 1024;
+        const int8_t* src = (j < S::kA ? pa[j & 3] : pb[(j - S::kA) & 3]) + k;
+        int8_t* dst = (j < S::kA ? la + j * S::kRows * kBigK : lb + (j - S::kA) * S::kRows * kBigK) + w * 1024;
         __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
     }
 }
@@ -225,30 +234,17 @@ struct BigOps {
                 for (int u = 0; u < 2; ++u)
                     acc[i][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[u], a[i], acc[i][u], 0, 0, 0);
     }
-    // The same with copies [FROM, FROM + F) .. of a later step between the MFMAs.
-    template <int FROM, int TO>
+    // The same with copies [FROM, TO) of a later step spread between the MFMAs:
+    // a wave that issues them in one go waits for the memory pipeline to take them.
+    template <int WN, int FROM, int TO, int I = 0>
     __device__ __forceinline__ void multiply_and_copy(i32x16 (&acc)[F][2], int8_t* la, int8_t* lb,
                                                       const int8_t* const (&pa)[4], const int8_t* const (&pb)[4],
                                                       int64_t k, int w) const {
         constexpr int N = TO - FROM;
-        big_copy<F, FROM, FROM + (N * 1 + F - 1) / F>(la, lb, pa, pb, k, w);
-        multiply(acc, 0, 1);
+        big_copy<WN, F, FROM + (N * I + F - 1) / F, FROM + (N * (I + 1) + F - 1) / F>(la, lb, pa, pb, k, w);
+        multiply(acc, I, I + 1);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (F > 1) {
-            big_copy<F, FROM + (N * 1 + F - 1) / F, FROM + (N * 2 + F - 1) / F>(la, lb, pa, pb, k, w);
-            multiply(acc, 1, 2);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (F > 2) {
-            big_copy<F, FROM + (N * 2 + F - 1) / F, FROM + (N * 3 + F - 1) / F>(la, lb, pa, pb, k, w);
-            multiply(acc, 2, 3);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (F > 3) {
-            big_copy<F, FROM + (N * 3 + F - 1) / F, FROM + (N * 4 + F - 1) / F>(la, lb, pa, pb, k, w);
-            multiply(acc, 3, 4);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        if constexpr (I + 1 < F) multiply_and_copy<WN, FROM, TO, I + 1>(acc, la, lb, pa, pb, k, w);
     }
 };
 
@@ -260,9 +256,9 @@ __device__ __forceinline__ void big_operands_here() {
 }
 
 // Zeroes the bytes from K on in the last step's rows of A (what B holds there is then multiplied by zero).
-template <int F>
+template <int WN, int F>
 __device__ __forceinline__ void big_mask(int8_t* la, int left, int tid) {
-    for (int i = tid; i < F * 64 * 8; i += 512) {
+    for (int i = tid; i < F * 64 * 8; i += 128 * WN) {
         const int row = i >> 3, k = ((i & 7) ^ big_swizzle(row)) << 4;
         if (k + 16 <= left) continue;
         i32x4* at = reinterpret_cast<i32x4*>(la + i * 16);
@@ -276,27 +272,44 @@ __device__ __forceinline__ void big_mask(int8_t* la, int left, int tid) {
     }
 }
 
-template <class D, int F>
-__device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0, int8_t* a0,
-                                         int8_t* b0, int8_t* a1, int8_t* b1, int32_t* lrow, float* lscale, int tid, int w,
-                                         int l) {
+// The buffers of a step: ST of them, each an array of its own, so that the
+// compiler can tell the copies into one from the operand reads of another.
+template <int ST>
+struct BigBuffers {
+    int8_t *a[ST], *b[ST];
+};
+
+// s_waitcnt that leaves at most n vector-memory operations outstanding and
+// waits for all LDS operations (vmcnt in bits 3:0 and 15:14, expcnt 6:4,
+// lgkmcnt 11:8), then the barrier.
+template <int N>
+__device__ __forceinline__ void big_barrier() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    asm volatile("s_barrier" ::: "memory");
+}
+
+template <class D, int WN, int ST, int F>
+__device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
+                                         const BigBuffers<ST>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
     typedef typename D::T T;
     const int wm = w & 1, wn = w >> 1;
-    // the rows this lane copies: 64 j + 8 w + l / 8, chunk (l % 8) ^ big_swizzle(row)
+    using S = BigShape<WN, F>;
+    // the rows this lane copies: kRows j + 8 w + l / 8, chunk (l % 8) ^ big_swizzle(row)
     const int crow = 8 * w + (l >> 3), chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
     const int8_t *pa[4], *pb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int64_t p = lo + 64 * j + crow;
-        const int64_t r = j < F && p < hi ? a_row(g, p) : -1;
+        const int row = S::kRows * j + crow;
+        const int64_t p = lo + row;
+        const int64_t r = j < S::kA && p < hi ? a_row(g, p) : -1;
         pa[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
-        if (j < F && (l & 7) == 0) {
-            lrow[64 * j + crow] = (int32_t)r;
-            lscale[64 * j + crow] = g.a_scale[max(r, (int64_t)0)];
+        if (j < S::kA && (l & 7) == 0) {
+            lrow[row] = (int32_t)r;
+            lscale[row] = g.a_scale[max(r, (int64_t)0)];
         }
-        pb[j] = g.B + e * g.strideb + min(n0 + 64 * j + crow, g.N - 1) * g.ldb;
+        pb[j] = g.B + e * g.strideb + min(n0 + row, g.N - 1) * g.ldb;
     }
-    if (tid < kBig) lscale[kBig + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
+    if (tid < 64 * WN) lscale[64 * WN + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
     const int64_t last = (g.K - 1) & ~(int64_t)15;  // chunks behind it are read from there and masked
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
@@ -311,66 +324,85 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
 
     // The operands of piece ks + 1 are read while the MFMAs of piece ks run.  The
     // barrier that ends a step stands before its last piece's MFMAs, when all of
-    // the step's operands are in registers: the copies of step s + 2 and the
-    // first operand reads of step s + 1 are then issued under those MFMAs.
+    // the step's operands are in registers: its buffer then takes the copies of
+    // step s + ST, half of them under those MFMAs and half under the next
+    // piece's.  Before the barrier a wave waits for its own copies of step s + 1;
+    // those of ST - 2 later steps stay in flight.  Copies behind the last step
+    // read its last chunk again, which keeps the counts the same.
     BigOps<F> x0, x1;
-    constexpr int kCopies = F + 4, kHalf = kCopies / 2;
-    big_copy<F, 0, kCopies>(a0, b0, pa, pb, min((int64_t)chunk, last), w);
-    __syncthreads();
+    constexpr int kCopies = S::kCopies, kHalf = kCopies / 2;
+#define SPX_AT(s) min((int64_t)(s) * kBigK + chunk, last)
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) big_copy<WN, F, 0, kCopies>(m.a[i], m.b[i], pa, pb, SPX_AT(i), w);
+    big_copy<WN, F, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], pa, pb, SPX_AT(ST - 1), w);
+    big_barrier<(ST - 2) * kCopies + kHalf>();
     if (steps == 1 && left < kBigK) {
-        big_mask<F>(a0, left, tid);
-        __syncthreads();
+        big_mask<WN, F>(m.a[0], left, tid);
+        big_barrier<(ST - 2) * kCopies + kHalf>();
     }
-    big_copy<F, 0, kHalf>(a1, b1, pa, pb, min((int64_t)kBigK + chunk, last), w);
-    x0.read(a0, b0, 0, wm, wn, l);
-#define SPX_STEP(s, la, lb, na, nb)                                                                             \
-    {                                                                                                            \
-        big_operands_here();                                                                                     \
-        x1.read(la, lb, 1, wm, wn, l);                                                                           \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x0.template multiply_and_copy<kHalf, kCopies>(acc, na, nb, pa, pb,                                       \
-                                             min((int64_t)((s) + 1) * kBigK + chunk, last), w);                  \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        big_operands_here();                                                                                     \
-        x0.read(la, lb, 2, wm, wn, l);                                                                           \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x1.multiply(acc);                                                                                        \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        big_operands_here();                                                                                     \
-        x1.read(la, lb, 3, wm, wn, l);                                                                           \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x0.multiply(acc);                                                                                        \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        __syncthreads();                                                                                         \
-        if ((s) + 2 == steps && left < kBigK) {                                                                  \
-            big_mask<F>(na, left, tid);                                                                          \
-            __syncthreads();                                                                                     \
-        }                                                                                                        \
-        x0.read(na, nb, 0, wm, wn, l);                                                                           \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
-        x1.template multiply_and_copy<0, kHalf>(acc, la, lb, pa, pb,                                             \
-                                       min((int64_t)((s) + 2) * kBigK + chunk, last), w);                        \
-        __builtin_amdgcn_sched_barrier(0);                                                                       \
+    x0.read(m.a[0], m.b[0], 0, wm, wn, l);
+#define SPX_STEP(s, I)                                                                                   \
+    {                                                                                                     \
+        constexpr int kNext = ((I) + 1) % ST, kBack = ((I) + ST - 1) % ST;                                \
+        big_operands_here();                                                                              \
+        x1.read(m.a[I], m.b[I], 1, wm, wn, l);                                                            \
+        __builtin_amdgcn_sched_barrier(0);                                                                \
+        x0.template multiply_and_copy<WN, kHalf, kCopies>(acc, m.a[kBack], m.b[kBack], pa, pb,            \
+                                                          SPX_AT((s) + ST - 1), w);                       \
+        big_operands_here();                                                                              \
+        x0.read(m.a[I], m.b[I], 2, wm, wn, l);                                                            \
+        __builtin_amdgcn_sched_barrier(0);                                                                \
+        x1.multiply(acc);                                                                                 \
+        big_operands_here();                                                                              \
+        x1.read(m.a[I], m.b[I], 3, wm, wn, l);                                                            \
+        __builtin_amdgcn_sched_barrier(0);                                                                \
+        x0.multiply(acc);                                                                                 \
+        __builtin_amdgcn_sched_barrier(0);                                                                \
+        big_barrier<(ST - 2) * kCopies>();                                                                \
+        if ((s) + 2 == steps && left < kBigK) {                                                           \
+            big_mask<WN, F>(m.a[kNext], left, tid);                                                       \
+            big_barrier<(ST - 2) * kCopies>();                                                            \
+        }                                                                                                 \
+        x0.read(m.a[kNext], m.b[kNext], 0, wm, wn, l);                                                    \
+        __builtin_amdgcn_sched_barrier(0);                                                                \
+        x1.template multiply_and_copy<WN, 0, kHalf>(acc, m.a[I], m.b[I], pa, pb, SPX_AT((s) + ST), w);    \
     }
     int s = 0;
-    for (; s + 2 <= steps; s += 2) {
-        SPX_STEP(s, a0, b0, a1, b1);
-        SPX_STEP(s + 1, a1, b1, a0, b0);
+    for (; s + ST <= steps; s += ST) {
+        SPX_STEP(s, 0);
+        SPX_STEP(s + 1, 1);
+        if constexpr (ST == 4) {
+            SPX_STEP(s + 2, 2);
+            SPX_STEP(s + 3, 3);
+        }
     }
-    if (s < steps) SPX_STEP(s, a0, b0, a1, b1);
-    __syncthreads();  // the copies behind the last step have landed too
+    if (s < steps) {
+        SPX_STEP(s, 0);
+        if constexpr (ST == 4) {
+            if (s + 1 < steps) {
+                SPX_STEP(s + 1, 1);
+                if (s + 2 < steps) SPX_STEP(s + 2, 2);
+            }
+        }
+    }
 #undef SPX_STEP
+#undef SPX_AT
+    __syncthreads();  // the copies behind the last step have landed too
 
-    // Sums of one 32-row block at a time through this wave's part of LDS
-    // (8.5 KB each, three to a buffer), then 8 consecutive columns a
-    // lane, 8 rows an instruction.  D layout of the 32 x 32 MFMA: lane l,
-    // register r -> first operand's row 8 (r/4) + 4 (l/32) + r%4 (a column of
-    // C), second operand's row l%32 (a row of C).
-    int32_t* mine = reinterpret_cast<int32_t*>(w < 3 ? b0 : w < 6 ? b1 : a0) + (w % 3) * (32 * kBigRow);
+    // Sums of one 32-row block at a time through this wave's part of LDS, then 8
+    // consecutive columns a lane, 8 rows an instruction.  D layout of the 32 x 32
+    // MFMA: lane l, register r -> first operand's row 8 (r/4) + 4 (l/32) + r%4 (a
+    // column of C), second operand's row l%32 (a row of C).
+    constexpr int kSums = 32 * kBigRow, kPer = 64 * WN * kBigK / (4 * kSums);  // waves to a buffer
+    static_assert(4 * kPer >= 2 * WN, "the waves' sums fit the four buffers");
+    int8_t* const buffer = w / kPer == 0 ? m.b[0] : w / kPer == 1 ? m.b[1] : w / kPer == 2 ? m.a[0] : m.a[1];
+    int32_t* mine = reinterpret_cast<int32_t*>(buffer) + (w % kPer) * kSums;
+    constexpr int N = Chunk<T>::N;
     const int64_t n = n0 + 64 * wn + 8 * (l & 7);
+    const bool inside = n0 + 64 * WN <= g.N;  // the whole tile's columns
     float sb[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sb[i] = lscale[kBig + 64 * wn + 8 * (l & 7) + i];
+    for (int i = 0; i < 8; ++i) sb[i] = lscale[64 * WN + 64 * wn + 8 * (l & 7) + i];
 #pragma unroll
     for (int i = 0; i < F; ++i) {
 #pragma unroll
@@ -381,79 +413,273 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
                 *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
             }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {  // rolled: straight-line code here is fetched once and costs more than it saves
-            const int row = 8 * q + (l >> 3), tr = 32 * (2 * i + wm) + row;
-            const i32x4 v0 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7));
-            const i32x4 v1 = *reinterpret_cast<const i32x4*>(mine + row * kBigRow + 8 * (l & 7) + 4);
-            const int r = lrow[tr];
-            if (r < 0 || n >= g.N) continue;
-            const float sa = lscale[tr];
+        const auto row_out = [&](int r, float sa, i32x4 v0, i32x4 v1, int64_t tr, bool whole) {
             T* c = (T*)g.C + (lo + tr) * g.ldc + n;
-            constexpr int N = Chunk<T>::N;
             typename Chunk<T>::V o[8 / N];
 #pragma unroll
             for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
 #pragma unroll
-            for (int x = 0; x < 8 / N; ++x)
-                if (n + x * N < g.N) chunk_store(c + x * N, g.N - n - x * N, o[x]);
+            for (int x = 0; x < 8 / N; ++x) {
+                if (whole)
+                    *reinterpret_cast<typename Chunk<T>::U*>(c + x * N) = o[x];
+                else if (n + x * N < g.N)
+                    chunk_store(c + x * N, g.N - n - x * N, o[x]);
+            }
+        };
+        const int32_t* at = mine + (l >> 3) * kBigRow + 8 * (l & 7);
+        const int tr0 = 32 * (2 * i + wm) + (l >> 3);
+        if (inside) {
+            i32x4 v[4][2];
+            int r[4];
+            float sa[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[q][0] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
+                v[q][1] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
+                r[q] = lrow[tr0 + 8 * q];
+                sa[q] = lscale[tr0 + 8 * q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (r[q] >= 0) row_out(r[q], sa[q], v[q][0], v[q][1], tr0 + 8 * q, true);
+        } else {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 v0 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
+                const i32x4 v1 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
+                const int r = lrow[tr0 + 8 * q];
+                if (r >= 0) row_out(r, lscale[tr0 + 8 * q], v0, v1, tr0 + 8 * q, false);
+            }
         }
         __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <class D>
-__global__ __launch_bounds__(512) void gemm_i8_big(GemmArgs g) {
-    __shared__ __attribute__((aligned(1024))) int8_t a0[kBig * kBigK], a1[kBig * kBigK], b0[kBig * kBigK], b1[kBig * kBigK];
-    __shared__ int32_t lrow[kBig];       // row of A of every row of the tile, or -1
-    __shared__ float lscale[2 * kBig];   // scales of the tile's rows, then of its columns
+template <class D, int WN, int ST>
+__global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(GemmArgs g) {
+    constexpr int kBytes = 64 * WN * kBigK;
+    __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
+    __shared__ int32_t lrow[64 * WN];       // row of A of every row of the tile, or -1
+    __shared__ float lscale[2 * 64 * WN];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     // neighbouring tiles on one XCD, four row tiles to a column tile
-    const int v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
+    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
     const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
     const uint32_t high = min(g.m_tiles - first, 4u);
-    const int64_t nt = in / high;
+    const int64_t n0 = (int64_t)(in / high) * (64 * WN);
     int e;
     int64_t lo, hi;
-    if (!find_tile<kBig>(g, (int)(first + in % high), l, e, lo, hi)) return;
-    switch ((hi - lo + 63) >> 6) {
-        case 1: big_tile<D, 1>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
-        case 2: big_tile<D, 2>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
-        case 3: big_tile<D, 3>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
-        default: big_tile<D, 4>(g, e, lo, hi, nt * kBig, a0, b0, a1, b1, lrow, lscale, tid, w, l); break;
+    if (!find_tile<64 * WN>(g, (int)(first + in % high), l, e, lo, hi)) return;
+    const int blocks = (int)((hi - lo + 63) >> 6);
+    if constexpr (ST == 4) {
+        __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
+        const BigBuffers<4> m = {{a0, a1, a2, a3}, {b0, b1, b2, b3}};
+        if (blocks == 1) return big_tile<D, WN, ST, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        big_tile<D, WN, ST, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+    } else {
+        const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
+        if (blocks == 1) return big_tile<D, WN, ST, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        if constexpr (WN == 4) {
+            if (blocks == 3) return big_tile<D, WN, ST, 3>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+            if (blocks == 4) return big_tile<D, WN, ST, 4>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        }
+        big_tile<D, WN, ST, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: tiles of 16 R rows x 16 C columns, W waves that share the tile and
+// split K.
+//
+// With few rows the time is that of reading B once, so B goes from memory
+// straight into MFMA operands (16 rows of 64 bytes an instruction), each wave
+// taking 128 bytes of every row in turn and reading its next 128 before it
+// multiplies; the rows of A come from L2 the same way.  The waves' int32 sums
+// meet in LDS, exact in any order.
+template <int R, int C>
+struct ThinOps {
+    i32x4 a[2][R], b[2][C];
+    __device__ __forceinline__ void read(const int8_t* const (&pa)[R], const int8_t* const (&pb)[C], int64_t k,
+                                         int64_t last) {
+        const int64_t k0 = min(k, last), k1 = min(k + 64, last);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {  // both halves of a 128-byte line, one after the other
+            b[0][j] = *reinterpret_cast<const i32x4*>(pb[j] + k0);
+            b[1][j] = *reinterpret_cast<const i32x4*>(pb[j] + k1);
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            a[0][j] = *reinterpret_cast<const i32x4*>(pa[j] + k0);
+            a[1][j] = *reinterpret_cast<const i32x4*>(pa[j] + k1);
+        }
+    }
+    // left: bytes of K from this lane's k on
+    __device__ __forceinline__ void mask(int64_t left) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int64_t keep = left - 64 * h - 4 * d;
+                const int32_t m = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * (int)keep)) - 1;
+#pragma unroll
+                for (int j = 0; j < R; ++j) a[h][j][d] &= m;
+            }
+    }
+    __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[h][j], a[h][i], acc[i][j], 0, 0, 0);
+    }
+};
+
+template <class D, int R, int C, int W>
+__global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
+    typedef typename D::T T;
+    constexpr int BM = 16 * R, BN = 16 * C, LD = BN + 4;
+    __shared__ __attribute__((aligned(16))) int32_t part[W * BM * LD];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    // the row tiles of one column tile follow each other: those of one expert meet its rows of B in one L2
+    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
+    int e;
+    int64_t lo, hi;
+    if (!find_tile<BM>(g, (int)(v % g.m_tiles), l, e, lo, hi)) return;
+    const int64_t n0 = (int64_t)(v / g.m_tiles) * BN;
+    const int8_t *pa[R], *pb[C];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t p = lo + 16 * i + (l & 15);
+        pa[i] = g.A + max(p < hi ? a_row(g, p) : -1, (int64_t)0) * g.lda;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) pb[j] = g.B + e * g.strideb + min(n0 + 16 * j + (l & 15), g.N - 1) * g.ldb;
+
+    i32x4 acc[R][C];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int64_t last = (g.K - 1) & ~(int64_t)15;
+    const int lk = 16 * (l >> 4);
+    ThinOps<R, C> x, y;
+    int64_t k = 128 * w;
+    x.read(pa, pb, k + lk, last);
+    for (; k < g.K; k += 256 * W) {
+        y.read(pa, pb, k + 128 * W + lk, last);
+        if (k + 128 > g.K) x.mask(g.K - k - lk);
+        x.multiply(acc);
+        if (k + 128 * W >= g.K) break;
+        x.read(pa, pb, k + 256 * W + lk, last);
+        if (k + 128 * W + 128 > g.K) y.mask(g.K - k - 128 * W - lk);
+        y.multiply(acc);
+    }
+    // D layout of the 16 x 16 MFMA: lane l, register r -> first operand's row 4 (l/16) + r (a column of C),
+    // second operand's row l%16 (a row of C)
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            *reinterpret_cast<i32x4*>(part + (w * BM + 16 * i + (l & 15)) * LD + 16 * j + 4 * (l >> 4)) = acc[i][j];
+    __syncthreads();
+    for (int x4 = tid; x4 < BM * BN / 4; x4 += 64 * W) {
+        const int row = x4 / (BN / 4), col = x4 % (BN / 4) * 4;
+        const int64_t p = lo + row, n = n0 + col;
+        if (p >= hi || n >= g.N) continue;
+        const int64_t ra = a_row(g, p);
+        if (ra < 0) continue;
+        i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < W; ++u) sum += *reinterpret_cast<const i32x4*>(part + (u * BM + row) * LD + col);
+        const float sa = g.a_scale[ra];
+        const float* sb = g.b_scale + e * g.N + n;
+        T* c = (T*)g.C + p * g.ldc + n;
+        typedef T V4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+        if (n + 4 <= g.N) {
+            V4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = scaled<D>(sum[i], sa, sb[i]);
+            *reinterpret_cast<V4*>(c) = o;
+        } else {
+            for (int i = 0; i < 3; ++i)
+                if (n + i < g.N) c[i] = scaled<D>(sum[i], sa, sb[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launch
 bool aligned16(const GemmArgs& g) {
-    return ((uintptr_t)g.A | (uintptr_t)g.B | (uintptr_t)g.lda | (uintptr_t)g.ldb | (uintptr_t)(g.E > 1 ? g.strideb : 0)) % 16 == 0;
+    return ((uintptr_t)g.A | (uintptr_t)g.B | (uintptr_t)g.lda | (uintptr_t)g.ldb |
+            (uintptr_t)(g.E > 1 ? g.strideb : 0)) % 16 == 0;
 }
 
-// Tile counts of the launch; false if there are 2^31 or more.
-bool set_tiles(GemmArgs& g, int64_t bm, int64_t bn) {
-    const int64_t m = g.offsets ? g.S / bm + std::min<int64_t>(g.E, g.S) : (g.S + bm - 1) / bm, n = (g.N + bn - 1) / bn;
-    g.m_tiles = (uint32_t)m;
-    g.n_tiles = (uint32_t)n;
-    return m * n < (int64_t)1 << 31;
+// Tile counts of a launch with bm x bn tiles (an upper bound on the row tiles
+// when the offsets are on the device).
+int64_t row_tiles(const GemmArgs& g, int64_t bm) {
+    return g.offsets ? g.S / bm + std::min<int64_t>(g.E, g.S) : (g.S + bm - 1) / bm;
 }
+int64_t tiles(const GemmArgs& g, int64_t bm, int64_t bn) { return row_tiles(g, bm) * ((g.N + bn - 1) / bn); }
 
-template <class D>
-int launch_big(GemmArgs g, hipStream_t s) {
-    set_tiles(g, kBig, kBig);
-    hipLaunchKernelGGL((gemm_i8_big<D>), dim3((unsigned)(g.m_tiles * g.n_tiles)), dim3(512), 0, s, g);
+// Workgroups of a launch: the kernels for 16-byte rows take one tile each and
+// are not launched with more; the plain one goes on to the next.
+constexpr int64_t kMostTiles = 1 << 22;
+
+template <class K>
+int launch(K kernel, GemmArgs g, int64_t bm, int64_t bn, int threads, hipStream_t s) {
+    const int64_t n = tiles(g, bm, bn);
+    if (n >= (int64_t)1 << 31) return SP_ERR_SIZE;
+    g.m_tiles = (uint32_t)row_tiles(g, bm);
+    g.n_tiles = (uint32_t)((g.N + bn - 1) / bn);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(n, kMostTiles)), dim3(threads), 0, s, g);
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 
+// Which kernel.  Times are M x N x K, or tokens x choices, experts, K, N with
+// the weights read from memory each time, in us.
 template <class D>
 int gemm_t(GemmArgs g, hipStream_t s) {
-    constexpr int64_t BM = 64, BN = 64;
+    if (g.a_rows == 0) return SP_OK;  // no row of C has a row of A
     const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
-    if (g.K > 0 && g.a_rows > 0 && aligned16(g) && g.S >= 32 * groups && set_tiles(g, kBig, kBig) &&
-        g.m_tiles * g.n_tiles < 1 << 22)
-        return launch_big<D>(g, s);
-    if (!set_tiles(g, BM, BN)) return SP_ERR_SIZE;
-    const uint32_t grid = std::min<uint32_t>(g.m_tiles * g.n_tiles, 1 << 22);
-    hipLaunchKernelGGL((gemm_i8_plain<D>), dim3((unsigned)grid), dim3(256), 0, s, g);
-    return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
+    // Rows that no 16-byte access fits: through registers, 1.5 to 8 times the
+    // others' time (8192 x 8192 x 4096: 646 against 254).
+    if (g.K == 0 || !aligned16(g) || tiles(g, 256, 256) > kMostTiles)
+        return launch(gemm_i8_plain<D>, g, 64, 64, 256, s);
+    // Few tiles: the smallest ones, or most CUs stay idle.  A step up where 128
+    // or 256 tiles are reached: 1 x 4096 x 4096 16x16 6.7, 16x32 8.5;
+    // 8 x 8192 x 4096 16x16 11.8, 16x32 11.0; 32 x 4096 x 4096 16x32 10.1,
+    // 32x32 11.9; 64 x 4096 x 4096 16x32 15.8, 32x32 12.1, 32x64 16.3;
+    // 128 x 4096 x 4096 32x32 19.8, 32x64 16.7, 128x128 23.7;
+    // 256 x 4096 x 4096 32x64 28.8, 128x128 23.1.
+    if (tiles(g, 16, 32) <= 128) return launch(gemm_i8_thin<D, 1, 1, 8>, g, 16, 16, 512, s);
+    // Few rows a matrix (up to 16 of a single one, 8 on the average of several,
+    // where some have more): 32 x 8, 64, 4096, 2048 16x32 91, 32x64 101, 128x128 128.
+    const bool few = tiles(g, 16, 32) <= kMostTiles;
+    if (tiles(g, 16, 32) <= 256 || (few && g.S <= (groups == 1 ? 16 : 8) * groups))
+        return launch(gemm_i8_thin<D, 1, 2, 4>, g, 16, 32, 256, s);
+    if (tiles(g, 32, 32) <= 256) return launch(gemm_i8_thin<D, 2, 2, 4>, g, 32, 32, 256, s);
+    // 96 x 8, 64, 4096, 2048 (12 rows an expert) 32x64 120, 128x128 131; 128 x 8 (16 rows) 127, 129;
+    // 64 x 2, 8, 4096, 14336 (16 rows) 135, 118.
+    if (tiles(g, 32, 64) <= 256 || (few && g.S <= 12 * groups))
+        return launch(gemm_i8_thin<D, 2, 4, 4>, g, 32, 64, 256, s);
+    // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
+    // for memory: four steps in LDS.  1024 x 4096 x 4096 28 against 36 with two
+    // steps and two workgroups a CU, and 55 with 256 x 256 tiles;
+    // 256 x 8, 64, 4096, 2048 (32 rows) 133, 157, 166.
+    const int64_t mid = tiles(g, 128, 128);
+    if (mid <= 256 || (few && g.S < 48 * groups))
+        return launch(gemm_i8_big<D, 2, 4>, g, 128, 128, 256, s);
+    // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 48, with four steps 53,
+    // with 256 x 256 tiles 57; 512 x 8, 64, 4096, 2048 (64 rows) 157, 152, 171;
+    // 256 x 2, 8, 4096, 14336 (64 rows) 146, 149, 170.  Also where 256-wide tiles
+    // would be empty for a fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
+    const int64_t wide = (g.N + 255) / 256 * 256, narrow = (g.N + 127) / 128 * 128;
+    if (mid <= 512 || (few && (g.S < 96 * groups || 5 * wide >= 6 * narrow)))
+        return launch(gemm_i8_big<D, 2, 2>, g, 128, 128, 256, s);
+    // 8192 x 8192 x 4096 251 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
+    // 71, 89; 4096 x 8, 64, 4096, 2048 (512 rows) 358, 420; 1024 x 8 (128 rows) 183, 195.
+    return launch(gemm_i8_big<D, 4, 2>, g, 256, 256, 512, s);
 }
 
 }  // namespace

@@ -339,7 +339,10 @@ def product_close(got, sums, sa, sb, dtype):
 PRODUCTS = [(1, 1, 1), (1, 64, 64), (1, 130, 1111), (2, 17, 16), (3, 33, 100), (5, 200, 4096), (15, 31, 127),
             (16, 16, 64), (17, 257, 129), (31, 64, 640), (33, 96, 255), (64, 128, 256), (65, 129, 1024), (100, 300, 513),
             (127, 255, 128), (130, 258, 192), (256, 256, 512), (257, 513, 1000), (300, 40, 2000), (40, 300, 8192),
-            (513, 1025, 384), (7, 5, 0), (2, 3, 131071), (520, 264, 65)]
+            (513, 1025, 384), (7, 5, 0), (2, 3, 131071), (520, 264, 65),
+            # one or more of each tile size: 16x32, 32x32, 32x64, 128x128 with four and two steps in LDS, 256x256
+            (3, 8200, 80), (16, 4200, 300), (130, 1000, 200), (300, 1000, 129), (600, 1100, 700), (2100, 2100, 136),
+            (2049, 2200, 400), (3000, 3100, 300), (2817, 4097, 128)]
 STRIDES = [(0, 0), (16, 16), (5, 3)]
 
 
@@ -379,7 +382,11 @@ EXPERTS = [(1, 1, 1, 16, 16, 0, "random", True), (1, 8, 64, 130, 256, 0, "random
            (50, 2, 7, 64, 128, 0, "none", True), (300, 3, 4, 257, 192, 0.1, "skew", True),
            (700, 2, 5, 300, 320, 0, "one", True), (130, 4, 9, 128, 1111, 0.2, "random", True),
            (600, 1, 130, 70, 64, 0.1, "random", False), (2000, 2, 8, 272, 512, 0.1, "skew", False),
-           (90, 3, 1024, 24, 48, 0, "random", True), (5, 2, 3, 8, 0, 0, "random", True)]
+           (90, 3, 1024, 24, 48, 0, "random", True), (5, 2, 3, 8, 0, 0, "random", True),
+           # the same for the experts: few rows each, 8 to 12, up to 48, up to 96, many
+           (60, 4, 32, 700, 272, 0.1, "random", True), (50, 7, 32, 600, 272, 0, "skew", True),
+           (100, 8, 32, 600, 144, 0.05, "random", True), (300, 8, 30, 1100, 300, 0.1, "skew", True),
+           (2600, 2, 4, 1700, 130, 0.05, "random", True), (5300, 1, 3, 1800, 272, 0, "skew", False)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
