@@ -171,68 +171,122 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
 }
 
 // ---------------------------------------------------------------- rows
-// A workgroup of 256 threads takes 256 / tpr tokens; tpr lanes (a power of
-// two) share a token's row, and blockIdx.y cuts the row when tpr lanes of one
-// chunk do not cover it.
+// TPR lanes share a token, 256 / TPR tokens a workgroup.  A token's slots are
+// taken U at a time: their places first, then the U rows' chunks, all in
+// flight together.  A slot routed nowhere is made to read the first row (there
+// is one, or no row is live) and its bits are zeroed, so that the loads need
+// no branch; its weight counts as zero.
+//
+// A row's last chunk starts at H - N where a whole one does not fit: it then
+// repeats elements of the chunk before it, which are written twice with the
+// same value (and counted once in the products of the gradient).  Only rows
+// shorter than one chunk (WHOLE false) go element by element.
 struct RowArgs {
     int64_t T, H, S, ld_tok, ld_row;
     int32_t slots;
-    int32_t tpr_log;
 };
 
-template <class D>
-__global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a, const typename D::T* __restrict__ X,
-                                                           const int32_t* __restrict__ pos,
-                                                           typename D::T* __restrict__ Xs) {
-    typedef typename D::T T;
-    constexpr int N = Chunk<T>::N;
-    const int rpb = 256 >> a.tpr_log, sub = threadIdx.x >> a.tpr_log, lane = threadIdx.x & ((1 << a.tpr_log) - 1);
-    const int64_t step = (int64_t)gridDim.y << a.tpr_log;
-    for (int64_t t = (int64_t)blockIdx.x * rpb + sub; t < a.T; t += (int64_t)gridDim.x * rpb) {
-        const int32_t* p = pos + t * a.slots;
-        for (int64_t c = ((int64_t)blockIdx.y << a.tpr_log) + lane; c * N < a.H; c += step) {
-            const auto v = chunk_load(X + t * a.ld_tok + c * N, a.H - c * N);
-            for (int j = 0; j < a.slots; ++j) {
-                const int q = p[j];
-                if (q >= 0 && q < a.S) chunk_store(Xs + q * a.ld_row + c * N, a.H - c * N, v);
-            }
-        }
+template <int TPR>
+__device__ __forceinline__ int64_t first_token() {
+    const int sub = threadIdx.x / TPR;
+    // a wave's lanes share the token: its places and weights are then scalar loads
+    return (int64_t)blockIdx.x * (256 / TPR) + (TPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+}
+
+// Places of slots [j0, j0 + U) of token t, -1 where there is none.
+template <int U>
+__device__ __forceinline__ void places(const RowArgs& a, const int32_t* __restrict__ pos, int64_t t, int j0,
+                                       int (&q)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int p = pos[t * a.slots + min(j0 + u, a.slots - 1)];
+        q[u] = j0 + u < a.slots && (unsigned)p < (unsigned)a.S ? p : -1;
     }
 }
 
-template <class D, bool W>
+template <class D, bool WHOLE>
+__device__ __forceinline__ typename Chunk<typename D::T>::V row_load(const RowArgs& a, const typename D::T* p) {
+    return WHOLE ? chunk_stream(p) : chunk_load(p, a.H);
+}
+template <class D, bool WHOLE>
+__device__ __forceinline__ void row_store(const RowArgs& a, typename D::T* p, typename Chunk<typename D::T>::V v) {
+    if (WHOLE)
+        chunk_stream(p, v);
+    else
+        chunk_store(p, a.H, v);
+}
+
+// The chunk at element k of the rows of U slots, zeros for a slot routed nowhere.
+template <class D, int U, bool WHOLE>
+__device__ __forceinline__ void slot_rows(const RowArgs& a, const typename D::T* __restrict__ Ys, int64_t ld, int64_t k,
+                                          const int (&q)[U], typename Chunk<typename D::T>::V (&y)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = row_load<D, WHOLE>(a, Ys + max(q[u], 0) * ld + k);
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = q[u] >= 0 ? y[u] : typename Chunk<typename D::T>::V(0);
+}
+
+template <class D, int TPR, bool WHOLE>
+__global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a, const typename D::T* __restrict__ X,
+                                                           const int32_t* __restrict__ pos,
+                                                           typename D::T* __restrict__ Xs) {
+    constexpr int N = Chunk<typename D::T>::N, U = 4;
+    const int64_t step = (int64_t)gridDim.y * TPR;
+    for (int64_t t = first_token<TPR>(); t < a.T; t += (int64_t)gridDim.x * (256 / TPR))
+        for (int64_t c = (int64_t)blockIdx.y * TPR + threadIdx.x % TPR; c * N < a.H; c += step) {
+            const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
+            const auto v = row_load<D, WHOLE>(a, X + t * a.ld_tok + k);
+            for (int j0 = 0; j0 < a.slots; j0 += U) {
+                int q[U];
+                places<U>(a, pos, t, j0, q);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (q[u] >= 0) row_store<D, WHOLE>(a, Xs + q[u] * a.ld_row + k, v);
+            }
+        }
+}
+
+// weights NULL: all ones (a product with 1 is exact).
+template <class D, int TPR, int U, bool WHOLE>
 __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a, const typename D::T* __restrict__ Ys,
                                                           const int32_t* __restrict__ pos,
                                                           const float* __restrict__ weights,
                                                           typename D::T* __restrict__ Y) {
     typedef typename D::T T;
     constexpr int N = Chunk<T>::N;
-    const int rpb = 256 >> a.tpr_log, sub = threadIdx.x >> a.tpr_log, lane = threadIdx.x & ((1 << a.tpr_log) - 1);
-    const int64_t step = (int64_t)gridDim.y << a.tpr_log;
-    for (int64_t t = (int64_t)blockIdx.x * rpb + sub; t < a.T; t += (int64_t)gridDim.x * rpb) {
-        const int32_t* p = pos + t * a.slots;
-        const float* w = weights + t * a.slots;
-        for (int64_t c = ((int64_t)blockIdx.y << a.tpr_log) + lane; c * N < a.H; c += step) {
+    const int64_t step = (int64_t)gridDim.y * TPR;
+    for (int64_t t = first_token<TPR>(); t < a.T; t += (int64_t)gridDim.x * (256 / TPR))
+        for (int64_t c = (int64_t)blockIdx.y * TPR + threadIdx.x % TPR; c * N < a.H; c += step) {
+            const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
             float acc[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-            for (int j = 0; j < a.slots; ++j) {
-                const int q = p[j];
-                if (q < 0 || q >= a.S) continue;
-                const auto v = chunk_load(Ys + q * a.ld_row + c * N, a.H - c * N);
+            for (int j0 = 0; j0 < a.slots; j0 += U) {
+                int q[U];
+                float w[U];
+                typename Chunk<T>::V y[U];
+                places<U>(a, pos, t, j0, q);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = W ? fmaf(w[j], D::up(v[i]), acc[i]) : acc[i] + D::up(v[i]);
+                for (int u = 0; u < U; ++u) {
+                    const float v = weights ? weights[t * a.slots + min(j0 + u, a.slots - 1)] : 1.0f;
+                    w[u] = q[u] >= 0 ? v : 0.0f;
+                }
+                slot_rows<D, U, WHOLE>(a, Ys, a.ld_row, k, q, y);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = fmaf(w[u], D::up(y[u][i]), acc[i]);
             }
             typename Chunk<T>::V o;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] = D::down(acc[i]);
-            chunk_store(Y + t * a.ld_tok + c * N, a.H - c * N, o);
+            row_store<D, WHOLE>(a, Y + t * a.ld_tok + k, o);
         }
-    }
 }
 
-// One workgroup per token: the token's dY row times each of its expert rows.
-template <class D>
+// TPR lanes form the products of a token's dY with U of its rows at a time and
+// add them across the lanes in a fixed order.
+template <class D, int TPR, int U, bool WHOLE>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, const typename D::T* __restrict__ dY,
                                                                    const typename D::T* __restrict__ Ys, int64_t ld_ys,
                                                                    const int32_t* __restrict__ pos,
@@ -241,79 +295,145 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, co
                                                                    float* __restrict__ dweights) {
     typedef typename D::T T;
     constexpr int N = Chunk<T>::N;
-    __shared__ float part[4];
-    const int tid = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        for (int j = 0; j < a.slots; ++j) {
-            const int q = pos[t * a.slots + j];
-            const bool live = q >= 0 && q < a.S;
-            float dot = 0.0f;
-            if (live) {
-                const float w = weights[t * a.slots + j];
-                for (int64_t c = tid; c * N < a.H; c += 256) {
-                    const auto g = chunk_load(dY + t * a.ld_tok + c * N, a.H - c * N);
-                    const auto y = chunk_load(Ys + q * ld_ys + c * N, a.H - c * N);
+    __shared__ float part[4][U];
+    const int lane = threadIdx.x % TPR;
+    for (int64_t t = first_token<TPR>(); t < a.T; t += (int64_t)gridDim.x * (256 / TPR))
+        for (int j0 = 0; j0 < a.slots; j0 += U) {
+            int q[U];
+            float w[U], dot[U];
+            places<U>(a, pos, t, j0, q);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = weights[t * a.slots + min(j0 + u, a.slots - 1)];
+                dot[u] = 0.0f;
+            }
+            for (int64_t c = lane; c * N < a.H; c += TPR) {
+                const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
+                const auto g = row_load<D, WHOLE>(a, dY + t * a.ld_tok + k);
+                typename Chunk<T>::V y[U];
+                slot_rows<D, U, WHOLE>(a, Ys, ld_ys, k, q, y);
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = D::up(g[i]);
+                // what the chunk before holds already counts as zero in the products, on both sides (0 * Inf is NaN)
+                const int again = (int)(c * N - k);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
                     typename Chunk<T>::V o;
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        dot = fmaf(D::up(g[i]), D::up(y[i]), dot);
-                        o[i] = D::down(w * D::up(g[i]));
+                        const float d = fmaf(f[i], D::up(y[u][i]), dot[u]);
+                        dot[u] = i >= again ? d : dot[u];
+                        o[i] = D::down(w[u] * f[i]);
                     }
-                    chunk_store(dYs + q * a.ld_row + c * N, a.H - c * N, o);
+                    if (q[u] >= 0) row_store<D, WHOLE>(a, dYs + q[u] * a.ld_row + k, o);
                 }
             }
-            dot = wave_sum(dot);
-            if ((tid & 63) == 0) part[tid >> 6] = dot;
-            __syncthreads();
-            if (tid == 0) dweights[t * a.slots + j] = live ? (part[0] + part[1]) + (part[2] + part[3]) : 0.0f;
-            __syncthreads();
+            if (TPR == 256) __syncthreads();  // part[] of the slots before has been read
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                dot[u] = group_sum(dot[u], TPR < 64 ? TPR : 64);
+                if (TPR == 256 && (threadIdx.x & 63) == 0) part[threadIdx.x >> 6][u] = dot[u];
+            }
+            if (TPR == 256) __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (lane == u && j0 + u < a.slots) {
+                    const float d = TPR == 256 ? (part[0][u] + part[1][u]) + (part[2][u] + part[3][u]) : dot[u];
+                    dweights[t * a.slots + j0 + u] = q[u] >= 0 ? d : 0.0f;
+                }
         }
-    }
-}
-
-// Lanes per token: the power of two that covers the row with one chunk a lane, 8 to 256.
-int lanes_log(int64_t H, int elems) {
-    const int64_t chunks = (H + elems - 1) / elems;
-    int l = 3;
-    while (l < 8 && ((int64_t)1 << l) < chunks) ++l;
-    return l;
 }
 
 constexpr int64_t kMaxGrid = 1 << 20;  // larger problems take several rounds of the grid
+constexpr int64_t kWavePerToken = 4096;
+
+// Lanes per token: 16, 64 or 256, enough to cover the row with a chunk a lane
+// where 256 do (grid.y cuts longer rows).
+template <class D>
+int lanes(int64_t H) {
+    const int64_t chunks = (H + Chunk<typename D::T>::N - 1) / Chunk<typename D::T>::N;
+    return chunks <= 16 ? 16 : chunks <= 64 ? 64 : 256;
+}
 
 template <class D>
-dim3 rows_grid(const RowArgs& a) {
-    constexpr int N = Chunk<typename D::T>::N;
-    const int64_t rpb = 256 >> a.tpr_log;
-    const int64_t per = (int64_t)N << a.tpr_log;
+dim3 rows_grid(const RowArgs& a, int tpr) {
+    const int64_t rpb = 256 / tpr, per = (int64_t)Chunk<typename D::T>::N * tpr;
     return dim3((unsigned)std::min<int64_t>((a.T + rpb - 1) / rpb, kMaxGrid),
                 (unsigned)std::min<int64_t>((a.H + per - 1) / per, 1024));
 }
 
+// go(lanes, whole) with both as compile-time constants
+template <int L, bool W>
+struct Shape {
+    static constexpr int lanes = L;
+    static constexpr bool whole = W;
+};
+template <class D, class Go>
+void by_shape(int lanes, int64_t H, Go go) {
+    if (H < Chunk<typename D::T>::N)
+        go(Shape<16, false>{});
+    else if (lanes == 16)
+        go(Shape<16, true>{});
+    else if (lanes == 64)
+        go(Shape<64, true>{});
+    else
+        go(Shape<256, true>{});
+}
+
 template <class D>
-hipError_t dispatch_t(RowArgs a, const void* X, const int32_t* pos, void* Xs, hipStream_t s) {
-    a.tpr_log = lanes_log(a.H, Chunk<typename D::T>::N);
-    hipLaunchKernelGGL((moe_dispatch_kernel<D>), rows_grid<D>(a), dim3(256), 0, s, a, (const typename D::T*)X, pos,
-                       (typename D::T*)Xs);
+hipError_t dispatch_t(const RowArgs& a, const void* X, const int32_t* pos, void* Xs, hipStream_t s) {
+    const int l = lanes<D>(a.H);
+    by_shape<D>(l, a.H, [&](auto c) {
+        typedef decltype(c) C;
+        hipLaunchKernelGGL((moe_dispatch_kernel<D, C::lanes, C::whole>), rows_grid<D>(a, C::lanes), dim3(256), 0, s, a,
+                           (const typename D::T*)X, pos, (typename D::T*)Xs);
+    });
+    return hipGetLastError();
+}
+
+template <class D, int U>
+hipError_t combine_u(const RowArgs& a, const void* Ys, const int32_t* pos, const float* weights, void* Y,
+                     hipStream_t s) {
+    by_shape<D>(lanes<D>(a.H), a.H, [&](auto c) {
+        typedef decltype(c) C;
+        hipLaunchKernelGGL((moe_combine_kernel<D, C::lanes, U, C::whole>), rows_grid<D>(a, C::lanes), dim3(256), 0, s,
+                           a, (const typename D::T*)Ys, pos, weights, (typename D::T*)Y);
+    });
     return hipGetLastError();
 }
 
 template <class D>
-hipError_t combine_t(RowArgs a, const void* Ys, const int32_t* pos, const float* weights, void* Y, hipStream_t s) {
-    a.tpr_log = lanes_log(a.H, Chunk<typename D::T>::N);
-    auto kernel = weights ? moe_combine_kernel<D, true> : moe_combine_kernel<D, false>;
-    hipLaunchKernelGGL(kernel, rows_grid<D>(a), dim3(256), 0, s, a, (const typename D::T*)Ys, pos, weights,
-                       (typename D::T*)Y);
-    return hipGetLastError();
+hipError_t combine_t(const RowArgs& a, const void* Ys, const int32_t* pos, const float* weights, void* Y,
+                     hipStream_t s) {
+    return a.slots <= 2   ? combine_u<D, 2>(a, Ys, pos, weights, Y, s)
+           : a.slots <= 4 ? combine_u<D, 4>(a, Ys, pos, weights, Y, s)
+                          : combine_u<D, 8>(a, Ys, pos, weights, Y, s);
 }
 
-template <class D>
-hipError_t combine_backward_t(RowArgs a, const void* dY, const void* Ys, int64_t ld_ys, const int32_t* pos,
+template <class D, int U>
+hipError_t combine_backward_u(const RowArgs& a, const void* dY, const void* Ys, int64_t ld_ys, const int32_t* pos,
                               const float* weights, void* dYs, float* dweights, hipStream_t s) {
-    hipLaunchKernelGGL((moe_combine_backward_kernel<D>), dim3((unsigned)std::min(a.T, kMaxGrid)), dim3(256), 0, s, a,
-                       (const typename D::T*)dY, (const typename D::T*)Ys, ld_ys, pos, weights, (typename D::T*)dYs,
-                       dweights);
+    // a wave per token where that fills the chip: one reduction for the whole row
+    int l = lanes<D>(a.H);
+    if (l == 256 && a.T >= kWavePerToken) l = 64;
+    by_shape<D>(l, a.H, [&](auto c) {
+        typedef decltype(c) C;
+        const int64_t rpb = 256 / C::lanes;
+        hipLaunchKernelGGL((moe_combine_backward_kernel<D, C::lanes, U, C::whole>),
+                           dim3((unsigned)std::min<int64_t>((a.T + rpb - 1) / rpb, kMaxGrid)), dim3(256), 0, s, a,
+                           (const typename D::T*)dY, (const typename D::T*)Ys, ld_ys, pos, weights, (typename D::T*)dYs,
+                           dweights);
+    });
     return hipGetLastError();
+}
+
+template <class D>
+hipError_t combine_backward_t(const RowArgs& a, const void* dY, const void* Ys, int64_t ld_ys, const int32_t* pos,
+                              const float* weights, void* dYs, float* dweights, hipStream_t s) {
+    return a.slots <= 2   ? combine_backward_u<D, 2>(a, dY, Ys, ld_ys, pos, weights, dYs, dweights, s)
+           : a.slots <= 4 ? combine_backward_u<D, 4>(a, dY, Ys, ld_ys, pos, weights, dYs, dweights, s)
+                          : combine_backward_u<D, 8>(a, dY, Ys, ld_ys, pos, weights, dYs, dweights, s);
 }
 
 int status(hipError_t e) { return e == hipSuccess ? SP_OK : SP_ERR_HIP; }
@@ -351,7 +471,7 @@ int moe_sort_device(int64_t n, int32_t E, const int32_t* ids, int32_t* offsets, 
 
 int moe_dispatch_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* X, int64_t ldx,
                         const int32_t* pos, void* Xs, int64_t lds, hipStream_t s) {
-    const RowArgs a{T, H, S, ldx, lds, slots, 0};
+    const RowArgs a{T, H, S, ldx, lds, slots};
     if (dtype == SP_F32) return status(dispatch_t<F32>(a, X, pos, Xs, s));
     if (dtype == SP_BF16) return status(dispatch_t<Bf16>(a, X, pos, Xs, s));
     return status(dispatch_t<F16>(a, X, pos, Xs, s));
@@ -359,7 +479,8 @@ int moe_dispatch_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t 
 
 int moe_combine_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* Ys, int64_t lds,
                        const int32_t* pos, const float* weights, void* Y, int64_t ldy, hipStream_t s) {
-    const RowArgs a{T, H, S, ldy, lds, slots, 0};
+    const RowArgs a{T, H, S, ldy, lds, slots};
+    if (S == 0) Ys = Y;  // no slot is live: what is read in their place is thrown away
     if (dtype == SP_F32) return status(combine_t<F32>(a, Ys, pos, weights, Y, s));
     if (dtype == SP_BF16) return status(combine_t<Bf16>(a, Ys, pos, weights, Y, s));
     return status(combine_t<F16>(a, Ys, pos, weights, Y, s));
@@ -368,7 +489,8 @@ int moe_combine_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t d
 int moe_combine_backward_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* dY,
                                 int64_t ldy, const void* Ys, int64_t lds, const int32_t* pos, const float* weights,
                                 void* dYs, int64_t ldd, float* dweights, hipStream_t s) {
-    const RowArgs a{T, H, S, ldy, ldd, slots, 0};
+    const RowArgs a{T, H, S, ldy, ldd, slots};
+    if (S == 0) Ys = dY;  // as in moe_combine_device
     if (dtype == SP_F32) return status(combine_backward_t<F32>(a, dY, Ys, lds, pos, weights, dYs, dweights, s));
     if (dtype == SP_BF16) return status(combine_backward_t<Bf16>(a, dY, Ys, lds, pos, weights, dYs, dweights, s));
     return status(combine_backward_t<F16>(a, dY, Ys, lds, pos, weights, dYs, dweights, s));

@@ -33,7 +33,17 @@ struct Chunk {
     typedef T U __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 
-// The `len` elements of the row from column c on, at most one chunk; the rest are zero.
+// A whole chunk; the data is used once (non-temporal).
+template <class T>
+__device__ __forceinline__ typename Chunk<T>::V chunk_stream(const T* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const typename Chunk<T>::U*>(p));
+}
+template <class T>
+__device__ __forceinline__ void chunk_stream(T* p, typename Chunk<T>::V v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Chunk<T>::U*>(p));
+}
+
+// The first `len` elements of a chunk, the rest zero.
 template <class T>
 __device__ __forceinline__ typename Chunk<T>::V chunk_load(const T* p, int64_t len) {
     typename Chunk<T>::V v;

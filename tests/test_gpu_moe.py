@@ -242,6 +242,17 @@ def test_places_out_of_range_are_skipped():
     assert (np.abs(f64(Y) - ref) <= (HALF["bf16"] + 8 * U) * np.abs(ref) + 8 * U * 60).all()
 
 
+@pytest.mark.parametrize("H", [3, 200])
+def test_no_sorted_rows(H):
+    """S = 0: every slot is routed nowhere, whatever its place says."""
+    pos = dev(np.array([[0, -1], [5, 1], [2, 2]], np.int32))
+    Ys = torch.empty(0, H, device="cuda")
+    assert (sp.moe_combine(Ys, pos, torch.ones(3, 2, device="cuda")) == 0).all()
+    dYs, dw = sp.moe_combine_backward(torch.ones(3, H, device="cuda"), Ys, pos, torch.ones(3, 2, device="cuda"))
+    assert dYs.shape == (0, H) and (dw == 0).all()
+    assert sp.moe_dispatch(torch.ones(3, H, device="cuda"), pos, S=0).shape == (0, H)
+
+
 def test_infinities_travel():
     pos = dev(np.array([[0, 1], [2, -1]], np.int32))
     Ys = torch.tensor([[float("inf"), 1.0], [float("-inf"), 2.0], [float("inf"), float("nan")]], device="cuda")
