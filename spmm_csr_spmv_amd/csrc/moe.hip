@@ -180,11 +180,21 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
 // A row's last chunk starts at H - N where a whole one does not fit: it then
 // repeats elements of the chunk before it, which are written twice with the
 // same value (and counted once in the products of the gradient).  Only rows
-// shorter than one chunk (WHOLE false) go element by element.
+// shorter than one chunk (kShort) go element by element.
+//
+// Where every row starts on a 128-byte line the loads are non-temporal (kStream; each
+// byte is read once: combine of 16384 x 8 rows of 2048 fp16 98 us, 115
+// without), and with 256 lanes a token the stores too (kStreamBoth; dispatch of 16384 x 4
+// rows of 4096 bf16 123 us, 129 without; rows of 1024 by 64 lanes 66, 63
+// without).  Rows that start inside a line share lines with their neighbours,
+// which only the caches put together: dispatch of 30000 x 6 rows of 333 fp16
+// 41 us non-temporal, 25 without.
 struct RowArgs {
     int64_t T, H, S, ld_tok, ld_row;
     int32_t slots;
+    bool lines;  // every row starts on a 128-byte line
 };
+enum Access { kShort, kCached, kStream, kStreamBoth };
 
 template <int TPR>
 __device__ __forceinline__ int64_t first_token() {
@@ -204,29 +214,30 @@ __device__ __forceinline__ void places(const RowArgs& a, const int32_t* __restri
     }
 }
 
-template <class D, bool WHOLE>
+template <class D, Access A>
 __device__ __forceinline__ typename Chunk<typename D::T>::V row_load(const RowArgs& a, const typename D::T* p) {
-    return WHOLE ? chunk_stream(p) : chunk_load(p, a.H);
+    if (A == kShort) return chunk_load(p, a.H);
+    return A == kCached ? chunk_load(p, Chunk<typename D::T>::N) : chunk_stream(p);
 }
-template <class D, bool WHOLE>
+template <class D, Access A>
 __device__ __forceinline__ void row_store(const RowArgs& a, typename D::T* p, typename Chunk<typename D::T>::V v) {
-    if (WHOLE)
+    if (A == kStreamBoth)
         chunk_stream(p, v);
     else
-        chunk_store(p, a.H, v);
+        chunk_store(p, A == kShort ? a.H : Chunk<typename D::T>::N, v);
 }
 
 // The chunk at element k of the rows of U slots, zeros for a slot routed nowhere.
-template <class D, int U, bool WHOLE>
+template <class D, int U, Access A>
 __device__ __forceinline__ void slot_rows(const RowArgs& a, const typename D::T* __restrict__ Ys, int64_t ld, int64_t k,
                                           const int (&q)[U], typename Chunk<typename D::T>::V (&y)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) y[u] = row_load<D, WHOLE>(a, Ys + max(q[u], 0) * ld + k);
+    for (int u = 0; u < U; ++u) y[u] = row_load<D, A>(a, Ys + max(q[u], 0) * ld + k);
 #pragma unroll
     for (int u = 0; u < U; ++u) y[u] = q[u] >= 0 ? y[u] : typename Chunk<typename D::T>::V(0);
 }
 
-template <class D, int TPR, bool WHOLE>
+template <class D, int TPR, Access A>
 __global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a, const typename D::T* __restrict__ X,
                                                            const int32_t* __restrict__ pos,
                                                            typename D::T* __restrict__ Xs) {
@@ -234,20 +245,20 @@ __global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a, const type
     const int64_t step = (int64_t)gridDim.y * TPR;
     for (int64_t t = first_token<TPR>(); t < a.T; t += (int64_t)gridDim.x * (256 / TPR))
         for (int64_t c = (int64_t)blockIdx.y * TPR + threadIdx.x % TPR; c * N < a.H; c += step) {
-            const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
-            const auto v = row_load<D, WHOLE>(a, X + t * a.ld_tok + k);
+            const int64_t k = A == kShort ? 0 : min(c * N, a.H - N);
+            const auto v = row_load<D, A>(a, X + t * a.ld_tok + k);
             for (int j0 = 0; j0 < a.slots; j0 += U) {
                 int q[U];
                 places<U>(a, pos, t, j0, q);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (q[u] >= 0) row_store<D, WHOLE>(a, Xs + q[u] * a.ld_row + k, v);
+                    if (q[u] >= 0) row_store<D, A>(a, Xs + q[u] * a.ld_row + k, v);
             }
         }
 }
 
 // weights NULL: all ones (a product with 1 is exact).
-template <class D, int TPR, int U, bool WHOLE>
+template <class D, int TPR, int U, Access A>
 __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a, const typename D::T* __restrict__ Ys,
                                                           const int32_t* __restrict__ pos,
                                                           const float* __restrict__ weights,
@@ -257,7 +268,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a, const typen
     const int64_t step = (int64_t)gridDim.y * TPR;
     for (int64_t t = first_token<TPR>(); t < a.T; t += (int64_t)gridDim.x * (256 / TPR))
         for (int64_t c = (int64_t)blockIdx.y * TPR + threadIdx.x % TPR; c * N < a.H; c += step) {
-            const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
+            const int64_t k = A == kShort ? 0 : min(c * N, a.H - N);
             float acc[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] = 0.0f;
@@ -271,7 +282,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a, const typen
                     const float v = weights ? weights[t * a.slots + min(j0 + u, a.slots - 1)] : 1.0f;
                     w[u] = q[u] >= 0 ? v : 0.0f;
                 }
-                slot_rows<D, U, WHOLE>(a, Ys, a.ld_row, k, q, y);
+                slot_rows<D, U, A>(a, Ys, a.ld_row, k, q, y);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -280,13 +291,13 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a, const typen
             typename Chunk<T>::V o;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] = D::down(acc[i]);
-            row_store<D, WHOLE>(a, Y + t * a.ld_tok + k, o);
+            row_store<D, A>(a, Y + t * a.ld_tok + k, o);
         }
 }
 
 // TPR lanes form the products of a token's dY with U of its rows at a time and
 // add them across the lanes in a fixed order.
-template <class D, int TPR, int U, bool WHOLE>
+template <class D, int TPR, int U, Access A>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, const typename D::T* __restrict__ dY,
                                                                    const typename D::T* __restrict__ Ys, int64_t ld_ys,
                                                                    const int32_t* __restrict__ pos,
@@ -308,10 +319,10 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, co
                 dot[u] = 0.0f;
             }
             for (int64_t c = lane; c * N < a.H; c += TPR) {
-                const int64_t k = WHOLE ? min(c * N, a.H - N) : 0;
-                const auto g = row_load<D, WHOLE>(a, dY + t * a.ld_tok + k);
+                const int64_t k = A == kShort ? 0 : min(c * N, a.H - N);
+                const auto g = row_load<D, A>(a, dY + t * a.ld_tok + k);
                 typename Chunk<T>::V y[U];
-                slot_rows<D, U, WHOLE>(a, Ys, ld_ys, k, q, y);
+                slot_rows<D, U, A>(a, Ys, ld_ys, k, q, y);
                 float f[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) f[i] = D::up(g[i]);
@@ -326,7 +337,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, co
                         dot[u] = i >= again ? d : dot[u];
                         o[i] = D::down(w[u] * f[i]);
                     }
-                    if (q[u] >= 0) row_store<D, WHOLE>(a, dYs + q[u] * a.ld_row + k, o);
+                    if (q[u] >= 0) row_store<D, A>(a, dYs + q[u] * a.ld_row + k, o);
                 }
             }
             if (TPR == 256) __syncthreads();  // part[] of the slots before has been read
@@ -346,47 +357,56 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(RowArgs a, co
 }
 
 constexpr int64_t kMaxGrid = 1 << 20;  // larger problems take several rounds of the grid
-constexpr int64_t kWavePerToken = 4096;
 
-// Lanes per token: 16, 64 or 256, enough to cover the row with a chunk a lane
-// where 256 do (grid.y cuts longer rows).
+// Lanes per token: 16, 64 or 256, so that none takes more than `each` chunks
+// where 256 suffice for that.  The row movements take one (grid.y cuts longer
+// rows); the gradient two, to spread its reduction over more of the row
+// (65536 x 2 rows of 1024 bf16 104 us with a wave per token, 126 with four;
+// 16384 x 4 rows of 4096 239 with one, 222 with four).
 template <class D>
-int lanes(int64_t H) {
+int lanes(int64_t H, int each) {
     const int64_t chunks = (H + Chunk<typename D::T>::N - 1) / Chunk<typename D::T>::N;
-    return chunks <= 16 ? 16 : chunks <= 64 ? 64 : 256;
+    return chunks <= 16 * each ? 16 : chunks <= 64 * each ? 64 : 256;
 }
 
+// Tokens in x; with few of them rows are cut over y (16 x 8 rows of 4096 bf16
+// combined in 3.5 us, uncut 4.4).  Many tokens fill the chip by themselves,
+// and a workgroup then takes whole rows (dispatch of 16384 x 4 rows of 4096
+// 123 us, cut 132).
 template <class D>
 dim3 rows_grid(const RowArgs& a, int tpr) {
     const int64_t rpb = 256 / tpr, per = (int64_t)Chunk<typename D::T>::N * tpr;
     return dim3((unsigned)std::min<int64_t>((a.T + rpb - 1) / rpb, kMaxGrid),
-                (unsigned)std::min<int64_t>((a.H + per - 1) / per, 1024));
+                (unsigned)(a.T >= 2048 ? 1 : std::min<int64_t>((a.H + per - 1) / per, 1024)));
 }
 
-// go(lanes, whole) with both as compile-time constants
-template <int L, bool W>
+bool on_lines(const void* p, int64_t ld, int32_t dtype) {
+    return ((uintptr_t)p | (uintptr_t)(ld * (dtype == SP_F32 ? 4 : 2))) % 128 == 0;
+}
+
+// go(shape) with the lanes and the kind of access as compile-time constants
+template <int L, Access A>
 struct Shape {
     static constexpr int lanes = L;
-    static constexpr bool whole = W;
+    static constexpr Access access = A;
 };
 template <class D, class Go>
-void by_shape(int lanes, int64_t H, Go go) {
-    if (H < Chunk<typename D::T>::N)
-        go(Shape<16, false>{});
+void by_shape(int lanes, const RowArgs& a, Go go) {
+    if (a.H < Chunk<typename D::T>::N)
+        go(Shape<16, kShort>{});
     else if (lanes == 16)
-        go(Shape<16, true>{});
+        go(Shape<16, kCached>{});
     else if (lanes == 64)
-        go(Shape<64, true>{});
+        a.lines ? go(Shape<64, kStream>{}) : go(Shape<64, kCached>{});
     else
-        go(Shape<256, true>{});
+        a.lines ? go(Shape<256, kStreamBoth>{}) : go(Shape<256, kCached>{});
 }
 
 template <class D>
 hipError_t dispatch_t(const RowArgs& a, const void* X, const int32_t* pos, void* Xs, hipStream_t s) {
-    const int l = lanes<D>(a.H);
-    by_shape<D>(l, a.H, [&](auto c) {
+    by_shape<D>(lanes<D>(a.H, 1), a, [&](auto c) {
         typedef decltype(c) C;
-        hipLaunchKernelGGL((moe_dispatch_kernel<D, C::lanes, C::whole>), rows_grid<D>(a, C::lanes), dim3(256), 0, s, a,
+        hipLaunchKernelGGL((moe_dispatch_kernel<D, C::lanes, C::access>), rows_grid<D>(a, C::lanes), dim3(256), 0, s, a,
                            (const typename D::T*)X, pos, (typename D::T*)Xs);
     });
     return hipGetLastError();
@@ -395,9 +415,9 @@ hipError_t dispatch_t(const RowArgs& a, const void* X, const int32_t* pos, void*
 template <class D, int U>
 hipError_t combine_u(const RowArgs& a, const void* Ys, const int32_t* pos, const float* weights, void* Y,
                      hipStream_t s) {
-    by_shape<D>(lanes<D>(a.H), a.H, [&](auto c) {
+    by_shape<D>(lanes<D>(a.H, 1), a, [&](auto c) {
         typedef decltype(c) C;
-        hipLaunchKernelGGL((moe_combine_kernel<D, C::lanes, U, C::whole>), rows_grid<D>(a, C::lanes), dim3(256), 0, s,
+        hipLaunchKernelGGL((moe_combine_kernel<D, C::lanes, U, C::access>), rows_grid<D>(a, C::lanes), dim3(256), 0, s,
                            a, (const typename D::T*)Ys, pos, weights, (typename D::T*)Y);
     });
     return hipGetLastError();
@@ -414,13 +434,10 @@ hipError_t combine_t(const RowArgs& a, const void* Ys, const int32_t* pos, const
 template <class D, int U>
 hipError_t combine_backward_u(const RowArgs& a, const void* dY, const void* Ys, int64_t ld_ys, const int32_t* pos,
                               const float* weights, void* dYs, float* dweights, hipStream_t s) {
-    // a wave per token where that fills the chip: one reduction for the whole row
-    int l = lanes<D>(a.H);
-    if (l == 256 && a.T >= kWavePerToken) l = 64;
-    by_shape<D>(l, a.H, [&](auto c) {
+    by_shape<D>(lanes<D>(a.H, 2), a, [&](auto c) {
         typedef decltype(c) C;
         const int64_t rpb = 256 / C::lanes;
-        hipLaunchKernelGGL((moe_combine_backward_kernel<D, C::lanes, U, C::whole>),
+        hipLaunchKernelGGL((moe_combine_backward_kernel<D, C::lanes, U, C::access>),
                            dim3((unsigned)std::min<int64_t>((a.T + rpb - 1) / rpb, kMaxGrid)), dim3(256), 0, s, a,
                            (const typename D::T*)dY, (const typename D::T*)Ys, ld_ys, pos, weights, (typename D::T*)dYs,
                            dweights);
@@ -471,7 +488,7 @@ int moe_sort_device(int64_t n, int32_t E, const int32_t* ids, int32_t* offsets, 
 
 int moe_dispatch_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* X, int64_t ldx,
                         const int32_t* pos, void* Xs, int64_t lds, hipStream_t s) {
-    const RowArgs a{T, H, S, ldx, lds, slots};
+    const RowArgs a{T, H, S, ldx, lds, slots, on_lines(X, ldx, dtype) && on_lines(Xs, lds, dtype)};
     if (dtype == SP_F32) return status(dispatch_t<F32>(a, X, pos, Xs, s));
     if (dtype == SP_BF16) return status(dispatch_t<Bf16>(a, X, pos, Xs, s));
     return status(dispatch_t<F16>(a, X, pos, Xs, s));
@@ -479,7 +496,7 @@ int moe_dispatch_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t 
 
 int moe_combine_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* Ys, int64_t lds,
                        const int32_t* pos, const float* weights, void* Y, int64_t ldy, hipStream_t s) {
-    const RowArgs a{T, H, S, ldy, lds, slots};
+    const RowArgs a{T, H, S, ldy, lds, slots, on_lines(Y, ldy, dtype) && on_lines(Ys, lds, dtype)};
     if (S == 0) Ys = Y;  // no slot is live: what is read in their place is thrown away
     if (dtype == SP_F32) return status(combine_t<F32>(a, Ys, pos, weights, Y, s));
     if (dtype == SP_BF16) return status(combine_t<Bf16>(a, Ys, pos, weights, Y, s));
@@ -489,7 +506,8 @@ int moe_combine_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t d
 int moe_combine_backward_device(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype, const void* dY,
                                 int64_t ldy, const void* Ys, int64_t lds, const int32_t* pos, const float* weights,
                                 void* dYs, int64_t ldd, float* dweights, hipStream_t s) {
-    const RowArgs a{T, H, S, ldy, ldd, slots};
+    const RowArgs a{T, H, S, ldy, ldd, slots,
+                    on_lines(dY, ldy, dtype) && on_lines(Ys, lds, dtype) && on_lines(dYs, ldd, dtype)};
     if (S == 0) Ys = dY;  // as in moe_combine_device
     if (dtype == SP_F32) return status(combine_backward_t<F32>(a, dY, Ys, lds, pos, weights, dYs, dweights, s));
     if (dtype == SP_BF16) return status(combine_backward_t<Bf16>(a, dY, Ys, lds, pos, weights, dYs, dweights, s));
