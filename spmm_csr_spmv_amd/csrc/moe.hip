@@ -24,19 +24,18 @@ namespace {
 // ---------------------------------------------------------------- counting sort
 constexpr int kSortThreads = 1024;   // 512 above kSortWideE experts, whose counts would not fit 64 KB of LDS
 constexpr int kSortWideE = 512;
-constexpr int kSortChunk = 4096;     // slots per workgroup, at least (more when the grid is at its cap)
-constexpr int kSortOneBlock = 8192;  // up to this many slots one workgroup does everything
+constexpr int kSortOneBlock = 4096;  // up to this many slots one workgroup does everything (6.9 us; two kernels 8.4)
 
-// Workgroups of the two-kernel path.  Every workgroup of the second kernel
-// reads all counts, so their number is bounded by kSortHist.
-constexpr int kSortMaxBlocks = 256;
-constexpr int kSortHist = 1 << 16;
+// Workgroups of the two-kernel path: 1024 slots each up to 128 of them (16384
+// slots 8.6 us, 9.5 with 4096 each), then up to 256 (524288 slots 12.9 us with
+// 128, 13.5 with 256).  Every workgroup of the second kernel reads all counts,
+// so that kSortHist bounds them.
+constexpr int kSortHist = 1 << 17;
 
 int sort_blocks(int64_t n, int32_t E) {
     if (n <= kSortOneBlock) return 1;
-    int64_t nb = (n + kSortChunk - 1) / kSortChunk;
-    const int64_t cap = std::max<int64_t>(8, std::min<int64_t>(kSortMaxBlocks, kSortHist / E));
-    return (int)std::min(nb, cap);
+    const int64_t nb = std::min<int64_t>((n + 1023) / 1024, std::max<int64_t>(128, std::min<int64_t>(256, n / 4096)));
+    return (int)std::min<int64_t>(nb, std::max<int64_t>(8, kSortHist / E));
 }
 
 __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
@@ -45,12 +44,24 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(const int32_t* 
     for (int e = threadIdx.x; e < E; e += kSortThreads) lds[e] = 0;
     __syncthreads();
     const int64_t b = blockIdx.x * per_block, end = min(b + per_block, n);
+#pragma unroll 4
     for (int64_t f = b + threadIdx.x; f < end; f += kSortThreads) {
         const int id = ids[f];
         if ((unsigned)id < (unsigned)E) atomicAdd(&lds[id], 1);  // integers: the order does not matter
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(int64_t)blockIdx.x * E + e] = lds[e];
+}
+
+// Slots f, f + 64, .. (up to end), loaded together; -1 behind the end.
+constexpr int kSortBatch = 4;
+__device__ __forceinline__ void load_ids(const int32_t* __restrict__ ids, int64_t f, int64_t end,
+                                         int (&id)[kSortBatch]) {
+#pragma unroll
+    for (int b = 0; b < kSortBatch; ++b) id[b] = ids[min(f + 64 * b, end - 1)];
+#pragma unroll
+    for (int b = 0; b < kSortBatch; ++b)
+        if (f + 64 * b >= end) id[b] = -1;
 }
 
 // Inclusive prefix sum over the 64 lanes.
@@ -90,9 +101,12 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
     const int64_t per_wave = (per_block + 64 * nw - 1) / (64 * nw) * 64;
     const int64_t wb = min(b + w * per_wave, end), we = min(wb + per_wave, end);
     int32_t* mine = cnt + w * E;
-    for (int64_t f = wb + lane; f < we; f += 64) {
-        const int id = ids[f];
-        if ((unsigned)id < (unsigned)E) atomicAdd(&mine[id], 1);
+    for (int64_t f0 = wb; f0 < we; f0 += 64 * kSortBatch) {
+        int id[kSortBatch];
+        load_ids(ids, f0 + lane, we, id);
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b)
+            if ((unsigned)id[b] < (unsigned)E) atomicAdd(&mine[id[b]], 1);
     }
     // slots of each expert in all workgroups and in the earlier ones
     const int groups = hist ? max(1, nth / E2) : 0;
@@ -101,6 +115,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
         const int g = i / E2, e = i % E2;
         int all = 0, early = 0;
         if (e < E)
+#pragma unroll 8
             for (int r = g; r < nb; r += groups) {
                 const int v = hist[(int64_t)r * E + e];
                 all += v;
@@ -113,10 +128,12 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
     // start[e] := slots of expert e (all workgroups)
     for (int e = tid; e < E; e += nth) {
         int s = 0;
-        if (hist)
+        if (hist) {
             for (int g = 0; g < groups; ++g) s += tot[g * E2 + e];
-        else
-            for (int v = 0; v < nw; ++v) s += cnt[v * E + e];
+        } else {
+#pragma unroll
+            for (int v = 0; v < kSortThreads / 64; ++v) s += v < nw ? cnt[v * E + e] : 0;
+        }
         start[e] = s;
     }
     __syncthreads();
@@ -136,35 +153,47 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
         int p = start[e];
         if (hist)
             for (int g = 0; g < groups; ++g) p += before[g * E2 + e];
-        for (int v = 0; v < nw; ++v) {
-            const int c = cnt[v * E + e];
-            cnt[v * E + e] = p;
-            p += c;
+        int c[kSortThreads / 64];  // all loads first
+#pragma unroll
+        for (int v = 0; v < kSortThreads / 64; ++v) c[v] = v < nw ? cnt[v * E + e] : 0;
+#pragma unroll
+        for (int v = 0; v < kSortThreads / 64; ++v) {
+            if (v < nw) cnt[v * E + e] = p;
+            p += c[v];
         }
     }
     if (blockIdx.x == 0)
         for (int e = tid; e <= E; e += nth) offsets[e] = start[e];
     __syncthreads();
 
-    for (int64_t f0 = wb; f0 < we; f0 += 64) {
-        const int64_t f = f0 + lane;
-        const int id = f < we ? ids[f] : -1;
-        const bool live = (unsigned)id < (unsigned)E;
-        uint64_t same = __ballot(live);
-        for (int k = 0; k < id_bits; ++k) {
-            const uint64_t m = __ballot((id >> k) & 1);
-            same &= ((id >> k) & 1) ? m : ~m;
+    for (int64_t f0 = wb; f0 < we; f0 += 64 * kSortBatch) {
+        int ids4[kSortBatch];
+        load_ids(ids, f0 + lane, we, ids4);
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            const int64_t f = f0 + 64 * b + lane;
+            const int id = ids4[b];
+            const bool live = (unsigned)id < (unsigned)E;
+            uint64_t same = __ballot(live);
+            if (same == 0) {  // nothing routed in this step (or behind the end)
+                if (f < we) pos[f] = -1;
+                continue;
+            }
+            for (int k = 0; k < id_bits; ++k) {
+                const uint64_t m = __ballot((id >> k) & 1);
+                same &= ((id >> k) & 1) ? m : ~m;
+            }
+            if (live) {
+                const int rank = __popcll(same & ((1ull << lane) - 1));
+                const int p = mine[id] + rank;
+                if (rank == 0) mine[id] = p + __popcll(same);  // the wave's lanes have all read it
+                src[p] = (int32_t)f;
+                pos[f] = p;
+            } else if (f < we) {
+                pos[f] = -1;
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        if (live) {
-            const int rank = __popcll(same & ((1ull << lane) - 1));
-            const int p = mine[id] + rank;
-            if (rank == 0) mine[id] = p + __popcll(same);  // the wave's lanes have all read it
-            src[p] = (int32_t)f;
-            pos[f] = p;
-        } else if (f < we) {
-            pos[f] = -1;
-        }
-        __builtin_amdgcn_wave_barrier();
     }
     // the places behind the last routed slot
     for (int64_t p = start[E] + (int64_t)blockIdx.x * nth + tid; p < n; p += (int64_t)nb * nth) src[p] = -1;
