@@ -15,6 +15,7 @@ import torch
 
 from ._binding import SP_OK, SparseError, _on, _sz, lib
 
+_Tensor = torch.Tensor
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -32,7 +33,10 @@ def _type(t, name):
 
 def _want(t, dtype, dim, name, device=None):
     """Checks type, number of dimensions and device (a number; None: any)."""
-    if not isinstance(t, torch.Tensor):
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == dim and (
+            device is None or t.get_device() == device):
+        return
+    if not isinstance(t, _Tensor):
         raise TypeError("%s must be a tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -40,8 +44,7 @@ def _want(t, dtype, dim, name, device=None):
         raise TypeError("%s must be a device tensor" % name)
     if t.dim() != dim:
         raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
-    if device is not None and t.get_device() != device:
-        raise ValueError("%s is on device %d, the others on %d" % (name, t.get_device(), device))
+    raise ValueError("%s is on device %d, the others on %d" % (name, t.get_device(), device))
 
 
 def _whole(t, dtype, dim, name, device=None):

@@ -46,38 +46,63 @@ __device__ __forceinline__ void cut(int a, int b, int i, int64_t& lo, int64_t& h
     hi = min(lo + height, (int64_t)b);
 }
 
-// Row tile number `tile` of the launch: expert e, rows [lo, hi) of its range,
-// at most BM of them.  Every wave of a workgroup finds it by itself: the
-// experts' tile counts, 64 at a time, a prefix sum over the lanes, and the
-// first lane past `tile`.  false: there are fewer tiles than that.  Offsets
-// outside [0, S] are clamped, a descending pair is an empty expert.
+// Rows [a, b) of expert e.  Offsets outside [0, S] are clamped, a descending
+// pair is an empty expert.
+__device__ __forceinline__ void expert_rows(const GemmArgs& g, int e, int& a, int& b) {
+    a = b = 0;
+    if (e < g.E) {
+        a = min(max(g.offsets[e], 0), (int)g.S);
+        b = max(a, min(max(g.offsets[e + 1], 0), (int)g.S));
+    }
+}
+
+// Inclusive prefix sum over the 64 lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// Row tiles that the experts' rows make (the launch has room for more: it
+// does not know the offsets).  Every wave counts for itself, 64 experts at a time.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const GemmArgs& g, int tile, int lane, int& e, int64_t& lo, int64_t& hi) {
+__device__ __forceinline__ uint32_t count_tiles(const GemmArgs& g, int lane) {
+    if (!g.offsets) return g.m_tiles;
+    uint32_t n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int a, b;
+        expert_rows(g, e0 + lane, a, b);
+        n += __builtin_amdgcn_readlane(wave_scan(((uint32_t)(b - a) + (BM - 1)) / BM, lane), 63);
+    }
+    return n;
+}
+
+// Row tile number `tile` of the launch: expert e and rows [lo, hi) of its
+// range, found by every wave of a workgroup for itself: the experts' tile
+// counts, a prefix sum over the lanes, and the first lane past `tile`.
+// false: there are fewer tiles than that.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const GemmArgs& g, uint32_t tile, int lane, int& e, int64_t& lo,
+                                          int64_t& hi) {
     if (!g.offsets) {
         e = 0;
-        cut<BM>(0, (int)g.S, tile, lo, hi);
+        cut<BM>(0, (int)g.S, (int)tile, lo, hi);
         return (int64_t)tile * BM < g.S;
     }
-    int before = 0;
+    uint32_t before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
-        int a = 0, b = 0;
-        if (e0 + lane < g.E) {
-            a = min(max(g.offsets[e0 + lane], 0), (int)g.S);
-            b = max(a, min(max(g.offsets[e0 + lane + 1], 0), (int)g.S));
-        }
-        const int mine = (int)(((uint32_t)(b - a) + (BM - 1)) / BM);
-        int sum = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += u;
-        }
+        int a, b;
+        expert_rows(g, e0 + lane, a, b);
+        const uint32_t mine = ((uint32_t)(b - a) + (BM - 1)) / BM, sum = wave_scan(mine, lane);
         const uint64_t past = __ballot(before + sum > tile);
         if (past) {
             const int l = __builtin_ctzll(past);
             e = e0 + l;
-            const int first = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
-            cut<BM>(__builtin_amdgcn_readlane(a, l), __builtin_amdgcn_readlane(b, l), tile - first, lo, hi);
+            const uint32_t first = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
+            cut<BM>(__builtin_amdgcn_readlane(a, l), __builtin_amdgcn_readlane(b, l), (int)(tile - first), lo, hi);
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -128,7 +153,7 @@ __global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
     for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int e;
         int64_t lo, hi;
-        if (!find_tile<BM>(g, (int)(t / g.n_tiles), l, e, lo, hi)) continue;
+        if (!find_tile<BM>(g, t / g.n_tiles, l, e, lo, hi)) continue;
         const int64_t n0 = (int64_t)(t % g.n_tiles) * BN;
         const int64_t ar = lo + row < hi ? a_row(g, lo + row) : -1;
         const int8_t* pa = g.A + max(ar, (int64_t)0) * g.lda;
@@ -462,14 +487,18 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
     __shared__ int32_t lrow[64 * WN];       // row of A of every row of the tile, or -1
     __shared__ float lscale[2 * 64 * WN];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    // neighbouring tiles on one XCD, four row tiles to a column tile
-    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
+    // Neighbouring tiles on one XCD, four row tiles to a column tile.  The tiles
+    // that there are, not those that the launch has room for, are dealt out to
+    // the XCDs: the last one would get the empty ones.
+    const uint32_t m_tiles = count_tiles<64 * WN>(g, l);
+    if (blockIdx.x >= m_tiles * g.n_tiles) return;
+    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)(m_tiles * g.n_tiles));
     const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
-    const uint32_t high = min(g.m_tiles - first, 4u);
+    const uint32_t high = min(m_tiles - first, 4u);
     const int64_t n0 = (int64_t)(in / high) * (64 * WN);
     int e;
     int64_t lo, hi;
-    if (!find_tile<64 * WN>(g, (int)(first + in % high), l, e, lo, hi)) return;
+    if (!find_tile<64 * WN>(g, first + in % high, l, e, lo, hi)) return;
     const int blocks = (int)((hi - lo + 63) >> 6);
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
@@ -546,7 +575,7 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
     int e;
     int64_t lo, hi;
-    if (!find_tile<BM>(g, (int)(v % g.m_tiles), l, e, lo, hi)) return;
+    if (!find_tile<BM>(g, v % g.m_tiles, l, e, lo, hi)) return;
     const int64_t n0 = (int64_t)(v / g.m_tiles) * BN;
     const int8_t *pa[R], *pb[C];
 #pragma unroll
