@@ -24,6 +24,12 @@ def _check(fn, code):
         raise SparseError(fn, code, lib())
 
 
+# The calls take a few microseconds on the GPU at small sizes, so each tests its
+# arguments in one expression first; _want and _whole, which say what is wrong,
+# run where that fails.
+_F32, _I32, _I8 = torch.float32, torch.int32, torch.int8
+
+
 def _type(t, name):
     code = _TYPES.get(t.dtype)
     if code is None:
@@ -82,15 +88,19 @@ def _apart(out, name, *inputs):
                 raise ValueError("%s overlaps an input" % name)
 
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _call(body, t, stream, *args):
     """body(raw stream, *args) with t's device current and allocations on the stream."""
     device = t.get_device()
-    if stream is None and device == torch._C._cuda_getDevice():
-        return body(torch._C._cuda_getCurrentRawStream(device), *args)
+    if stream is None and device == _current_device():
+        return body(_current_stream(device), *args)
     if stream is not None and stream.device.index != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
     with torch.cuda.device(device), _on(stream):
-        return body(torch._C._cuda_getCurrentRawStream(device), *args)
+        return body(_current_stream(device), *args)
 
 
 @functools.lru_cache(maxsize=256)
@@ -106,16 +116,16 @@ def moe_sort(ids, num_experts, work=None, stream=None):
     at place p (-1 from place offsets[-1] on), pos[f] the place of slot f; a slot
     whose id is outside [0, num_experts) is routed nowhere, its pos is -1.  `work` is
     a uint8 device tensor of moe_sort_bufsize bytes (allocated when None)."""
-    _whole(ids, torch.int32, ids.dim(), "ids")
+    _whole(ids, _I32, ids.dim(), "ids")
     n, num_experts = ids.numel(), int(num_experts)
     need = _sort_bytes(n, num_experts)
     return _call(_sort, ids, stream, ids, n, num_experts, need, work)
 
 
 def _sort(raw, ids, n, num_experts, need, work):
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
-    src = torch.empty(n, dtype=torch.int32, device=ids.device)
-    pos = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    offsets = torch.empty(num_experts + 1, dtype=_I32, device=ids.device)
+    src = torch.empty(n, dtype=_I32, device=ids.device)
+    pos = torch.empty(ids.shape, dtype=_I32, device=ids.device)
     if work is None:
         work = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
     elif work.device != ids.device or not work.is_contiguous():
@@ -131,24 +141,27 @@ def moe_dispatch(X, pos, S=None, out=None, stream=None):
     int32 T x slots (moe_sort); S defaults to T * slots.  Rows that no slot names keep
     their contents (they are undefined where out is allocated here)."""
     code = _type(X, "X")
-    _want(X, X.dtype, 2, "X")
-    _whole(pos, torch.int32, 2, "pos", X.get_device())
-    T, H = X.shape
-    if pos.shape[0] != T or pos.shape[1] < 1:
+    device = X.get_device()
+    if not (X.dim() == 2 and device >= 0 and pos.dtype is _I32 and pos.dim() == 2 and pos.get_device() == device
+            and pos.is_contiguous()):
+        _want(X, X.dtype, 2, "X")
+        _whole(pos, _I32, 2, "pos", device)
+    T, slots = pos.shape
+    if X.shape[0] != T or slots < 1:
         raise ValueError("pos must be T x slots, slots at least 1")
-    return _call(_dispatch, X, stream, code, X, pos, S, out)
+    return _call(_dispatch, X, stream, code, X, pos, T, slots, S, out)
 
 
-def _dispatch(raw, code, X, pos, S, out):
-    T, H = X.shape
+def _dispatch(raw, code, X, pos, T, slots, S, out):
+    H = X.shape[1]
     if out is None:
-        out = torch.empty(pos.numel() if S is None else int(S), H, dtype=X.dtype, device=X.device)
+        out = torch.empty(T * slots if S is None else int(S), H, dtype=X.dtype, device=X.device)
     else:
         _want(out, X.dtype, 2, "out", X.get_device())
         if out.shape[1] != H or (S is not None and out.shape[0] != S):
             raise ValueError("out must be S x H")
         _apart(out, "out", X, pos)
-    _check("moe_dispatch", lib().moe_dispatch(T, pos.shape[1], H, out.shape[0], code, X.data_ptr(),
+    _check("moe_dispatch", lib().moe_dispatch(T, slots, H, out.shape[0], code, X.data_ptr(),
                                               _rows(X, "X"), pos.data_ptr(), out.data_ptr(), _rows(out, "out"), raw))
     return out
 
@@ -157,19 +170,22 @@ def moe_combine(Ys, pos, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] Ys[pos[t, j]] (T x H); weights float32 T x slots, or
     None for all ones (then it is also the gradient of moe_dispatch)."""
     code = _type(Ys, "Ys")
-    _want(Ys, Ys.dtype, 2, "Ys")
-    _whole(pos, torch.int32, 2, "pos", Ys.get_device())
-    if pos.shape[1] < 1:
-        raise ValueError("pos must be T x slots, slots at least 1")
-    if weights is not None:
-        _whole(weights, torch.float32, 2, "weights", Ys.get_device())
-        if weights.shape != pos.shape:
-            raise ValueError("weights must have pos's shape")
+    device = Ys.get_device()
+    if not (Ys.dim() == 2 and device >= 0 and pos.dtype is _I32 and pos.dim() == 2 and pos.get_device() == device
+            and pos.is_contiguous()):
+        _want(Ys, Ys.dtype, 2, "Ys")
+        _whole(pos, _I32, 2, "pos", device)
+    if weights is not None and not (weights.dtype is _F32 and weights.shape == pos.shape
+                                    and weights.get_device() == device and weights.is_contiguous()):
+        _whole(weights, _F32, 2, "weights", device)
+        raise ValueError("weights must have pos's shape")
     return _call(_combine, Ys, stream, code, Ys, pos, weights, out)
 
 
 def _combine(raw, code, Ys, pos, weights, out):
     (T, slots), (S, H) = pos.shape, Ys.shape
+    if slots < 1:
+        raise ValueError("pos must be T x slots, slots at least 1")
     if out is None:
         out = torch.empty(T, H, dtype=Ys.dtype, device=Ys.device)
     else:
@@ -188,12 +204,16 @@ def moe_combine_backward(dY, Ys, pos, weights, dYs=None, dweights=None, stream=N
     rows that no slot names keep their contents, undefined where dYs is allocated here)
     and dweights[t, j] = <dY[t], Ys[pos[t, j]]>, 0 where the slot is routed nowhere."""
     code = _type(Ys, "Ys")
-    _want(Ys, Ys.dtype, 2, "Ys")
-    _want(dY, Ys.dtype, 2, "dY", Ys.get_device())
-    _whole(pos, torch.int32, 2, "pos", Ys.get_device())
-    _whole(weights, torch.float32, 2, "weights", Ys.get_device())
-    (T, slots), (S, H) = pos.shape, Ys.shape
-    if slots < 1 or weights.shape != pos.shape or tuple(dY.shape) != (T, H):
+    device = Ys.get_device()
+    if not (Ys.dim() == 2 and device >= 0 and dY.dtype is Ys.dtype and dY.dim() == 2 and dY.get_device() == device
+            and pos.dtype is _I32 and pos.dim() == 2 and pos.get_device() == device and pos.is_contiguous()
+            and weights.dtype is _F32 and weights.get_device() == device and weights.is_contiguous()):
+        _want(Ys, Ys.dtype, 2, "Ys")
+        _want(dY, Ys.dtype, 2, "dY", device)
+        _whole(pos, _I32, 2, "pos", device)
+        _whole(weights, _F32, 2, "weights", device)
+    T, slots = pos.shape
+    if slots < 1 or weights.shape != pos.shape or dY.shape[0] != T or dY.shape[1] != Ys.shape[1]:
         raise ValueError("dY must be T x H, pos and weights T x slots, slots at least 1")
     return _call(_combine_backward, Ys, stream, code, dY, Ys, pos, weights, dYs, dweights)
 
@@ -208,9 +228,9 @@ def _combine_backward(raw, code, dY, Ys, pos, weights, dYs, dweights):
             raise ValueError("dYs must be S x H")
         _apart(dYs, "dYs", dY, Ys, pos, weights)
     if dweights is None:
-        dweights = torch.empty(T, slots, dtype=torch.float32, device=Ys.device)
+        dweights = torch.empty(T, slots, dtype=_F32, device=Ys.device)
     else:
-        _whole(dweights, torch.float32, 2, "dweights", Ys.get_device())
+        _whole(dweights, _F32, 2, "dweights", Ys.get_device())
         if dweights.shape != pos.shape:
             raise ValueError("dweights must have pos's shape")
         _apart(dweights, "dweights", dY, Ys, pos, weights, dYs)
@@ -233,18 +253,18 @@ def quantize_rows_i8(X, q=None, scale=None, stream=None):
 def _quantize(raw, code, X, q, scale):
     rows, K = X.shape
     if q is None:
-        q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.int8, device=X.device)
+        q = torch.empty(rows, (K + 15) // 16 * 16, dtype=_I8, device=X.device)
         if q.shape[1] != K:
             q = q[:, :K]
     else:
-        _want(q, torch.int8, 2, "q", X.get_device())
+        _want(q, _I8, 2, "q", X.get_device())
         if q.shape != X.shape:
             raise ValueError("q must have X's shape")
         _apart(q, "q", X)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        scale = torch.empty(rows, dtype=_F32, device=X.device)
     else:
-        _whole(scale, torch.float32, 1, "scale", X.get_device())
+        _whole(scale, _F32, 1, "scale", X.get_device())
         if scale.shape[0] != rows:
             raise ValueError("scale must have one entry per row")
         _apart(scale, "scale", X, q)
@@ -253,9 +273,17 @@ def _quantize(raw, code, X, q, scale):
     return q, scale
 
 
-def _codes(A, a_scale):
-    _want(A, torch.int8, 2, "A")
-    _whole(a_scale, torch.float32, 1, "a_scale", A.get_device())
+def _operands(A, a_scale, B, b_scale, dim):
+    """Types, dimensions and devices of a product's operands (B has dim dimensions)."""
+    device = A.get_device()
+    if not (A.dtype is _I8 and A.dim() == 2 and device >= 0 and B.dtype is _I8 and B.dim() == dim
+            and B.get_device() == device and a_scale.dtype is _F32 and a_scale.dim() == 1
+            and a_scale.get_device() == device and a_scale.is_contiguous() and b_scale.dtype is _F32
+            and b_scale.dim() == dim - 1 and b_scale.get_device() == device and b_scale.is_contiguous()):
+        _want(A, _I8, 2, "A")
+        _whole(a_scale, _F32, 1, "a_scale", device)
+        _want(B, _I8, dim, "B", device)
+        _whole(b_scale, _F32, dim - 1, "b_scale", device)
     if a_scale.shape[0] != A.shape[0]:
         raise ValueError("a_scale must have one entry per row of A")
 
@@ -276,9 +304,7 @@ def _product_out(out, dtype, rows, N, A, *inputs):
 def gemm_i8(A, a_scale, B, b_scale, out=None, dtype=torch.bfloat16, stream=None):
     """out[m, n] = a_scale[m] b_scale[n] sum_k A[m, k] B[n, k]: A int8 M x K, B int8 N x K, scales
     float32; out in `dtype` (float32, bfloat16 or float16) when it is allocated here."""
-    _codes(A, a_scale)
-    _want(B, torch.int8, 2, "B", A.get_device())
-    _whole(b_scale, torch.float32, 1, "b_scale", A.get_device())
+    _operands(A, a_scale, B, b_scale, 2)
     (M, K), N = A.shape, B.shape[0]
     if B.shape[1] != K or b_scale.shape[0] != N:
         raise ValueError("B must be N x K and b_scale have one entry per row of B")
@@ -299,15 +325,13 @@ def moe_gemm_i8(A, a_scale, B, b_scale, offsets, src=None, slots=1, out=None, dt
     int32 [E + 1] (moe_sort).  Row p of out in expert e's range is the product of A's row p, or
     with src (moe_sort's, and its slots per token) of A's row src[p] // slots.  Rows behind the
     last expert's keep their contents (undefined where out is allocated here)."""
-    _codes(A, a_scale)
-    _want(B, torch.int8, 3, "B", A.get_device())
-    _whole(b_scale, torch.float32, 2, "b_scale", A.get_device())
-    _whole(offsets, torch.int32, 1, "offsets", A.get_device())
+    _operands(A, a_scale, B, b_scale, 3)
+    _whole(offsets, _I32, 1, "offsets", A.get_device())
     (rows, K), (E, N, _) = A.shape, B.shape
     if B.shape[2] != K or tuple(b_scale.shape) != (E, N) or offsets.shape[0] != E + 1:
         raise ValueError("B must be E x N x K, b_scale E x N and offsets E + 1")
     if src is not None:
-        _whole(src, torch.int32, 1, "src", A.get_device())
+        _whole(src, _I32, 1, "src", A.get_device())
     S = rows if src is None else src.shape[0]
     if K > 1 and B.stride(2) != 1 or N > 1 and B.stride(1) < K:
         raise ValueError("B must have a contiguous last dimension and rows that do not overlap")
