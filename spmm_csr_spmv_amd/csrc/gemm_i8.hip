@@ -7,6 +7,7 @@
 // K over instructions, waves and workgroups never changes a result; the float
 // of a sum is multiplied by a_scale, then by b_scale, and rounded once to C's type.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "rows.h"
@@ -118,77 +119,29 @@ __device__ __forceinline__ int64_t a_row(const GemmArgs& g, int64_t p) {
     return f >= 0 && r < g.a_rows ? r : -1;
 }
 
-// Bytes [k, k + 16) of a row of K bytes, zero from K on; p need not be aligned.
-__device__ __forceinline__ i32x4 load16(const int8_t* row, int64_t k, int64_t K) {
+// Rows that start anywhere (K >= 16): 16 bytes at min(k, K - 16), so that nothing
+// outside the row is read.  The last piece of a row that K cuts then begins
+// with bytes that the piece before holds too; low_mask zeroes them on A's
+// side (word d of the four, for a piece wanted at k), B's are multiplied by zero.
+__device__ __forceinline__ i32x4 load_any(const int8_t* row, int64_t k, int64_t K) {
+    return *reinterpret_cast<const i32x4_u*>(row + min(k, K - 16));
+}
+__device__ __forceinline__ int32_t low_mask(int64_t k, int64_t K, int d) {
+    const int64_t drop = k - (K - 16) - 4 * d;
+    return drop <= 0 ? -1 : drop >= 4 ? 0 : (int32_t)(0xffffffffu << (8 * (int)drop));
+}
+
+// The bytes of a row shorter than 16 from k on, zeros behind them.
+__device__ __forceinline__ i32x4 load_short(const int8_t* row, int64_t k, int64_t K) {
     i32x4 v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        v = *reinterpret_cast<const i32x4_u*>(row + k);
-    } else if (k < K) {
-        union {
-            i32x4 v;
-            int8_t b[16];
-        } u = {v};
-        for (int i = 0; i < 16; ++i)
-            if (k + i < K) u.b[i] = row[k + i];
-        v = u.v;
-    }
+    for (int i = 0; i < 16; ++i)
+        if (k + i < K) v[i >> 2] |= (int32_t)((uint32_t)(uint8_t)row[k + i] << (8 * (i & 3)));
     return v;
 }
 
 template <class D>
 __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
     return D::down((float)sum * sa * sb);
-}
-
-// Any size, alignment and stride: 64 x 64 tile, four waves of 32 x 32, K in
-// steps of 64 bytes through registers and LDS.
-template <class D>
-__global__ __launch_bounds__(256) void gemm_i8_plain(GemmArgs g) {
-    constexpr int BM = 64, BN = 64, BK = 64, LD = BK + 16;
-    __shared__ __attribute__((aligned(16))) int8_t la[BM * LD], lb[BN * LD];
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
-    const int row = tid >> 2, chunk = tid & 3;  // what this thread stages
-    const int wm = 32 * (w >> 1), wn = 32 * (w & 1);
-    const uint32_t tiles = g.m_tiles * g.n_tiles;
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        int e;
-        int64_t lo, hi;
-        if (!find_tile<BM>(g, t / g.n_tiles, l, e, lo, hi)) continue;
-        const int64_t n0 = (int64_t)(t % g.n_tiles) * BN;
-        const int64_t ar = lo + row < hi ? a_row(g, lo + row) : -1;
-        const int8_t* pa = g.A + max(ar, (int64_t)0) * g.lda;
-        const int8_t* pb = g.B + e * g.strideb + (n0 + row) * g.ldb;
-        const bool bok = n0 + row < g.N;
-        i32x16 acc;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0;
-        for (int64_t k0 = 0; k0 < g.K; k0 += BK) {
-            const int64_t k = k0 + 16 * chunk;
-            const i32x4 va = load16(pa, k, ar >= 0 ? g.K : 0), vb = load16(pb, k, bok ? g.K : 0);
-            __syncthreads();
-            *reinterpret_cast<i32x4*>(la + row * LD + 16 * chunk) = va;
-            *reinterpret_cast<i32x4*>(lb + row * LD + 16 * chunk) = vb;
-            __syncthreads();
-#pragma unroll
-            for (int ks = 0; ks < BK; ks += 32) {
-                const i32x4 a = *reinterpret_cast<const i32x4*>(la + (wm + (l & 31)) * LD + ks + 16 * (l >> 5));
-                const i32x4 b = *reinterpret_cast<const i32x4*>(lb + (wn + (l & 31)) * LD + ks + 16 * (l >> 5));
-                acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
-            }
-        }
-        // D layout of the 32 x 32 MFMA: lane l, register r -> row 8 (r/4) + 4 (l/32) + r%4, column l%32
-        const int64_t n = n0 + wn + (l & 31);
-        if (n < g.N) {
-            const float sb = g.b_scale[e * g.N + n];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t p = lo + wm + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3);
-                if (p >= hi) continue;
-                const int64_t ra = a_row(g, p);
-                if (ra >= 0) ((typename D::T*)g.C)[p * g.ldc + n] = scaled<D>(acc[r], g.a_scale[ra], sb);
-            }
-        }
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -313,28 +266,116 @@ __device__ __forceinline__ void big_barrier() {
     asm volatile("s_barrier" ::: "memory");
 }
 
+// Where a lane's copies read: rows kRows j + 8 w + l / 8 of the tile, chunk
+// (l % 8) ^ big_swizzle(row); the tile's rows of A and scales go to LDS.
+template <int WN, int F>
+struct BigRows {
+    const int8_t *a[4], *b[4];
+    int chunk;
+    __device__ __forceinline__ BigRows(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0, int32_t* lrow,
+                                       float* lscale, int tid, int w, int l) {
+        using S = BigShape<WN, F>;
+        const int crow = 8 * w + (l >> 3);
+        chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = S::kRows * j + crow;
+            const int64_t p = lo + row;
+            const int64_t r = j < S::kA && p < hi ? a_row(g, p) : -1;
+            a[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
+            if (j < S::kA && (l & 7) == 0) {
+                lrow[row] = (int32_t)r;
+                lscale[row] = g.a_scale[max(r, (int64_t)0)];
+            }
+            b[j] = g.B + e * g.strideb + min(n0 + row, g.N - 1) * g.ldb;
+        }
+        if (tid < 64 * WN) lscale[64 * WN + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
+    }
+};
+
+// The tile's sums scaled and stored; l0 .. l3 are LDS buffers of 64 WN x kBigK
+// bytes that nothing uses any more.
+template <class D, int WN, int F>
+__device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F][2], int8_t* l0, int8_t* l1, int8_t* l2,
+                                        int8_t* l3, const int32_t* lrow, const float* lscale, int64_t lo, int64_t n0,
+                                        int w, int l) {
+    typedef typename D::T T;
+    const int wm = w & 1, wn = w >> 1;
+    // Sums of one 32-row block at a time through this wave's part of LDS, then 8
+    // consecutive columns a lane, 8 rows an instruction.  D layout of the 32 x 32
+    // MFMA: lane l, register r -> first operand's row 8 (r/4) + 4 (l/32) + r%4 (a
+    // column of C), second operand's row l%32 (a row of C).
+    constexpr int kSums = 32 * kBigRow, kPer = 64 * WN * kBigK / (4 * kSums);  // waves to a buffer
+    static_assert(4 * kPer >= 2 * WN, "the waves' sums fit the four buffers");
+    int8_t* const buffer = w / kPer == 0 ? l0 : w / kPer == 1 ? l1 : w / kPer == 2 ? l2 : l3;
+    int32_t* mine = reinterpret_cast<int32_t*>(buffer) + (w % kPer) * kSums;
+    constexpr int N = Chunk<T>::N;
+    const int64_t n = n0 + 64 * wn + 8 * (l & 7);
+    const bool inside = n0 + 64 * WN <= g.N;  // the whole tile's columns
+    float sb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sb[i] = lscale[64 * WN + 64 * wn + 8 * (l & 7) + i];
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 v = {acc[i][u][4 * q], acc[i][u][4 * q + 1], acc[i][u][4 * q + 2], acc[i][u][4 * q + 3]};
+                *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
+            }
+        __builtin_amdgcn_wave_barrier();
+        const auto row_out = [&](int r, float sa, i32x4 v0, i32x4 v1, int64_t tr, bool whole) {
+            T* c = (T*)g.C + (lo + tr) * g.ldc + n;
+            typename Chunk<T>::V o[8 / N];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
+#pragma unroll
+            for (int x = 0; x < 8 / N; ++x) {
+                if (whole)
+                    *reinterpret_cast<typename Chunk<T>::U*>(c + x * N) = o[x];
+                else if (n + x * N < g.N)
+                    chunk_store(c + x * N, g.N - n - x * N, o[x]);
+            }
+        };
+        const int32_t* at = mine + (l >> 3) * kBigRow + 8 * (l & 7);
+        const int tr0 = 32 * (2 * i + wm) + (l >> 3);
+        if (inside) {
+            i32x4 v[4][2];
+            int r[4];
+            float sa[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[q][0] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
+                v[q][1] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
+                r[q] = lrow[tr0 + 8 * q];
+                sa[q] = lscale[tr0 + 8 * q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (r[q] >= 0) row_out(r[q], sa[q], v[q][0], v[q][1], tr0 + 8 * q, true);
+        } else {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 v0 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
+                const i32x4 v1 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
+                const int r = lrow[tr0 + 8 * q];
+                if (r >= 0) row_out(r, lscale[tr0 + 8 * q], v0, v1, tr0 + 8 * q, false);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <class D, int WN, int ST, int F>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
                                          const BigBuffers<ST>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
-    typedef typename D::T T;
-    const int wm = w & 1, wn = w >> 1;
     using S = BigShape<WN, F>;
-    // the rows this lane copies: kRows j + 8 w + l / 8, chunk (l % 8) ^ big_swizzle(row)
-    const int crow = 8 * w + (l >> 3), chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
-    const int8_t *pa[4], *pb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = S::kRows * j + crow;
-        const int64_t p = lo + row;
-        const int64_t r = j < S::kA && p < hi ? a_row(g, p) : -1;
-        pa[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
-        if (j < S::kA && (l & 7) == 0) {
-            lrow[row] = (int32_t)r;
-            lscale[row] = g.a_scale[max(r, (int64_t)0)];
-        }
-        pb[j] = g.B + e * g.strideb + min(n0 + row, g.N - 1) * g.ldb;
-    }
-    if (tid < 64 * WN) lscale[64 * WN + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
+    const int wm = w & 1, wn = w >> 1;
+    const BigRows<WN, F> rows(g, e, lo, hi, n0, lrow, lscale, tid, w, l);
+    const auto& pa = rows.a;
+    const auto& pb = rows.b;
+    const int chunk = rows.chunk;
     const int64_t last = (g.K - 1) & ~(int64_t)15;  // chunks behind it are read from there and masked
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
@@ -414,70 +455,20 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
 #undef SPX_AT
     __syncthreads();  // the copies behind the last step have landed too
 
-    // Sums of one 32-row block at a time through this wave's part of LDS, then 8
-    // consecutive columns a lane, 8 rows an instruction.  D layout of the 32 x 32
-    // MFMA: lane l, register r -> first operand's row 8 (r/4) + 4 (l/32) + r%4 (a
-    // column of C), second operand's row l%32 (a row of C).
-    constexpr int kSums = 32 * kBigRow, kPer = 64 * WN * kBigK / (4 * kSums);  // waves to a buffer
-    static_assert(4 * kPer >= 2 * WN, "the waves' sums fit the four buffers");
-    int8_t* const buffer = w / kPer == 0 ? m.b[0] : w / kPer == 1 ? m.b[1] : w / kPer == 2 ? m.a[0] : m.a[1];
-    int32_t* mine = reinterpret_cast<int32_t*>(buffer) + (w % kPer) * kSums;
-    constexpr int N = Chunk<T>::N;
-    const int64_t n = n0 + 64 * wn + 8 * (l & 7);
-    const bool inside = n0 + 64 * WN <= g.N;  // the whole tile's columns
-    float sb[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sb[i] = lscale[64 * WN + 64 * wn + 8 * (l & 7) + i];
-#pragma unroll
-    for (int i = 0; i < F; ++i) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const i32x4 v = {acc[i][u][4 * q], acc[i][u][4 * q + 1], acc[i][u][4 * q + 2], acc[i][u][4 * q + 3]};
-                *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
-            }
-        __builtin_amdgcn_wave_barrier();
-        const auto row_out = [&](int r, float sa, i32x4 v0, i32x4 v1, int64_t tr, bool whole) {
-            T* c = (T*)g.C + (lo + tr) * g.ldc + n;
-            typename Chunk<T>::V o[8 / N];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
-#pragma unroll
-            for (int x = 0; x < 8 / N; ++x) {
-                if (whole)
-                    *reinterpret_cast<typename Chunk<T>::U*>(c + x * N) = o[x];
-                else if (n + x * N < g.N)
-                    chunk_store(c + x * N, g.N - n - x * N, o[x]);
-            }
-        };
-        const int32_t* at = mine + (l >> 3) * kBigRow + 8 * (l & 7);
-        const int tr0 = 32 * (2 * i + wm) + (l >> 3);
-        if (inside) {
-            i32x4 v[4][2];
-            int r[4];
-            float sa[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v[q][0] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
-                v[q][1] = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
-                r[q] = lrow[tr0 + 8 * q];
-                sa[q] = lscale[tr0 + 8 * q];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (r[q] >= 0) row_out(r[q], sa[q], v[q][0], v[q][1], tr0 + 8 * q, true);
-        } else {
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                const i32x4 v0 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
-                const i32x4 v1 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
-                const int r = lrow[tr0 + 8 * q];
-                if (r >= 0) row_out(r, lscale[tr0 + 8 * q], v0, v1, tr0 + 8 * q, false);
-            }
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    big_out<D, WN, F>(g, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, lo, n0, w, l);
+}
+
+// Tile v of the m_tiles x n_tiles that there are: four row tiles to a column
+// tile, so that neighbours, which run on one XCD, share rows of A and of B in
+// its L2.  It is the tiles that there are, not those that the launch has room
+// for, that are dealt out to the XCDs: the last one would get the empty ones.
+template <int WN>
+__device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t v, uint32_t m_tiles, int lane, int& e, int64_t& lo,
+                                          int64_t& hi, int64_t& n0) {
+    const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
+    const uint32_t high = min(m_tiles - first, 4u);
+    n0 = (int64_t)(in / high) * (64 * WN);
+    return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
 }
 
 template <class D, int WN, int ST>
@@ -487,18 +478,12 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
     __shared__ int32_t lrow[64 * WN];       // row of A of every row of the tile, or -1
     __shared__ float lscale[2 * 64 * WN];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    // Neighbouring tiles on one XCD, four row tiles to a column tile.  The tiles
-    // that there are, not those that the launch has room for, are dealt out to
-    // the XCDs: the last one would get the empty ones.
     const uint32_t m_tiles = count_tiles<64 * WN>(g, l);
     if (blockIdx.x >= m_tiles * g.n_tiles) return;
     const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)(m_tiles * g.n_tiles));
-    const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
-    const uint32_t high = min(m_tiles - first, 4u);
-    const int64_t n0 = (int64_t)(in / high) * (64 * WN);
     int e;
-    int64_t lo, hi;
-    if (!find_tile<64 * WN>(g, first + in % high, l, e, lo, hi)) return;
+    int64_t lo, hi, n0;
+    if (!big_place<WN>(g, v, m_tiles, l, e, lo, hi, n0)) return;
     const int blocks = (int)((hi - lo + 63) >> 6);
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
@@ -517,6 +502,101 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
 }
 
 // ---------------------------------------------------------------------------
+// Rows of any alignment and length: the 128 x 128 tiles, with the copies
+// through registers (global_load_lds wants aligned pieces): the next step's
+// loads are in flight while this one is multiplied, and go to the other LDS
+// buffer after it.  A workgroup goes on to the next tile where there are more
+// than the launch has workgroups.
+template <class D, int F>
+__device__ __forceinline__ void staged_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
+                                            const BigBuffers<2>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
+    using S = BigShape<2, F>;
+    const int wm = w & 1, wn = w >> 1;
+    const BigRows<2, F> rows(g, e, lo, hi, n0, lrow, lscale, tid, w, l);
+    const int steps = (int)((g.K + kBigK - 1) / kBigK);
+    i32x4 v[S::kCopies];
+    const auto load = [&](int s) {
+        const int64_t k = (int64_t)s * kBigK + rows.chunk;
+        if (g.K >= 16) {
+#pragma unroll
+            for (int j = 0; j < S::kCopies; ++j) v[j] = load_any(j < S::kA ? rows.a[j & 3] : rows.b[(j - S::kA) & 3], k, g.K);
+        } else {
+#pragma unroll
+            for (int j = 0; j < S::kCopies; ++j)
+                v[j] = load_short(j < S::kA ? rows.a[j & 3] : rows.b[(j - S::kA) & 3], k, g.K);
+        }
+    };
+    const auto store = [&](int s) {
+        const int64_t k = (int64_t)s * kBigK + rows.chunk;
+        if (s == steps - 1 && g.K >= 16) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int32_t keep = low_mask(k, g.K, d);
+#pragma unroll
+                for (int j = 0; j < S::kA; ++j) v[j][d] &= keep;
+            }
+        }
+        int8_t* la = (s & 1 ? m.a[1] : m.a[0]) + w * 1024 + l * 16;
+        int8_t* lb = (s & 1 ? m.b[1] : m.b[0]) + w * 1024 + l * 16;
+#pragma unroll
+        for (int j = 0; j < S::kCopies; ++j)
+            *reinterpret_cast<i32x4*>(j < S::kA ? la + j * S::kRows * kBigK : lb + (j - S::kA) * S::kRows * kBigK) = v[j];
+    };
+
+    i32x16 acc[F][2];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][u][r] = 0;
+    if (steps > 0) {
+        load(0);
+        store(0);
+    }
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        const int8_t* la = s & 1 ? m.a[1] : m.a[0];
+        const int8_t* lb = s & 1 ? m.b[1] : m.b[0];
+        if (s + 1 < steps) load(s + 1);
+        BigOps<F> x0, x1;
+        x0.read(la, lb, 0, wm, wn, l);
+#pragma unroll
+        for (int ks = 0; ks < 4; ks += 2) {
+            x1.read(la, lb, ks + 1, wm, wn, l);
+            x0.multiply(acc);
+            if (ks == 0) x0.read(la, lb, 2, wm, wn, l);
+            x1.multiply(acc);
+        }
+        if (s + 1 < steps) store(s + 1);
+        __syncthreads();
+    }
+    big_out<D, 2, F>(g, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, lo, n0, w, l);
+}
+
+template <class D>
+__global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
+    constexpr int kBytes = 128 * kBigK;
+    __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
+    __shared__ int32_t lrow[128];
+    __shared__ float lscale[2 * 128];
+    const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    const uint32_t m_tiles = count_tiles<128>(g, l), total = m_tiles * g.n_tiles;
+    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+        const uint32_t v = total <= gridDim.x ? xcd_contiguous((int)t, 0, (int)total) : t;
+        int e;
+        int64_t lo, hi, n0;
+        if (!big_place<2>(g, v, m_tiles, l, e, lo, hi, n0)) continue;
+        __syncthreads();  // the tile before has been stored
+        if (hi - lo <= 64)
+            staged_tile<D, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        else
+            staged_tile<D, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Few rows: tiles of 16 R rows x 16 C columns, W waves that share the tile and
 // split K.
 //
@@ -525,31 +605,36 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
 // taking 128 bytes of every row in turn and reading its next 128 before it
 // multiplies; the rows of A come from L2 the same way.  The waves' int32 sums
 // meet in LDS, exact in any order.
-template <int R, int C>
+// ANY: rows of any alignment (K >= 16), read as load_any does.
+template <int R, int C, bool ANY>
 struct ThinOps {
+    typedef typename std::conditional<ANY, i32x4_u, i32x4>::type V;
     i32x4 a[2][R], b[2][C];
     __device__ __forceinline__ void read(const int8_t* const (&pa)[R], const int8_t* const (&pb)[C], int64_t k,
                                          int64_t last) {
         const int64_t k0 = min(k, last), k1 = min(k + 64, last);
 #pragma unroll
         for (int j = 0; j < C; ++j) {  // both halves of a 128-byte line, one after the other
-            b[0][j] = *reinterpret_cast<const i32x4*>(pb[j] + k0);
-            b[1][j] = *reinterpret_cast<const i32x4*>(pb[j] + k1);
+            b[0][j] = *reinterpret_cast<const V*>(pb[j] + k0);
+            b[1][j] = *reinterpret_cast<const V*>(pb[j] + k1);
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            a[0][j] = *reinterpret_cast<const i32x4*>(pa[j] + k0);
-            a[1][j] = *reinterpret_cast<const i32x4*>(pa[j] + k1);
+            a[0][j] = *reinterpret_cast<const V*>(pa[j] + k0);
+            a[1][j] = *reinterpret_cast<const V*>(pa[j] + k1);
         }
     }
-    // left: bytes of K from this lane's k on
-    __device__ __forceinline__ void mask(int64_t left) {
+    // zeroes what does not belong to the row from this lane's k on
+    __device__ __forceinline__ void mask(int64_t k, int64_t K) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                const int64_t keep = left - 64 * h - 4 * d;
-                const int32_t m = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * (int)keep)) - 1;
+                const int64_t keep = K - k - 64 * h - 4 * d;
+                const int32_t m = ANY         ? low_mask(k + 64 * h, K, d)
+                                  : keep >= 4 ? -1
+                                  : keep <= 0 ? 0
+                                              : (1 << (8 * (int)keep)) - 1;
 #pragma unroll
                 for (int j = 0; j < R; ++j) a[h][j][d] &= m;
             }
@@ -565,7 +650,7 @@ struct ThinOps {
     }
 };
 
-template <class D, int R, int C, int W>
+template <class D, int R, int C, int W, bool ANY>
 __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     typedef typename D::T T;
     constexpr int BM = 16 * R, BN = 16 * C, LD = BN + 4;
@@ -591,18 +676,18 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    const int64_t last = (g.K - 1) & ~(int64_t)15;
+    const int64_t last = ANY ? g.K - 16 : (g.K - 1) & ~(int64_t)15;
     const int lk = 16 * (l >> 4);
-    ThinOps<R, C> x, y;
+    ThinOps<R, C, ANY> x, y;
     int64_t k = 128 * w;
     x.read(pa, pb, k + lk, last);
     for (; k < g.K; k += 256 * W) {
         y.read(pa, pb, k + 128 * W + lk, last);
-        if (k + 128 > g.K) x.mask(g.K - k - lk);
+        if (k + 128 > g.K) x.mask(k + lk, g.K);
         x.multiply(acc);
         if (k + 128 * W >= g.K) break;
         x.read(pa, pb, k + 256 * W + lk, last);
-        if (k + 128 * W + 128 > g.K) y.mask(g.K - k - 128 * W - lk);
+        if (k + 128 * W + 128 > g.K) y.mask(k + 128 * W + lk, g.K);
         y.multiply(acc);
     }
     // D layout of the 16 x 16 MFMA: lane l, register r -> first operand's row 4 (l/16) + r (a column of C),
@@ -651,8 +736,8 @@ int64_t row_tiles(const GemmArgs& g, int64_t bm) {
 }
 int64_t tiles(const GemmArgs& g, int64_t bm, int64_t bn) { return row_tiles(g, bm) * ((g.N + bn - 1) / bn); }
 
-// Workgroups of a launch: the kernels for 16-byte rows take one tile each and
-// are not launched with more; the plain one goes on to the next.
+// Workgroups of a launch: all kernels but gemm_i8_staged take one tile each and
+// are not launched with more; that one goes on to the next.
 constexpr int64_t kMostTiles = 1 << 22;
 
 template <class K>
@@ -665,38 +750,43 @@ int launch(K kernel, GemmArgs g, int64_t bm, int64_t bn, int threads, hipStream_
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 
+template <class D, int R, int C, int W>
+int launch_thin(bool any, const GemmArgs& g, hipStream_t s) {
+    return any ? launch(gemm_i8_thin<D, R, C, W, true>, g, 16 * R, 16 * C, 64 * W, s)
+               : launch(gemm_i8_thin<D, R, C, W, false>, g, 16 * R, 16 * C, 64 * W, s);
+}
+
 // Which kernel.  Times are M x N x K, or tokens x choices, experts, K, N with
 // the weights read from memory each time, in us.
 template <class D>
 int gemm_t(GemmArgs g, hipStream_t s) {
     if (g.a_rows == 0) return SP_OK;  // no row of C has a row of A
     const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
-    // Rows that no 16-byte access fits: through registers, 1.5 to 8 times the
-    // others' time (8192 x 8192 x 4096: 646 against 254).
-    if (g.K == 0 || !aligned16(g) || tiles(g, 256, 256) > kMostTiles)
-        return launch(gemm_i8_plain<D>, g, 64, 64, 256, s);
+    const int64_t mid = tiles(g, 128, 128);
+    const bool any = !aligned16(g);
+    if (g.K < 16 || mid > kMostTiles) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     // Few tiles: the smallest ones, or most CUs stay idle.  A step up where 128
     // or 256 tiles are reached: 1 x 4096 x 4096 16x16 6.7, 16x32 8.5;
     // 8 x 8192 x 4096 16x16 11.8, 16x32 11.0; 32 x 4096 x 4096 16x32 10.1,
     // 32x32 11.9; 64 x 4096 x 4096 16x32 15.8, 32x32 12.1, 32x64 16.3;
     // 128 x 4096 x 4096 32x32 19.8, 32x64 16.7, 128x128 23.7;
     // 256 x 4096 x 4096 32x64 28.8, 128x128 23.1.
-    if (tiles(g, 16, 32) <= 128) return launch(gemm_i8_thin<D, 1, 1, 8>, g, 16, 16, 512, s);
+    if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(any, g, s);
     // Few rows a matrix (up to 16 of a single one, 8 on the average of several,
     // where some have more): 32 x 8, 64, 4096, 2048 16x32 91, 32x64 101, 128x128 128.
     const bool few = tiles(g, 16, 32) <= kMostTiles;
     if (tiles(g, 16, 32) <= 256 || (few && g.S <= (groups == 1 ? 16 : 8) * groups))
-        return launch(gemm_i8_thin<D, 1, 2, 4>, g, 16, 32, 256, s);
-    if (tiles(g, 32, 32) <= 256) return launch(gemm_i8_thin<D, 2, 2, 4>, g, 32, 32, 256, s);
+        return launch_thin<D, 1, 2, 4>(any, g, s);
+    if (tiles(g, 32, 32) <= 256) return launch_thin<D, 2, 2, 4>(any, g, s);
     // 96 x 8, 64, 4096, 2048 (12 rows an expert) 32x64 120, 128x128 131; 128 x 8 (16 rows) 127, 129;
     // 64 x 2, 8, 4096, 14336 (16 rows) 135, 118.
     if (tiles(g, 32, 64) <= 256 || (few && g.S <= 12 * groups))
-        return launch(gemm_i8_thin<D, 2, 4, 4>, g, 32, 64, 256, s);
+        return launch_thin<D, 2, 4, 4>(any, g, s);
     // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
     // for memory: four steps in LDS.  1024 x 4096 x 4096 28 against 36 with two
     // steps and two workgroups a CU, and 55 with 256 x 256 tiles;
     // 256 x 8, 64, 4096, 2048 (32 rows) 133, 157, 166.
-    const int64_t mid = tiles(g, 128, 128);
+    if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     if (mid <= 256 || (few && g.S < 48 * groups))
         return launch(gemm_i8_big<D, 2, 4>, g, 128, 128, 256, s);
     // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 48, with four steps 53,
