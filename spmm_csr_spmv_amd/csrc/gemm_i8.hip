@@ -774,9 +774,12 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     //
     // Few rows a matrix (up to 16 of a single one, 8 on the average of several,
     // where some have more) take the 16-row tiles in any number: 32 x 8, 64,
-    // 4096, 2048 16x32 91, 32x64 101, 128x128 128; with 9 to 12 rows on the
-    // average the 32-row ones: 96 x 8, 64, 4096, 2048 32x64 120, 128x128 131;
+    // 4096, 2048 16x32 91, 32x64 101, 128x128 117; with 9 to 12 rows on the
+    // average the 32-row ones: 96 x 8, 64, 4096, 2048 32x64 120, 128x128 134;
     // 128 x 8 (16 rows) 127, 129; 64 x 2, 8, 4096, 14336 (16 rows) 135, 118.
+    // Short sums do not pay their four waves: 128 x 8, 128, 2048, 2048 (8 rows)
+    // 16x32 124, 128x128 103; 64 x 8, 128, 1024, 2048 (4 rows) 68, 63; but
+    // 64 x 8, 64, 4096, 1024 (8 rows) 60, 63.
     //
     // Rows that are not aligned lose most there (an operand load of sixteen
     // unaligned pieces): with K one less, 32 x 8, 64, 4095, 2048 16x32 268,
@@ -784,26 +787,25 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     // 64 x 4096 x 4095 32x32 24, staged 33; 256 x 4096 x 4097 32x64 71, staged 36.
     const bool few = !any && tiles(g, 16, 32) <= kMostTiles;
     if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(any, g, s);
-    if (tiles(g, 16, 32) <= 256 || (few && g.S <= (groups == 1 ? 16 : 8) * groups))
+    const bool deep = few && g.K > 2048;
+    if (tiles(g, 16, 32) <= 256 || (few && groups == 1 && g.S <= 16) || (deep && g.S <= 8 * groups))
         return launch_thin<D, 1, 2, 4>(any, g, s);
     if (tiles(g, 32, 32) <= 256) return launch_thin<D, 2, 2, 4>(any, g, s);
-    if (tiles(g, 32, 64) <= 256 || (few && g.S <= 12 * groups)) return launch_thin<D, 2, 4, 4>(any, g, s);
+    if (tiles(g, 32, 64) <= 256 || (deep && g.S <= 12 * groups)) return launch_thin<D, 2, 4, 4>(any, g, s);
     // 8192 x 8192 x 4095 403, with aligned rows 262.
     if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
     // for memory: four steps in LDS.  1024 x 4096 x 4096 26 against 36 with two
     // steps and two workgroups a CU, and 55 with 256 x 256 tiles;
-    // 256 x 8, 64, 4096, 2048 (32 rows) 133, 157, 166.
-    if (mid <= 256 || (few && g.S < 48 * groups)) return launch(gemm_i8_big<D, 2, 4>, g, 128, 128, 256, s);
+    // 256 x 8, 64, 4096, 2048 (32 rows) 133, 162, 166; 512 x 8 (64 rows) 144, 157, 171.
+    if (mid <= 256 || (few && g.S < 96 * groups)) return launch(gemm_i8_big<D, 2, 4>, g, 128, 128, 256, s);
     // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 46, with four steps 53,
-    // with 256 x 256 tiles 57; 512 x 8, 64, 4096, 2048 (64 rows) 157, 152, 171;
-    // 1024 x 8, 128, 2048, 1536 (64 rows) 130, 138, 124.  Also where 256-wide tiles
-    // would be empty for a fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
+    // with 256 x 256 tiles 57.  Also where 256-wide tiles would be empty for a
+    // fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
     const int64_t wide = (g.N + 255) / 256 * 256, narrow = (g.N + 127) / 128 * 128;
-    if (mid <= 512 || (few && (g.S < 96 * groups || 5 * wide >= 6 * narrow)))
-        return launch(gemm_i8_big<D, 2, 2>, g, 128, 128, 256, s);
+    if (mid <= 512 || (few && 5 * wide >= 6 * narrow)) return launch(gemm_i8_big<D, 2, 2>, g, 128, 128, 256, s);
     // 8192 x 8192 x 4096 251 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
-    // 71, 89; 4096 x 8, 64, 4096, 2048 (512 rows) 358, 420; 1024 x 8 (128 rows) 183, 195.
+    // 71, 89; 4096 x 8, 64, 4096, 2048 (512 rows) 335, 425; 1024 x 8 (128 rows) 183, 195.
     return launch(gemm_i8_big<D, 4, 2>, g, 256, 256, 512, s);
 }
 

@@ -397,7 +397,10 @@ EXPERTS = [(1, 1, 1, 16, 16, 0, "random", True), (1, 8, 64, 130, 256, 0, "random
            # the same for the experts: few rows each, 8 to 12, up to 48, up to 96, many
            (60, 4, 32, 700, 272, 0.1, "random", True), (50, 7, 32, 600, 272, 0, "skew", True),
            (100, 8, 32, 600, 144, 0.05, "random", True), (300, 8, 30, 1100, 300, 0.1, "skew", True),
-           (2600, 2, 4, 1700, 130, 0.05, "random", True), (5300, 1, 3, 1800, 272, 0, "skew", False)]
+           (2600, 2, 4, 1700, 130, 0.05, "random", True), (5300, 1, 3, 1800, 272, 0, "skew", False),
+           # long sums with few rows each
+           (60, 4, 32, 300, 2064, 0.1, "random", True), (100, 3, 30, 310, 2200, 0.1, "skew", True),
+           (9, 2, 4, 1000, 4097, 0, "random", True)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
