@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "moe.h"
 #include "rows.h"
 
 namespace spx {

@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "device_common.h"
+#include "moe.h"
 #include "rows.h"
 
 namespace spx {

@@ -1,6 +1,6 @@
 // extern "C" entry points of the mixture-of-experts operators: argument
 // checks, then the launch.  None of them allocates or synchronises.
-#include "internal.h"
+#include "moe.h"
 #include "spmm_csr_spmv.h"
 
 namespace {
