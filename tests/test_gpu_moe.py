@@ -100,13 +100,28 @@ def test_sort_of_sorted_and_reversed_ids():
             np.testing.assert_array_equal(i64(g), r)
 
 
+def test_sort_with_a_workspace_and_other_shapes():
+    rng = rng_for("workspace")
+    for shape in ((9000,), (3000, 3), (30, 20, 15), ()):
+        ids = rng.integers(-1, 20, shape).astype(np.int32)
+        work = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        got = sp.moe_sort(dev(ids).reshape(shape), 20, work=work)
+        for g, r in zip(got, sort_ref(ids, 20)):
+            np.testing.assert_array_equal(i64(g), r)
+    with pytest.raises(sp.SparseError) as e:
+        sp.moe_sort(dev(rng.integers(0, 20, 9000).astype(np.int32)), 20, work=work[:100])
+    assert e.value.code == 4
+
+
 # ------------------------------------------------------------------ rows
 # T, slots, E, H, share routed nowhere, kind
 MOVES = [(1, 1, 1, 1, 0, "random"), (1, 8, 64, 4096, 0, "random"), (3, 2, 4, 7, 0, "random"),
          (5, 3, 2, 8, 0.4, "random"), (9, 4, 16, 9, 0, "random"), (17, 8, 8, 64, 0.2, "random"),
          (33, 5, 11, 257, 0.2, "random"), (40, 9, 12, 130, 0.1, "random"), (64, 17, 3, 100, 0.1, "skew"),
          (21, 6, 7, 2045, 0.3, "random"), (300, 2, 8, 1001, 0.1, "skew"), (30, 2, 8, 8200, 0, "random"),
-         (6, 2, 5, 33, 0, "none"), (1030, 1, 5, 72, 0.5, "random"), (4, 2, 3, 0, 0, "random")]
+         (6, 2, 5, 33, 0, "none"), (1030, 1, 5, 72, 0.5, "random"), (4, 2, 3, 0, 0, "random"),
+         # whole lines by 64 lanes a token, and whole rows a workgroup (2048 tokens and more)
+         (40, 3, 5, 320, 0.1, "random"), (33, 2, 5, 512, 0, "random"), (2050, 2, 4, 2176, 0.1, "random")]
 LAYOUTS = [(0, 0), (3, 1), (8, 0), (13, 5)]  # gap between rows, first element's offset
 
 
@@ -223,6 +238,23 @@ def test_gradients_against_differences():
             b[i, j] -= step
             slope = (f(a) - f(b)) / float(a[i, j].double() - b[i, j].double())
             assert abs(slope - float(grad[i, j])) <= noise, (slope, float(grad[i, j]))
+
+
+def test_fewer_places_than_slots():
+    """S below T * slots: what was sorted behind it is dropped, as a capacity over all experts would."""
+    rng = rng_for("capacity")
+    T, k, E, H, S = 50, 4, 6, 40, 120
+    _, src, pos = sort_ref(route(rng, T, k, E), E)
+    dpos = dev(pos.astype(np.int32))
+    X = rows_tensor(rng, T, H, "f32")
+    Xs = sp.moe_dispatch(X, dpos, S=S)
+    np.testing.assert_array_equal(f64(Xs), f64(X)[src[:S] // k])
+    dweights = torch.full((T, k), 9.0, device="cuda")
+    dYs, dw = sp.moe_combine_backward(X, Xs, dpos, torch.ones(T, k, device="cuda"), dweights=dweights)
+    assert dw is dweights
+    np.testing.assert_array_equal(f64(dYs), f64(X)[src[:S] // k])
+    norm = (f64(X) ** 2).sum(-1, keepdims=True)
+    assert (np.abs(f64(dw) - np.where(pos < S, norm, 0)) <= (H + 1) * U * norm).all()
 
 
 def test_places_out_of_range_are_skipped():
@@ -385,6 +417,89 @@ def test_product_of_extreme_codes():
     for gap in (0, 1):  # rows 16-byte aligned and not
         got = sp.gemm_i8(strided(A, gap), dev(one[:20]), strided(B, gap), dev(one[:33]), dtype=torch.float32)
         product_close(got, A.astype(np.float64) @ B.astype(np.float64).T, one[:20], one[:33], "f32")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 70, 64), (40, 70, 160), (300, 400, 128), (600, 1100, 48)])
+def test_product_of_unaligned_buffers(M, N, K):
+    """Row distances of whole 16 bytes, first elements off by one: each operand alone, then both."""
+    rng = rng_for("unaligned", M)
+    A, B = codes(rng, M, K), codes(rng, N, K)
+    sa, sb = np.ones(M, np.float32), np.ones(N, np.float32)
+    want = A.astype(np.float64) @ B.astype(np.float64).T
+    for a, b in ((0, 1), (1, 0), (1, 1)):
+        got = sp.gemm_i8(strided(A, 0, a), dev(sa), strided(B, 0, b), dev(sb), dtype=torch.float32)
+        np.testing.assert_array_equal(f64(got), want)  # sums below 2^24
+
+
+def test_scales_travel():
+    """A NaN scale makes its row NaN, an infinite one infinite (NaN where the sum is 0), a zero one zero, and no other."""
+    rng = rng_for("scales")
+    for M in (5, 150):
+        A, B = codes(rng, M, 64), codes(rng, 70, 64)
+        B[3] = 0
+        sa = np.ones(M, np.float32)
+        sa[1], sa[2], sa[3] = np.nan, np.inf, 0
+        sums = A.astype(np.float64) @ B.astype(np.float64).T
+        got = f64(sp.gemm_i8(dev(A), dev(sa), dev(B), dev(np.ones(70, np.float32)), dtype=torch.float32))
+        assert np.isnan(got[1]).all() and (got[3] == 0).all() and np.isnan(got[2, 3])
+        np.testing.assert_array_equal(got[2][sums[2] != 0], np.sign(sums[2][sums[2] != 0]) * np.inf)
+        rest = [0] + list(range(4, M))
+        np.testing.assert_array_equal(got[rest], sums[rest])
+
+
+def test_empty_products():
+    z8, z = torch.zeros(0, 32, dtype=torch.int8, device="cuda"), torch.zeros(0, device="cuda")
+    a8, a = torch.ones(4, 32, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    assert sp.gemm_i8(z8, z, a8, a).shape == (0, 4) and sp.gemm_i8(a8, a, z8, z).shape == (4, 0)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    b8, b = torch.ones(2, 4, 32, dtype=torch.int8, device="cuda"), torch.ones(2, 4, device="cuda")
+    assert sp.moe_gemm_i8(z8, z, b8, b, off).shape == (0, 4)
+    src = torch.full((6,), -1, dtype=torch.int32, device="cuda")
+    out = torch.full((6, 4), 5.0, device="cuda")
+    sp.moe_gemm_i8(z8, z, b8, b, off + 6, src=src, slots=2, out=out)  # rows to fill, but A has none
+    assert (out == 5).all()
+    q, s = sp.quantize_rows_i8(torch.zeros(0, 7, device="cuda"))
+    assert q.shape == (0, 7) and s.shape == (0,)
+
+
+def test_beyond_32_bits():
+    """Outputs and operands of more than 2^31 elements, and of more than 4 GB."""
+    say("beyond 32 bits")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, N, K = 70000, 40000, 32  # 5.6 GB of bf16
+    A = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    B = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones(M, device="cuda")
+    C = sp.gemm_i8(A, one, B, one[:N])
+    rows = torch.tensor([0, 1, 53686, 53688, 69998, 69999], device="cuda")
+    want = (A[rows].double() @ B.double().t()).to(torch.bfloat16)  # exact sums, one rounding
+    assert torch.equal(C[rows], want)
+    # the same values as rows to quantise, and as sorted rows of 80000 elements
+    q, s = sp.quantize_rows_i8(C)
+    x = C[rows].double()
+    top = x.abs().amax(1)
+    assert torch.equal(q[rows], torch.round(127 * x / top[:, None]).to(torch.int8))
+    assert torch.equal(s[rows], (top.float() / 127))
+    Ys = C.view(M // 2, 2 * N)
+    pos = torch.randperm(M // 2, generator=g, device="cuda").to(torch.int32).view(-1, 2)
+    w = torch.rand(pos.shape, generator=g, device="cuda")
+    Y = sp.moe_combine(Ys, pos, w)
+    t = torch.tensor([0, 9000, M // 4 - 1], device="cuda")
+    terms = w[t].double().unsqueeze(-1) * Ys[pos[t].long()].double()
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    assert ((Y[t].double() - ref).abs() <= (2.0 ** -8) * (ref.abs() + 3 * U * mag) + 3 * U * mag).all()
+    back = sp.moe_dispatch(Y, pos, out=Ys)  # over the rows they came from
+    assert torch.equal(back[pos[t].long()], Y[t].unsqueeze(1).expand(-1, 2, -1))
+    del C, q, Ys, Y, back, terms
+    # 4.8 GB of expert weights
+    E, F, H = 24, 8192, 24576
+    W = torch.randint(-127, 128, (E, F, H), generator=g, device="cuda", dtype=torch.int8)
+    X = torch.randint(-127, 128, (48, H), generator=g, device="cuda", dtype=torch.int8)
+    off = torch.arange(0, 49, 2, device="cuda", dtype=torch.int32)
+    out = sp.moe_gemm_i8(X, one[:48], W, torch.ones(E, F, device="cuda"), off, dtype=torch.float32)
+    for e in (0, 10, 11, E - 1):
+        want = X[2 * e:2 * e + 2].double() @ W[e].double().t()
+        assert ((out[2 * e:2 * e + 2].double() - want).abs() <= 3.001 * U * want.abs()).all()
 
 
 # T, slots, E, N, K, share routed nowhere, kind, gathered
