@@ -612,14 +612,16 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  * the tokens' rows, and no dispatched copy of them is needed).  C is S x N.
  * A row of C behind offsets[num_experts], or whose r is outside [0, a_rows),
  * keeps its contents.  Offsets are read on the device and not validated: they
- * are clamped to [0, S], a descending pair is an empty expert, and rows that
- * two experts claim are unspecified.
+ * are clamped to [0, S] and a descending pair is an empty expert; where ranges
+ * overlap, the contents of all rows of C are unspecified (nothing outside the
+ * operands is read and nothing outside C written).
  *
  * Alignment: none needed for A and B (C and the scales: the element's).  When
- * A, B, lda, ldb (and strideb) are multiples of 16 bytes the fast kernels
- * run; they read the rows in 16-byte pieces, so that up to 15 bytes behind a
- * row's last (K rounded up to 16) are read and ignored, also behind the last
- * row: within its 16-byte piece, never past it.
+ * A, B, lda, ldb (and strideb) are multiples of 16 bytes the kernels for
+ * aligned rows run, up to three times as fast; they read the rows in 16-byte
+ * pieces, so that up to 15 bytes behind a row's last (K rounded up to 16) are
+ * read and ignored, also behind the last row: within its 16-byte piece, never
+ * past it.  Other rows are read exactly.
  * None of these calls allocates or synchronises; all are deterministic.
  * Errors: SP_ERR_NULL, SP_ERR_SIZE, SP_ERR_UNSUPPORTED (types, K, num_experts,
  * alignment), SP_ERR_HIP.

@@ -27,6 +27,10 @@ constexpr int kSortThreads = 1024;   // 512 above kSortWideE experts, whose coun
 constexpr int kSortWideE = 512;
 constexpr int kSortOneBlock = 4096;  // up to this many slots one workgroup does everything (6.9 us; two kernels 8.4)
 
+// The floor is bytes that take a microsecond; what the sort takes is its chain
+// of dependent steps: 3.7 us for one token's 8 slots, 3.0 (counts) + 10.2
+// (placement) for 524288 slots over 128 experts.
+//
 // Workgroups of the two-kernel path: 1024 slots each up to 128 of them (16384
 // slots 8.6 us, 9.5 with 4096 each), then up to 256 (524288 slots 12.9 us with
 // 128, 13.5 with 256).  Every workgroup of the second kernel reads all counts,
@@ -206,6 +210,10 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
 // flight together.  A slot routed nowhere is made to read the first row (there
 // is one, or no row is live) and its bits are zeroed, so that the loads need
 // no branch; its weight counts as zero.
+//
+// Memory bounds all three: 16384 x 4 rows of 4096 bf16 dispatched in 122 us
+// (5.5 TB/s, four fifths writes), combined in 112 (6.0), their gradients formed
+// in 219 (5.5); a copy reaches 5.6 TB/s.
 //
 // A row's last chunk starts at H - N where a whole one does not fit: it then
 // repeats elements of the chunk before it, which are written twice with the
