@@ -64,27 +64,28 @@ def _rows(t, name):
     """Row distance of a 2-D tensor with contiguous, disjoint rows."""
     rows, cols = t.shape
     ld, step = t.stride()
+    if step == 1 and ld >= cols > 0:
+        return ld
     if cols > 1 and step != 1 or rows > 1 and ld < cols:
         raise ValueError("%s must have a contiguous last dimension and rows that do not overlap" % name)
     return max(ld, cols, 1)
 
 
-def _span(t):
-    """First byte and the one behind the last (row gaps count as used)."""
-    n = t.numel()
-    if n and not t.is_contiguous():
-        n = sum((s - 1) * d for s, d in zip(t.shape, t.stride())) + 1
-    p = t.data_ptr()
-    return p, p + n * t.element_size()
+def _reach(t):
+    """Bytes from a tensor's first element to behind its last (row gaps count as used)."""
+    if t.is_contiguous():
+        return t.nbytes
+    return (sum((n - 1) * d for n, d in zip(t.shape, t.stride())) + 1) * t.element_size() if t.numel() else 0
 
 
 def _apart(out, name, *inputs):
     """Refuses an output whose bytes overlap an input's."""
-    lo, hi = _span(out)
+    lo = out.data_ptr()
+    hi = lo + _reach(out)
     for t in inputs:
         if t is not None:
-            b, e = _span(t)
-            if b < hi and lo < e:
+            b = t.data_ptr()
+            if b < hi and lo < b + _reach(t):
                 raise ValueError("%s overlaps an input" % name)
 
 
@@ -123,16 +124,19 @@ def moe_sort(ids, num_experts, work=None, stream=None):
 
 
 def _sort(raw, ids, n, num_experts, need, work):
-    offsets = torch.empty(num_experts + 1, dtype=_I32, device=ids.device)
-    src = torch.empty(n, dtype=_I32, device=ids.device)
-    pos = torch.empty(ids.shape, dtype=_I32, device=ids.device)
+    device = ids.device
+    offsets = torch.empty(num_experts + 1, dtype=_I32, device=device)
+    src = torch.empty(n, dtype=_I32, device=device)
+    pos = torch.empty(ids.shape, dtype=_I32, device=device)
     if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-    elif work.device != ids.device or not work.is_contiguous():
-        raise ValueError("work must be a contiguous tensor on %s" % ids.device)
-    nbytes = work.numel() * work.element_size() if work is not None else 0
-    _check("moe_sort", lib().moe_sort(n, num_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(),
-                                      pos.data_ptr(), work.data_ptr() if nbytes else None, nbytes, raw))
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif work.device != device or not work.is_contiguous():
+        raise ValueError("work must be a contiguous tensor on %s" % device)
+    nbytes = 0 if work is None else work.nbytes
+    rc = lib().moe_sort(n, num_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(), pos.data_ptr(),
+                        work.data_ptr() if nbytes else None, nbytes, raw)
+    if rc != SP_OK:
+        raise SparseError("moe_sort", rc, lib())
     return offsets, src, pos
 
 
@@ -156,13 +160,17 @@ def _dispatch(raw, code, X, pos, T, slots, S, out):
     H = X.shape[1]
     if out is None:
         out = torch.empty(T * slots if S is None else int(S), H, dtype=X.dtype, device=X.device)
+        ld_out = H
     else:
         _want(out, X.dtype, 2, "out", X.get_device())
         if out.shape[1] != H or (S is not None and out.shape[0] != S):
             raise ValueError("out must be S x H")
         _apart(out, "out", X, pos)
-    _check("moe_dispatch", lib().moe_dispatch(T, slots, H, out.shape[0], code, X.data_ptr(),
-                                              _rows(X, "X"), pos.data_ptr(), out.data_ptr(), _rows(out, "out"), raw))
+        ld_out = _rows(out, "out")
+    rc = lib().moe_dispatch(T, slots, H, out.shape[0], code, X.data_ptr(), _rows(X, "X"), pos.data_ptr(),
+                            out.data_ptr(), ld_out, raw)
+    if rc != SP_OK:
+        raise SparseError("moe_dispatch", rc, lib())
     return out
 
 
@@ -188,14 +196,17 @@ def _combine(raw, code, Ys, pos, weights, out):
         raise ValueError("pos must be T x slots, slots at least 1")
     if out is None:
         out = torch.empty(T, H, dtype=Ys.dtype, device=Ys.device)
+        ld_out = H
     else:
         _want(out, Ys.dtype, 2, "out", Ys.get_device())
         if tuple(out.shape) != (T, H):
             raise ValueError("out must be T x H")
         _apart(out, "out", Ys, pos, weights)
-    _check("moe_combine", lib().moe_combine(T, slots, H, S, code, Ys.data_ptr(), _rows(Ys, "Ys"), pos.data_ptr(),
-                                            weights.data_ptr() if weights is not None else None, out.data_ptr(),
-                                            _rows(out, "out"), raw))
+        ld_out = _rows(out, "out")
+    rc = lib().moe_combine(T, slots, H, S, code, Ys.data_ptr(), _rows(Ys, "Ys"), pos.data_ptr(),
+                           None if weights is None else weights.data_ptr(), out.data_ptr(), ld_out, raw)
+    if rc != SP_OK:
+        raise SparseError("moe_combine", rc, lib())
     return out
 
 
