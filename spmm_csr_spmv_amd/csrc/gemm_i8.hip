@@ -616,23 +616,27 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
 // (R = 1, C = 2, W = 4): 90 us, 5.9 TB/s of weights where reads alone reach
 // 7.0.  Loads are cached: both halves of a line are used, one after the other
 // (non-temporal ones fetch it twice, 118 us).
-// ANY: rows of any alignment (K >= 16), read as load_any does.
-template <int R, int C, bool ANY>
+template <int R, int C>
 struct ThinOps {
-    typedef typename std::conditional<ANY, i32x4_u, i32x4>::type V;
+    static constexpr int kA = R, kB = C;                // loads for the rows of A and of B
+    static constexpr int kLds = 0;
     i32x4 a[2][R], b[2][C];
-    __device__ __forceinline__ void read(const int8_t* const (&pa)[R], const int8_t* const (&pb)[C], int64_t k,
+    static __device__ __forceinline__ int row(int j, int l) { return 16 * j + (l & 15); }
+    static __device__ __forceinline__ int offset(int l) { return 16 * (l >> 4); }
+    // a piece that K cuts is read whole: 16 aligned bytes
+    static __device__ __forceinline__ int64_t last(int64_t K) { return (K - 1) & ~(int64_t)15; }
+    __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* const (&pb)[kB], int64_t k,
                                          int64_t last) {
         const int64_t k0 = min(k, last), k1 = min(k + 64, last);
 #pragma unroll
         for (int j = 0; j < C; ++j) {  // both halves of a 128-byte line, one after the other
-            b[0][j] = *reinterpret_cast<const V*>(pb[j] + k0);
-            b[1][j] = *reinterpret_cast<const V*>(pb[j] + k1);
+            b[0][j] = *reinterpret_cast<const i32x4*>(pb[j] + k0);
+            b[1][j] = *reinterpret_cast<const i32x4*>(pb[j] + k1);
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            a[0][j] = *reinterpret_cast<const V*>(pa[j] + k0);
-            a[1][j] = *reinterpret_cast<const V*>(pa[j] + k1);
+            a[0][j] = *reinterpret_cast<const i32x4*>(pa[j] + k0);
+            a[1][j] = *reinterpret_cast<const i32x4*>(pa[j] + k1);
         }
     }
     // zeroes what does not belong to the row from this lane's k on
@@ -642,15 +646,12 @@ struct ThinOps {
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const int64_t keep = K - k - 64 * h - 4 * d;
-                const int32_t m = ANY         ? low_mask(k + 64 * h, K, d)
-                                  : keep >= 4 ? -1
-                                  : keep <= 0 ? 0
-                                              : (1 << (8 * (int)keep)) - 1;
+                const int32_t m = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * (int)keep)) - 1;
 #pragma unroll
                 for (int j = 0; j < R; ++j) a[h][j][d] &= m;
             }
     }
-    __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C]) const {
+    __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C], int8_t*, int) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -661,11 +662,68 @@ struct ThinOps {
     }
 };
 
+// The same for rows of any alignment (K >= 16, read as load_any does).  Eight
+// lanes read 128 bytes of a row, and the operands are put together through LDS
+// that only this wave uses: an unaligned load of sixteen pieces in sixteen
+// rows takes three times as long (32 x 8, 64 experts, 4095 x 2048 268 us so,
+// AAA us with whole pieces).
+template <int R, int C>
+struct ThinAny {
+    static constexpr int kA = 2 * R, kB = 2 * C;
+    static constexpr int kLds = 16 * (R + C) * kBigK;
+    i32x4 v[kA + kB];
+    static __device__ __forceinline__ int row(int j, int l) { return 8 * j + (l >> 3); }
+    static __device__ __forceinline__ int offset(int l) { return 16 * (l & 7); }
+    static __device__ __forceinline__ int64_t last(int64_t K) { return K - 16; }
+    __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* const (&pb)[kB], int64_t k,
+                                         int64_t last) {
+        const int64_t at = min(k, last);
+#pragma unroll
+        for (int j = 0; j < kB; ++j) v[kA + j] = *reinterpret_cast<const i32x4_u*>(pb[j] + at);
+#pragma unroll
+        for (int j = 0; j < kA; ++j) v[j] = *reinterpret_cast<const i32x4_u*>(pa[j] + at);
+    }
+    __device__ __forceinline__ void mask(int64_t k, int64_t K) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int32_t m = low_mask(k, K, d);
+#pragma unroll
+            for (int j = 0; j < kA; ++j) v[j][d] &= m;
+        }
+    }
+    // A wave's LDS operations are done in order: no wait between them.
+    __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C], int8_t* lds, int l) const {
+#pragma unroll
+        for (int j = 0; j < kA + kB; ++j) {
+            const int r = 8 * j + (l >> 3);
+            *reinterpret_cast<i32x4*>(lds + r * kBigK + (((l & 7) ^ big_swizzle(r)) << 4)) = v[j];
+        }
+        i32x4 x[2][R + C];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < R + C; ++j) {
+                const int r = 16 * j + (l & 15);
+                x[h][j] = *reinterpret_cast<const i32x4*>(lds + r * kBigK + (((4 * h + (l >> 4)) ^ big_swizzle(r)) << 4));
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[h][R + j], x[h][i], acc[i][j], 0, 0, 0);
+    }
+};
+
 template <class D, int R, int C, int W, bool ANY>
 __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     typedef typename D::T T;
+    typedef typename std::conditional<ANY, ThinAny<R, C>, ThinOps<R, C>>::type Ops;
     constexpr int BM = 16 * R, BN = 16 * C, LD = BN + 4;
-    __shared__ __attribute__((aligned(16))) int32_t part[W * BM * LD];
+    constexpr int kSums = BM * LD * 4, kWave = Ops::kLds > kSums ? Ops::kLds : kSums;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[W * kWave];
+    int32_t* part = reinterpret_cast<int32_t*>(lds);
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     // the row tiles of one column tile follow each other: those of one expert meet its rows of B in one L2
     const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
@@ -673,34 +731,36 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     int64_t lo, hi;
     if (!find_tile<BM>(g, v % g.m_tiles, l, e, lo, hi)) return;
     const int64_t n0 = (int64_t)(v / g.m_tiles) * BN;
-    const int8_t *pa[R], *pb[C];
+    const int8_t *pa[Ops::kA], *pb[Ops::kB];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int64_t p = lo + 16 * i + (l & 15);
+    for (int i = 0; i < Ops::kA; ++i) {
+        const int64_t p = lo + Ops::row(i, l);
         pa[i] = g.A + max(p < hi ? a_row(g, p) : -1, (int64_t)0) * g.lda;
     }
 #pragma unroll
-    for (int j = 0; j < C; ++j) pb[j] = g.B + e * g.strideb + min(n0 + 16 * j + (l & 15), g.N - 1) * g.ldb;
+    for (int j = 0; j < Ops::kB; ++j) pb[j] = g.B + e * g.strideb + min(n0 + Ops::row(j, l), g.N - 1) * g.ldb;
 
     i32x4 acc[R][C];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    const int64_t last = ANY ? g.K - 16 : (g.K - 1) & ~(int64_t)15;
-    const int lk = 16 * (l >> 4);
-    ThinOps<R, C, ANY> x, y;
+    const int64_t last = Ops::last(g.K);
+    const int lk = Ops::offset(l);
+    int8_t* const mine = lds + w * Ops::kLds;
+    Ops x, y;
     int64_t k = 128 * w;
     x.read(pa, pb, k + lk, last);
     for (; k < g.K; k += 256 * W) {
         y.read(pa, pb, k + 128 * W + lk, last);
         if (k + 128 > g.K) x.mask(k + lk, g.K);
-        x.multiply(acc);
+        x.multiply(acc, mine, l);
         if (k + 128 * W >= g.K) break;
         x.read(pa, pb, k + 256 * W + lk, last);
         if (k + 128 * W + 128 > g.K) y.mask(k + 128 * W + lk, g.K);
-        y.multiply(acc);
+        y.multiply(acc, mine, l);
     }
+    if (ANY) __syncthreads();  // the sums take the same LDS
     // D layout of the 16 x 16 MFMA: lane l, register r -> first operand's row 4 (l/16) + r (a column of C),
     // second operand's row l%16 (a row of C)
 #pragma unroll
