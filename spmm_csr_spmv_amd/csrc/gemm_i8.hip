@@ -7,7 +7,6 @@
 // K over instructions, waves and workgroups never changes a result; the float
 // of a sum is multiplied by a_scale, then by b_scale, and rounded once to C's type.
 #include <algorithm>
-#include <type_traits>
 
 #include "device_common.h"
 #include "moe.h"
@@ -606,82 +605,29 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
 
 // ---------------------------------------------------------------------------
 // Few rows: tiles of 16 R rows x 16 C columns, W waves that share the tile and
-// split K.
+// split K; rows of any alignment, K >= 16.
 //
-// With few rows the time is that of reading B once, so B goes from memory
-// straight into MFMA operands (16 rows of 64 bytes an instruction), each wave
-// taking 128 bytes of every row in turn and reading its next 128 before it
-// multiplies; the rows of A come from L2 the same way.  The waves' int32 sums
-// meet in LDS, exact in any order.  32 tokens x 8 of 64 experts, 4096 x 2048
-// (R = 1, C = 2, W = 4): 90 us, 5.9 TB/s of weights where reads alone reach
-// 7.0.  Loads are cached: both halves of a line are used, one after the other
-// (non-temporal ones fetch it twice, 118 us).
+// With few rows the time is that of reading B once.  Each wave takes 128 bytes
+// of every row in turn, eight lanes a row, and has its next 128 in flight while
+// it puts these together to MFMA operands, through LDS that no other wave
+// uses: nothing waits for another wave before the int32 sums meet, exact in
+// any order.  32 tokens x 8 of 64 experts, 4096 x 2048 (R = 1, C = 2, W = 4):
+// 87 us, 6.2 TB/s of weights where reads alone reach 7.0.  Operands loaded as
+// the MFMA wants them, sixteen rows of 64 bytes an instruction, took 91 us
+// (118 non-temporal, which fetches each line twice), 64 x 4096 x 4096 so 12.1
+// against 9.2, and with unaligned rows three times as long.
 template <int R, int C>
 struct ThinOps {
-    static constexpr int kA = R, kB = C;                // loads for the rows of A and of B
-    static constexpr int kLds = 0;
-    i32x4 a[2][R], b[2][C];
-    static __device__ __forceinline__ int row(int j, int l) { return 16 * j + (l & 15); }
-    static __device__ __forceinline__ int offset(int l) { return 16 * (l >> 4); }
-    // a piece that K cuts is read whole: 16 aligned bytes
-    static __device__ __forceinline__ int64_t last(int64_t K) { return (K - 1) & ~(int64_t)15; }
-    __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* const (&pb)[kB], int64_t k,
-                                         int64_t last) {
-        const int64_t k0 = min(k, last), k1 = min(k + 64, last);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {  // both halves of a 128-byte line, one after the other
-            b[0][j] = *reinterpret_cast<const i32x4*>(pb[j] + k0);
-            b[1][j] = *reinterpret_cast<const i32x4*>(pb[j] + k1);
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            a[0][j] = *reinterpret_cast<const i32x4*>(pa[j] + k0);
-            a[1][j] = *reinterpret_cast<const i32x4*>(pa[j] + k1);
-        }
-    }
-    // zeroes what does not belong to the row from this lane's k on
-    __device__ __forceinline__ void mask(int64_t k, int64_t K) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int64_t keep = K - k - 64 * h - 4 * d;
-                const int32_t m = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * (int)keep)) - 1;
-#pragma unroll
-                for (int j = 0; j < R; ++j) a[h][j][d] &= m;
-            }
-    }
-    __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C], int8_t*, int) const {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[h][j], a[h][i], acc[i][j], 0, 0, 0);
-    }
-};
-
-// The same for rows of any alignment (K >= 16, read as load_any does).  Eight
-// lanes read 128 bytes of a row, and the operands are put together through LDS
-// that only this wave uses: an unaligned load of sixteen pieces in sixteen
-// rows takes three times as long (32 x 8, 64 experts, 4095 x 2048 268 us so,
-// AAA us with whole pieces).
-template <int R, int C>
-struct ThinAny {
     static constexpr int kA = 2 * R, kB = 2 * C;
     static constexpr int kLds = 16 * (R + C) * kBigK;
     i32x4 v[kA + kB];
-    static __device__ __forceinline__ int row(int j, int l) { return 8 * j + (l >> 3); }
-    static __device__ __forceinline__ int offset(int l) { return 16 * (l & 7); }
-    static __device__ __forceinline__ int64_t last(int64_t K) { return K - 16; }
+    // load j of this lane: row 8 j + l / 8 of A's, then of B's, 16 bytes at k + 16 (l % 8)
     __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* const (&pb)[kB], int64_t k,
-                                         int64_t last) {
-        const int64_t at = min(k, last);
+                                         int64_t K) {
 #pragma unroll
-        for (int j = 0; j < kB; ++j) v[kA + j] = *reinterpret_cast<const i32x4_u*>(pb[j] + at);
+        for (int j = 0; j < kB; ++j) v[kA + j] = load_any(pb[j], k, K);
 #pragma unroll
-        for (int j = 0; j < kA; ++j) v[j] = *reinterpret_cast<const i32x4_u*>(pa[j] + at);
+        for (int j = 0; j < kA; ++j) v[j] = load_any(pa[j], k, K);
     }
     __device__ __forceinline__ void mask(int64_t k, int64_t K) {
 #pragma unroll
@@ -716,10 +662,10 @@ struct ThinAny {
     }
 };
 
-template <class D, int R, int C, int W, bool ANY>
+template <class D, int R, int C, int W>
 __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     typedef typename D::T T;
-    typedef typename std::conditional<ANY, ThinAny<R, C>, ThinOps<R, C>>::type Ops;
+    typedef ThinOps<R, C> Ops;
     constexpr int BM = 16 * R, BN = 16 * C, LD = BN + 4;
     constexpr int kSums = BM * LD * 4, kWave = Ops::kLds > kSums ? Ops::kLds : kSums;
     __shared__ __attribute__((aligned(1024))) int8_t lds[W * kWave];
@@ -734,33 +680,32 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     const int8_t *pa[Ops::kA], *pb[Ops::kB];
 #pragma unroll
     for (int i = 0; i < Ops::kA; ++i) {
-        const int64_t p = lo + Ops::row(i, l);
+        const int64_t p = lo + 8 * i + (l >> 3);
         pa[i] = g.A + max(p < hi ? a_row(g, p) : -1, (int64_t)0) * g.lda;
     }
 #pragma unroll
-    for (int j = 0; j < Ops::kB; ++j) pb[j] = g.B + e * g.strideb + min(n0 + Ops::row(j, l), g.N - 1) * g.ldb;
+    for (int j = 0; j < Ops::kB; ++j) pb[j] = g.B + e * g.strideb + min(n0 + 8 * j + (l >> 3), g.N - 1) * g.ldb;
 
     i32x4 acc[R][C];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < C; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    const int64_t last = Ops::last(g.K);
-    const int lk = Ops::offset(l);
+    const int lk = 16 * (l & 7);
     int8_t* const mine = lds + w * Ops::kLds;
     Ops x, y;
     int64_t k = 128 * w;
-    x.read(pa, pb, k + lk, last);
+    x.read(pa, pb, k + lk, g.K);
     for (; k < g.K; k += 256 * W) {
-        y.read(pa, pb, k + 128 * W + lk, last);
+        y.read(pa, pb, k + 128 * W + lk, g.K);
         if (k + 128 > g.K) x.mask(k + lk, g.K);
         x.multiply(acc, mine, l);
         if (k + 128 * W >= g.K) break;
-        x.read(pa, pb, k + 256 * W + lk, last);
+        x.read(pa, pb, k + 256 * W + lk, g.K);
         if (k + 128 * W + 128 > g.K) y.mask(k + 128 * W + lk, g.K);
         y.multiply(acc, mine, l);
     }
-    if (ANY) __syncthreads();  // the sums take the same LDS
+    __syncthreads();  // the sums take the same LDS
     // D layout of the 16 x 16 MFMA: lane l, register r -> first operand's row 4 (l/16) + r (a column of C),
     // second operand's row l%16 (a row of C)
 #pragma unroll
@@ -821,12 +766,6 @@ int launch(K kernel, GemmArgs g, int64_t bm, int64_t bn, int threads, hipStream_
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 
-template <class D, int R, int C, int W>
-int launch_thin(bool any, const GemmArgs& g, hipStream_t s) {
-    return any ? launch(gemm_i8_thin<D, R, C, W, true>, g, 16 * R, 16 * C, 64 * W, s)
-               : launch(gemm_i8_thin<D, R, C, W, false>, g, 16 * R, 16 * C, 64 * W, s);
-}
-
 // Which kernel.  Times are M x N x K, or tokens x choices, experts, K, N with
 // the weights read from memory each time, in us.
 template <class D>
@@ -857,12 +796,12 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     // staged 128x128 116; 8 x 8192 x 4001 16x32 16.4, staged 42.6;
     // 64 x 4096 x 4095 32x32 24, staged 33; 256 x 4096 x 4097 32x64 71, staged 36.
     const bool few = !any && tiles(g, 16, 32) <= kMostTiles;
-    if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(any, g, s);
+    if (tiles(g, 16, 32) <= 128) return launch(gemm_i8_thin<D, 1, 1, 8>, g, 16, 16, 512, s);
     const bool deep = few && g.K > 2048;
     if (tiles(g, 16, 32) <= 256 || (few && groups == 1 && g.S <= 16) || (deep && g.S <= 8 * groups))
-        return launch_thin<D, 1, 2, 4>(any, g, s);
-    if (tiles(g, 32, 32) <= 256) return launch_thin<D, 2, 2, 4>(any, g, s);
-    if (tiles(g, 32, 64) <= 256 || (deep && g.S <= 12 * groups)) return launch_thin<D, 2, 4, 4>(any, g, s);
+        return launch(gemm_i8_thin<D, 1, 2, 4>, g, 16, 32, 256, s);
+    if (tiles(g, 32, 32) <= 256) return launch(gemm_i8_thin<D, 2, 2, 4>, g, 32, 32, 256, s);
+    if (tiles(g, 32, 64) <= 256 || (deep && g.S <= 12 * groups)) return launch(gemm_i8_thin<D, 2, 4, 4>, g, 32, 64, 256, s);
     // 8192 x 8192 x 4095 403, with aligned rows 262.
     if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
