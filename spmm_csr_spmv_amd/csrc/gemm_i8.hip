@@ -126,6 +126,10 @@ __device__ __forceinline__ int64_t a_row(const GemmArgs& g, int64_t p) {
 __device__ __forceinline__ i32x4 load_any(const int8_t* row, int64_t k, int64_t K) {
     return *reinterpret_cast<const i32x4_u*>(row + min(k, K - 16));
 }
+// For rows that nothing else reads: non-temporal.
+__device__ __forceinline__ i32x4 load_any_once(const int8_t* row, int64_t k, int64_t K) {
+    return __builtin_nontemporal_load(reinterpret_cast<const i32x4_u*>(row + min(k, K - 16)));
+}
 __device__ __forceinline__ int32_t low_mask(int64_t k, int64_t K, int d) {
     const int64_t drop = k - (K - 16) - 4 * d;
     return drop <= 0 ? -1 : drop >= 4 ? 0 : (int32_t)(0xffffffffu << (8 * (int)drop));
@@ -185,8 +189,8 @@ struct BigShape {
     static constexpr int kCopies = kA + kB;
 };
 
-// Copies [FROM, TO) of the step's, in the order A, B.
-template <int WN, int F, int FROM, int TO>
+// Copies [FROM, TO) of the step's, in the order A, B.  ONCE: no other tile reads these rows of B.
+template <int WN, int F, bool ONCE, int FROM, int TO>
 __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const int8_t* const (&pa)[4],
                                          const int8_t* const (&pb)[4], int64_t k, int w) {
     using S = BigShape<WN, F>;
@@ -194,7 +198,10 @@ __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const int8_t* c
     for (int j = FROM; j < TO; ++j) {
         const int8_t* src = (j < S::kA ? pa[j & 3] : pb[(j - S::kA) & 3]) + k;
         int8_t* dst = (j < S::kA ? la + j * S::kRows * kBigK : lb + (j - S::kA) * S::kRows * kBigK) + w * 1024;
-        __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+        if (ONCE && j >= S::kA)
+            __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 2);  // non-temporal
+        else
+            __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
     }
 }
 
@@ -219,15 +226,15 @@ struct BigOps {
     }
     // The same with copies [FROM, TO) of a later step spread between the MFMAs:
     // a wave that issues them in one go waits for the memory pipeline to take them.
-    template <int WN, int FROM, int TO, int I = 0>
+    template <int WN, bool ONCE, int FROM, int TO, int I = 0>
     __device__ __forceinline__ void multiply_and_copy(i32x16 (&acc)[F][2], int8_t* la, int8_t* lb,
                                                       const int8_t* const (&pa)[4], const int8_t* const (&pb)[4],
                                                       int64_t k, int w) const {
         constexpr int N = TO - FROM;
-        big_copy<WN, F, FROM + (N * I + F - 1) / F, FROM + (N * (I + 1) + F - 1) / F>(la, lb, pa, pb, k, w);
+        big_copy<WN, F, ONCE, FROM + (N * I + F - 1) / F, FROM + (N * (I + 1) + F - 1) / F>(la, lb, pa, pb, k, w);
         multiply(acc, I, I + 1);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (I + 1 < F) multiply_and_copy<WN, FROM, TO, I + 1>(acc, la, lb, pa, pb, k, w);
+        if constexpr (I + 1 < F) multiply_and_copy<WN, ONCE, FROM, TO, I + 1>(acc, la, lb, pa, pb, k, w);
     }
 };
 
@@ -372,7 +379,7 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
     }
 }
 
-template <class D, int WN, int ST, int F>
+template <class D, int WN, int ST, bool ONCE, int F>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
                                          const BigBuffers<ST>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
     using S = BigShape<WN, F>;
@@ -404,8 +411,8 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     constexpr int kCopies = S::kCopies, kHalf = kCopies / 2;
 #define SPX_AT(s) min((int64_t)(s) * kBigK + chunk, last)
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) big_copy<WN, F, 0, kCopies>(m.a[i], m.b[i], pa, pb, SPX_AT(i), w);
-    big_copy<WN, F, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], pa, pb, SPX_AT(ST - 1), w);
+    for (int i = 0; i < ST - 1; ++i) big_copy<WN, F, ONCE, 0, kCopies>(m.a[i], m.b[i], pa, pb, SPX_AT(i), w);
+    big_copy<WN, F, ONCE, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], pa, pb, SPX_AT(ST - 1), w);
     big_barrier<(ST - 2) * kCopies + kHalf>();
     if (steps == 1 && left < kBigK) {
         big_mask<WN, F>(m.a[0], left, tid);
@@ -418,8 +425,8 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
         big_operands_here();                                                                              \
         x1.read(m.a[I], m.b[I], 1, wm, wn, l);                                                            \
         __builtin_amdgcn_sched_barrier(0);                                                                \
-        x0.template multiply_and_copy<WN, kHalf, kCopies>(acc, m.a[kBack], m.b[kBack], pa, pb,            \
-                                                          SPX_AT((s) + ST - 1), w);                       \
+        x0.template multiply_and_copy<WN, ONCE, kHalf, kCopies>(acc, m.a[kBack], m.b[kBack], pa, pb,      \
+                                                                SPX_AT((s) + ST - 1), w);                       \
         big_operands_here();                                                                              \
         x0.read(m.a[I], m.b[I], 2, wm, wn, l);                                                            \
         __builtin_amdgcn_sched_barrier(0);                                                                \
@@ -436,7 +443,7 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
         }                                                                                                 \
         x0.read(m.a[kNext], m.b[kNext], 0, wm, wn, l);                                                    \
         __builtin_amdgcn_sched_barrier(0);                                                                \
-        x1.template multiply_and_copy<WN, 0, kHalf>(acc, m.a[I], m.b[I], pa, pb, SPX_AT((s) + ST), w);    \
+        x1.template multiply_and_copy<WN, ONCE, 0, kHalf>(acc, m.a[I], m.b[I], pa, pb, SPX_AT((s) + ST), w); \
     }
     int s = 0;
     for (; s + ST <= steps; s += ST) {
@@ -476,7 +483,7 @@ __device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t v, uint32_
     return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
 }
 
-template <class D, int WN, int ST>
+template <class D, int WN, int ST, bool ONCE>
 __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(GemmArgs g) {
     constexpr int kBytes = 64 * WN * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
@@ -493,16 +500,16 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
         const BigBuffers<4> m = {{a0, a1, a2, a3}, {b0, b1, b2, b3}};
-        if (blocks == 1) return big_tile<D, WN, ST, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
-        big_tile<D, WN, ST, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        if (blocks == 1) return big_tile<D, WN, ST, ONCE, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        big_tile<D, WN, ST, ONCE, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
     } else {
         const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
-        if (blocks == 1) return big_tile<D, WN, ST, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        if (blocks == 1) return big_tile<D, WN, ST, ONCE, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
         if constexpr (WN == 4) {
-            if (blocks == 3) return big_tile<D, WN, ST, 3>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
-            if (blocks == 4) return big_tile<D, WN, ST, 4>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+            if (blocks == 3) return big_tile<D, WN, ST, ONCE, 3>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+            if (blocks == 4) return big_tile<D, WN, ST, ONCE, 4>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
         }
-        big_tile<D, WN, ST, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
+        big_tile<D, WN, ST, ONCE, 2>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
     }
 }
 
@@ -612,11 +619,12 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
 // it puts these together to MFMA operands, through LDS that no other wave
 // uses: nothing waits for another wave before the int32 sums meet, exact in
 // any order.  32 tokens x 8 of 64 experts, 4096 x 2048 (R = 1, C = 2, W = 4):
-// 87 us, 6.2 TB/s of weights where reads alone reach 7.0.  Operands loaded as
-// the MFMA wants them, sixteen rows of 64 bytes an instruction, took 91 us
-// (118 non-temporal, which fetches each line twice), 64 x 4096 x 4096 so 12.1
-// against 9.2, and with unaligned rows three times as long.
-template <int R, int C>
+// 76 us, 7.0 TB/s of weights, what reads alone reach, with ONCE, non-temporal
+// loads of B where one row tile reads it (86 without).  Operands loaded as the
+// MFMA wants them, sixteen rows of 64 bytes an instruction, took 91 (118
+// non-temporal, which fetched each line twice), 64 x 4096 x 4096 so 12.1 against
+// 9.2, and with unaligned rows three times as long.
+template <int R, int C, bool ONCE>
 struct ThinOps {
     static constexpr int kA = 2 * R, kB = 2 * C;
     static constexpr int kLds = 16 * (R + C) * kBigK;
@@ -625,7 +633,7 @@ struct ThinOps {
     __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* const (&pb)[kB], int64_t k,
                                          int64_t K) {
 #pragma unroll
-        for (int j = 0; j < kB; ++j) v[kA + j] = load_any(pb[j], k, K);
+        for (int j = 0; j < kB; ++j) v[kA + j] = ONCE ? load_any_once(pb[j], k, K) : load_any(pb[j], k, K);
 #pragma unroll
         for (int j = 0; j < kA; ++j) v[j] = load_any(pa[j], k, K);
     }
@@ -662,10 +670,10 @@ struct ThinOps {
     }
 };
 
-template <class D, int R, int C, int W>
+template <class D, int R, int C, int W, bool ONCE>
 __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
     typedef typename D::T T;
-    typedef ThinOps<R, C> Ops;
+    typedef ThinOps<R, C, ONCE> Ops;
     constexpr int BM = 16 * R, BN = 16 * C, LD = BN + 4;
     constexpr int kSums = BM * LD * 4, kWave = Ops::kLds > kSums ? Ops::kLds : kSums;
     __shared__ __attribute__((aligned(1024))) int8_t lds[W * kWave];
@@ -766,6 +774,12 @@ int launch(K kernel, GemmArgs g, int64_t bm, int64_t bn, int threads, hipStream_
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 
+template <class D, int R, int C, int W>
+int launch_thin(bool once, const GemmArgs& g, hipStream_t s) {
+    return once ? launch(gemm_i8_thin<D, R, C, W, true>, g, 16 * R, 16 * C, 64 * W, s)
+                : launch(gemm_i8_thin<D, R, C, W, false>, g, 16 * R, 16 * C, 64 * W, s);
+}
+
 // Which kernel.  Times are M x N x K, or tokens x choices, experts, K, N with
 // the weights read from memory each time, in us.
 template <class D>
@@ -775,48 +789,55 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     const int64_t mid = tiles(g, 128, 128);
     const bool any = !aligned16(g);
     if (g.K < 16 || mid > kMostTiles) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
+    const bool few = tiles(g, 16, 32) <= kMostTiles;
+    const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
+    // Up to 32 rows a matrix: B's rows are (nearly all) read by one row tile,
+    // and non-temporal.  32 x 8, 64, 4096, 2048 76 against 86 otherwise;
+    // 256 x 8 (32 rows) 130, 133; 512 x 8 (64 rows) 162, 143; 64 x 2048 x 2048 5.5,
+    // 5.0.  Not where unaligned pieces share lines: 96 x 8, 64, 4095, 2048 150, 139.
+    const bool once = !any && g.S <= 32 * groups;
     // Few tiles: the smallest ones, or most CUs stay idle.  A step up where 128
-    // or 256 tiles are reached: 1 x 4096 x 4096 16x16 6.7, 16x32 8.5;
-    // 8 x 8192 x 4096 16x16 11.8, 16x32 11.0; 32 x 4096 x 4096 16x32 10.1,
-    // 32x32 11.9; 64 x 4096 x 4096 16x32 15.8, 32x32 12.1, 32x64 16.3;
-    // 128 x 4096 x 4096 32x32 19.8, 32x64 16.7, 128x128 23.7;
-    // 256 x 4096 x 4096 32x64 28.8, 128x128 23.1.
+    // or 256 tiles are reached: 1 x 4096 x 4096 16x16 5.8, 16x32 7.3;
+    // 8 x 8192 x 4096 16x16 9.6, 16x32 9.3; 32 x 4096 x 4096 16x32 8.4,
+    // 32x32 9.1; 64 x 4096 x 4096 16x32 10.4, 32x32 9.1, 32x64 11.0;
+    // 128 x 4096 x 4096 32x32 12.6, 32x64 11.5, 128x128 23.7;
+    // 300 x 4096 x 1024 32x32 12, 32x64 14, 128x128 9.4.
     //
-    // Few rows a matrix (up to 16 of a single one, 8 on the average of several,
-    // where some have more) take the 16-row tiles in any number: 32 x 8, 64,
-    // 4096, 2048 16x32 91, 32x64 101, 128x128 117; with 9 to 12 rows on the
-    // average the 32-row ones: 96 x 8, 64, 4096, 2048 32x64 120, 128x128 134;
-    // 128 x 8 (16 rows) 127, 129; 64 x 2, 8, 4096, 14336 (16 rows) 135, 118.
-    // Short sums do not pay their four waves: 128 x 8, 128, 2048, 2048 (8 rows)
-    // 16x32 124, 128x128 103; 64 x 8, 128, 1024, 2048 (4 rows) 68, 63; but
-    // 64 x 8, 64, 4096, 1024 (8 rows) 60, 63.
-    //
-    // Rows that are not aligned lose most there (an operand load of sixteen
-    // unaligned pieces): with K one less, 32 x 8, 64, 4095, 2048 16x32 268,
-    // staged 128x128 116; 8 x 8192 x 4001 16x32 16.4, staged 42.6;
-    // 64 x 4096 x 4095 32x32 24, staged 33; 256 x 4096 x 4097 32x64 71, staged 36.
-    const bool few = !any && tiles(g, 16, 32) <= kMostTiles;
-    if (tiles(g, 16, 32) <= 128) return launch(gemm_i8_thin<D, 1, 1, 8>, g, 16, 16, 512, s);
-    const bool deep = few && g.K > 2048;
-    if (tiles(g, 16, 32) <= 256 || (few && groups == 1 && g.S <= 16) || (deep && g.S <= 8 * groups))
-        return launch(gemm_i8_thin<D, 1, 2, 4>, g, 16, 32, 256, s);
-    if (tiles(g, 32, 32) <= 256) return launch(gemm_i8_thin<D, 2, 2, 4>, g, 32, 32, 256, s);
-    if (tiles(g, 32, 64) <= 256 || (deep && g.S <= 12 * groups)) return launch(gemm_i8_thin<D, 2, 4, 4>, g, 32, 64, 256, s);
-    // 8192 x 8192 x 4095 403, with aligned rows 262.
+    // Few rows a matrix take them in any number.  One matrix: 16 rows 16x32
+    // (16 x 14336 x 4096 13.6, 32x64 14.2, 128x128 17.5), 32 rows 32x64
+    // (32 x 14336 x 4096 16.0, 128x128 21.3).  Experts: up to 8 rows on the
+    // average, where some have more, 16x32 (32 x 8, 64, 4096, 2048 76, 32x32 81,
+    // 128x128 117; 64 x 8 86, 86), up to 16 rows 32x32 (128 x 8 102, 16x32 115,
+    // 128x128 126; 160 x 8 (20 rows) 121, 134, 117).  Shorter sums do not pay the
+    // four waves of the latter: 128 x 8, 64, 2048, 2048 68, 128x128 60;
+    // 17 x 28672 x 2048 32x64 16.5, 128x128 13.9.
+    if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(once, g, s);
+    if (tiles(g, 16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= 8 * groups))
+        return launch_thin<D, 1, 2, 4>(once, g, s);
+    if (tiles(g, 32, 32) <= 256 || (experts && g.S <= 16 * groups && g.K > 2048))
+        return launch_thin<D, 2, 2, 4>(once, g, s);
+    // Unaligned rows, whose 128 x 128 tiles are slower, up to 512 tiles:
+    // 256 x 4096 x 4097 30, 128x128 47; 1024 x 1024 x 1023 12.4, 13.3.
+    if (tiles(g, 32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && g.K > 2048))
+        return launch_thin<D, 2, 4, 4>(once, g, s);
+    // 8192 x 8192 x 4095 403, with aligned rows 262; 32 x 8, 64, 4095, 2048 115
+    // (thin tiles 112), 96 x 8 119 (139), 24 x 8, 128, 1023, 2047 50 (58).
     if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
     // for memory: four steps in LDS.  1024 x 4096 x 4096 26 against 36 with two
     // steps and two workgroups a CU, and 55 with 256 x 256 tiles;
     // 256 x 8, 64, 4096, 2048 (32 rows) 133, 162, 166; 512 x 8 (64 rows) 144, 157, 171.
-    if (mid <= 256 || (few && g.S < 96 * groups)) return launch(gemm_i8_big<D, 2, 4>, g, 128, 128, 256, s);
+    if (once) return launch(gemm_i8_big<D, 2, 4, true>, g, 128, 128, 256, s);
+    if (mid <= 256 || (few && g.S < 96 * groups)) return launch(gemm_i8_big<D, 2, 4, false>, g, 128, 128, 256, s);
     // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 46, with four steps 53,
     // with 256 x 256 tiles 57.  Also where 256-wide tiles would be empty for a
     // fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
     const int64_t wide = (g.N + 255) / 256 * 256, narrow = (g.N + 127) / 128 * 128;
-    if (mid <= 512 || (few && 5 * wide >= 6 * narrow)) return launch(gemm_i8_big<D, 2, 2>, g, 128, 128, 256, s);
+    if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
+        return launch(gemm_i8_big<D, 2, 2, false>, g, 128, 128, 256, s);
     // 8192 x 8192 x 4096 251 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
     // 71, 89; 4096 x 8, 64, 4096, 2048 (512 rows) 335, 425; 1024 x 8 (128 rows) 183, 195.
-    return launch(gemm_i8_big<D, 4, 2>, g, 256, 256, 512, s);
+    return launch(gemm_i8_big<D, 4, 2, false>, g, 256, 256, 512, s);
 }
 
 }  // namespace
