@@ -37,12 +37,23 @@ struct GemmArgs {
     uint32_t m_tiles, n_tiles; // m_tiles is an upper bound when offsets are given; the product fits 31 bits
 };
 
-// Tile i of the rows [a, b): as many tiles as BM asks for, of equal height in units of 64 rows.
+// The rows of an expert make as many tiles as BM asks for, of equal height in
+// units of 64 rows (the last may be lower).  32-bit divisions: a 64-bit one
+// takes hundreds of instructions.
+template <int BM>
+__device__ __forceinline__ uint32_t row_tiles_of(uint32_t rows) {
+    return (rows + (BM - 1)) / BM;
+}
+template <int BM>
+__device__ __forceinline__ uint32_t tile_units(uint32_t rows) {
+    const uint32_t tiles = max(row_tiles_of<BM>(rows), 1u);
+    return ((rows + 63) / 64 + tiles - 1) / tiles;
+}
+
+// Tile i of the rows [a, b).
 template <int BM>
 __device__ __forceinline__ void cut(int a, int b, int i, int64_t& lo, int64_t& hi) {
-    const uint32_t rows = b - a, tiles = (rows + (BM - 1)) / BM;
-    const uint32_t units = (rows + 63) / 64;  // 32-bit divisions: a 64-bit one takes hundreds of instructions
-    const int64_t height = BM <= 64 ? BM : (units + tiles - 1) / max(tiles, 1u) * 64;
+    const int64_t height = BM <= 64 ? BM : 64 * (int64_t)tile_units<BM>(b - a);
     lo = a + i * height;
     hi = min(lo + height, (int64_t)b);
 }
@@ -57,28 +68,20 @@ __device__ __forceinline__ void expert_rows(const GemmArgs& g, int e, int& a, in
     }
 }
 
-// Inclusive prefix sum over the 64 lanes.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t u = __shfl_up(v, d, 64);
-        if (lane >= d) v += u;
-    }
-    return v;
+// Inclusive prefix sum over the 64 lanes: shifts by 1, 2, 4, 8 within rows of
+// 16 lanes, then the last lane of row 0 and 2 to the next row, and lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lanes_from(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
 }
-
-// Row tiles that the experts' rows make (the launch has room for more: it
-// does not know the offsets).  Every wave counts for itself, 64 experts at a time.
-template <int BM>
-__device__ __forceinline__ uint32_t count_tiles(const GemmArgs& g, int lane) {
-    if (!g.offsets) return g.m_tiles;
-    uint32_t n = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-        int a, b;
-        expert_rows(g, e0 + lane, a, b);
-        n += __builtin_amdgcn_readlane(wave_scan(((uint32_t)(b - a) + (BM - 1)) / BM, lane), 63);
-    }
-    return n;
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v += lanes_from<0x111, 0xf>(v);
+    v += lanes_from<0x112, 0xf>(v);
+    v += lanes_from<0x114, 0xf>(v);
+    v += lanes_from<0x118, 0xf>(v);
+    v += lanes_from<0x142, 0xa>(v);
+    v += lanes_from<0x143, 0xc>(v);
+    return v;
 }
 
 // Row tile number `tile` of the launch: expert e and rows [lo, hi) of its
@@ -97,7 +100,7 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& g, uint32_t tile, int 
     for (int e0 = 0; e0 < g.E; e0 += 64) {
         int a, b;
         expert_rows(g, e0 + lane, a, b);
-        const uint32_t mine = ((uint32_t)(b - a) + (BM - 1)) / BM, sum = wave_scan(mine, lane);
+        const uint32_t mine = row_tiles_of<BM>(b - a), sum = wave_scan(mine);
         const uint64_t past = __ballot(before + sum > tile);
         if (past) {
             const int l = __builtin_ctzll(past);
@@ -470,17 +473,77 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     big_out<D, WN, F>(g, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, lo, n0, w, l);
 }
 
-// Tile v of the m_tiles x n_tiles that there are: four row tiles to a column
-// tile, so that neighbours, which run on one XCD, share rows of A and of B in
-// its L2.  It is the tiles that there are, not those that the launch has room
-// for, that are dealt out to the XCDs: the last one would get the empty ones.
+// The row tiles that there are (a launch has room for more: it does not know
+// the offsets), and of them those of experts whose tiles are i + 1 units of 64
+// rows high.  Every wave counts for itself, 64 experts at a time.
 template <int WN>
-__device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t v, uint32_t m_tiles, int lane, int& e, int64_t& lo,
-                                          int64_t& hi, int64_t& n0) {
+struct BigCount {
+    uint32_t all, of[WN];
+    __device__ __forceinline__ BigCount(const GemmArgs& g, int lane) {
+        all = g.m_tiles;
+        if (!g.offsets) return;
+#pragma unroll
+        for (int i = 0; i < WN; ++i) of[i] = 0;
+        for (int e0 = 0; e0 < g.E; e0 += 64) {
+            int a, b;
+            expert_rows(g, e0 + lane, a, b);
+            const uint32_t tiles = row_tiles_of<64 * WN>(b - a), units = tile_units<64 * WN>(b - a);
+#pragma unroll
+            for (int i = 0; i < WN; ++i)
+                of[i] += __builtin_amdgcn_readlane(wave_scan(units == i + 1 ? tiles : 0), 63);
+        }
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < WN; ++i) all += of[i];
+    }
+};
+
+// Tile number t of all m.all x n_tiles, one of expert e's with the rows [lo, hi)
+// and columns from n0 on.  Four row tiles to a column tile follow each other.
+//
+// One matrix: neighbours run on one XCD and share rows of A and of B in its L2.
+// Experts: the tallest tiles first, so that what still runs when the others have
+// ended is short, and eight tiles, two column tiles', to each XCD in turn, so
+// that every XCD has as many of each height.  Against runs of neighbours in the
+// experts' order (us; uneven loads are log-normal with sigma 0.7): 8192 rows of
+// 64 uneven experts, 4096 x 2048 180, 192; 16384 of 128, 2048 x 1536 132, 141;
+// 8192 of 8 experts, 4096 x 14336 516, 532; 32768 of 64, 4096 x 2048 325, 331,
+// all of 512 rows 296, 294.
+template <int WN>
+__device__ __forceinline__ bool big_place(const GemmArgs& g, const BigCount<WN>& m, uint32_t t, int lane, int& e,
+                                          int64_t& lo, int64_t& hi, int64_t& n0) {
+    const uint32_t m_tiles = m.all, all = m_tiles * g.n_tiles;
+    const uint32_t v = !g.offsets ? (uint32_t)xcd_contiguous((int)t, 0, (int)all)
+                       : t < all / 64 * 64 ? t / 64 * 64 + t % 8 * 8 + t / 8 % 8 : t;
     const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
     const uint32_t high = min(m_tiles - first, 4u);
     n0 = (int64_t)(in / high) * (64 * WN);
-    return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
+    uint32_t tile = first + in % high;
+    if (!g.offsets) {
+        e = 0;
+        cut<64 * WN>(0, (int)g.S, (int)tile, lo, hi);
+        return true;
+    }
+    uint32_t height = WN;
+#pragma unroll
+    for (int i = WN - 1; i > 0; --i)
+        if (height == i + 1 && tile >= m.of[i]) tile -= m.of[i], height = i;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int a, b;
+        expert_rows(g, e0 + lane, a, b);
+        const uint32_t mine = tile_units<64 * WN>(b - a) == height ? row_tiles_of<64 * WN>(b - a) : 0;
+        const uint32_t sum = wave_scan(mine);
+        const uint64_t past = __ballot(sum > tile);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            e = e0 + l;
+            const uint32_t before = __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
+            cut<64 * WN>(__builtin_amdgcn_readlane(a, l), __builtin_amdgcn_readlane(b, l), (int)(tile - before), lo, hi);
+            return true;
+        }
+        tile -= __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
 }
 
 template <class D, int WN, int ST, bool ONCE>
@@ -490,12 +553,11 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
     __shared__ int32_t lrow[64 * WN];       // row of A of every row of the tile, or -1
     __shared__ float lscale[2 * 64 * WN];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    const uint32_t m_tiles = count_tiles<64 * WN>(g, l);
-    if (blockIdx.x >= m_tiles * g.n_tiles) return;
-    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)(m_tiles * g.n_tiles));
     int e;
     int64_t lo, hi, n0;
-    if (!big_place<WN>(g, v, m_tiles, l, e, lo, hi, n0)) return;
+    const BigCount<WN> m_tiles(g, l);
+    if (blockIdx.x >= m_tiles.all * g.n_tiles) return;
+    if (!big_place<WN>(g, m_tiles, blockIdx.x, l, e, lo, hi, n0)) return;
     const int blocks = (int)((hi - lo + 63) >> 6);
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
@@ -596,12 +658,12 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
     __shared__ float lscale[2 * 128];
     const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    const uint32_t m_tiles = count_tiles<128>(g, l), total = m_tiles * g.n_tiles;
+    const BigCount<2> m_tiles(g, l);
+    const uint32_t total = m_tiles.all * g.n_tiles;
     for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
-        const uint32_t v = total <= gridDim.x ? xcd_contiguous((int)t, 0, (int)total) : t;
         int e;
         int64_t lo, hi, n0;
-        if (!big_place<2>(g, v, m_tiles, l, e, lo, hi, n0)) continue;
+        if (!big_place<2>(g, m_tiles, t, l, e, lo, hi, n0)) continue;
         __syncthreads();  // the tile before has been stored
         if (hi - lo <= 64)
             staged_tile<D, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
