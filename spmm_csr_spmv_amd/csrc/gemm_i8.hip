@@ -44,16 +44,12 @@ template <int BM>
 __device__ __forceinline__ uint32_t row_tiles_of(uint32_t rows) {
     return (rows + (BM - 1)) / BM;
 }
-template <int BM>
-__device__ __forceinline__ uint32_t tile_units(uint32_t rows) {
-    const uint32_t tiles = max(row_tiles_of<BM>(rows), 1u);
-    return ((rows + 63) / 64 + tiles - 1) / tiles;
-}
 
 // Tile i of the rows [a, b).
 template <int BM>
 __device__ __forceinline__ void cut(int a, int b, int i, int64_t& lo, int64_t& hi) {
-    const int64_t height = BM <= 64 ? BM : 64 * (int64_t)tile_units<BM>(b - a);
+    const uint32_t rows = b - a, tiles = max(row_tiles_of<BM>(rows), 1u), units = (rows + 63) / 64;
+    const int64_t height = BM <= 64 ? BM : (units + tiles - 1) / tiles * 64;
     lo = a + i * height;
     hi = min(lo + height, (int64_t)b);
 }
@@ -82,6 +78,20 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     v += lanes_from<0x142, 0xa>(v);
     v += lanes_from<0x143, 0xc>(v);
     return v;
+}
+
+// Row tiles that the experts' rows make (the launch has room for more: it
+// does not know the offsets).  Every wave counts for itself, 64 experts at a time.
+template <int BM>
+__device__ __forceinline__ uint32_t count_tiles(const GemmArgs& g, int lane) {
+    if (!g.offsets) return g.m_tiles;
+    uint32_t n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int a, b;
+        expert_rows(g, e0 + lane, a, b);
+        n += __builtin_amdgcn_readlane(wave_scan(row_tiles_of<BM>(b - a)), 63);
+    }
+    return n;
 }
 
 // Row tile number `tile` of the launch: expert e and rows [lo, hi) of its
@@ -473,77 +483,34 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     big_out<D, WN, F>(g, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, lo, n0, w, l);
 }
 
-// The row tiles that there are (a launch has room for more: it does not know
-// the offsets), and of them those of experts whose tiles are i + 1 units of 64
-// rows high.  Every wave counts for itself, 64 experts at a time.
-template <int WN>
-struct BigCount {
-    uint32_t all, of[WN];
-    __device__ __forceinline__ BigCount(const GemmArgs& g, int lane) {
-        all = g.m_tiles;
-        if (!g.offsets) return;
-#pragma unroll
-        for (int i = 0; i < WN; ++i) of[i] = 0;
-        for (int e0 = 0; e0 < g.E; e0 += 64) {
-            int a, b;
-            expert_rows(g, e0 + lane, a, b);
-            const uint32_t tiles = row_tiles_of<64 * WN>(b - a), units = tile_units<64 * WN>(b - a);
-#pragma unroll
-            for (int i = 0; i < WN; ++i)
-                of[i] += __builtin_amdgcn_readlane(wave_scan(units == i + 1 ? tiles : 0), 63);
-        }
-        all = 0;
-#pragma unroll
-        for (int i = 0; i < WN; ++i) all += of[i];
-    }
-};
-
-// Tile number t of all m.all x n_tiles, one of expert e's with the rows [lo, hi)
-// and columns from n0 on.  Four row tiles to a column tile follow each other.
+// Tile number t of the m_tiles x n_tiles that there are.  Four row tiles to a
+// column tile follow each other.  It is the tiles that there are, not those that
+// the launch has room for, that are dealt out to the XCDs.
 //
 // One matrix: neighbours run on one XCD and share rows of A and of B in its L2.
-// Experts: the tallest tiles first, so that what still runs when the others have
-// ended is short, and eight tiles, two column tiles', to each XCD in turn, so
-// that every XCD has as many of each height.  Against runs of neighbours in the
-// experts' order (us; uneven loads are log-normal with sigma 0.7): 8192 rows of
-// 64 uneven experts, 4096 x 2048 180, 192; 16384 of 128, 2048 x 1536 132, 141;
-// 8192 of 8 experts, 4096 x 14336 516, 532; 32768 of 64, 4096 x 2048 325, 331,
-// all of 512 rows 296, 294.
-template <int WN>
-__device__ __forceinline__ bool big_place(const GemmArgs& g, const BigCount<WN>& m, uint32_t t, int lane, int& e,
+// Experts: tiles go to the XCDs RUN at a time in turn: experts with many rows,
+// bound by the matrix cores, and with few, bound by memory, are then under way
+// on all of them.  Against runs of neighbours, and one and eight at a time (us;
+// uneven loads are log-normal with sigma 0.7): 8192 rows of 64 uneven experts,
+// 4096 x 2048 192, 179, 186; 16384 of 128, 2048 x 1536 141, 131, 132; 512 of 8
+// even ones, 4096 x 14336 133, 119, 132; in 256 x 256 tiles 8192 of 8 541, 524,
+// 515; 32768 of 64, 4096 x 2048 340, 338, 336.  The tallest tiles first gained
+// nothing on that.  RUN = 0, neighbours, where a row tile has few column tiles
+// and all matrices fit the caches: 40000 of 16, 512 x 300 26, 29, 29.
+template <int WN, int RUN>
+__device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t m_tiles, uint32_t t, int lane, int& e,
                                           int64_t& lo, int64_t& hi, int64_t& n0) {
-    const uint32_t m_tiles = m.all, all = m_tiles * g.n_tiles;
-    const uint32_t v = !g.offsets ? (uint32_t)xcd_contiguous((int)t, 0, (int)all)
-                       : t < all / 64 * 64 ? t / 64 * 64 + t % 8 * 8 + t / 8 % 8 : t;
+    const uint32_t all = m_tiles * g.n_tiles;
+    constexpr uint32_t kRound = RUN > 0 ? RUN * kXcds : 1;
+    uint32_t v = t;
+    if (RUN == 0 || !g.offsets)
+        v = (uint32_t)xcd_contiguous((int)t, 0, (int)all);
+    else if (t < all / kRound * kRound)
+        v = t / kRound * kRound + t % kXcds * RUN + t / kXcds % RUN;
     const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
     const uint32_t high = min(m_tiles - first, 4u);
     n0 = (int64_t)(in / high) * (64 * WN);
-    uint32_t tile = first + in % high;
-    if (!g.offsets) {
-        e = 0;
-        cut<64 * WN>(0, (int)g.S, (int)tile, lo, hi);
-        return true;
-    }
-    uint32_t height = WN;
-#pragma unroll
-    for (int i = WN - 1; i > 0; --i)
-        if (height == i + 1 && tile >= m.of[i]) tile -= m.of[i], height = i;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-        int a, b;
-        expert_rows(g, e0 + lane, a, b);
-        const uint32_t mine = tile_units<64 * WN>(b - a) == height ? row_tiles_of<64 * WN>(b - a) : 0;
-        const uint32_t sum = wave_scan(mine);
-        const uint64_t past = __ballot(sum > tile);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            e = e0 + l;
-            const uint32_t before = __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
-            cut<64 * WN>(__builtin_amdgcn_readlane(a, l), __builtin_amdgcn_readlane(b, l), (int)(tile - before), lo, hi);
-            return true;
-        }
-        tile -= __builtin_amdgcn_readlane(sum, 63);
-    }
-    return false;
+    return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
 }
 
 template <class D, int WN, int ST, bool ONCE>
@@ -555,9 +522,9 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     int e;
     int64_t lo, hi, n0;
-    const BigCount<WN> m_tiles(g, l);
-    if (blockIdx.x >= m_tiles.all * g.n_tiles) return;
-    if (!big_place<WN>(g, m_tiles, blockIdx.x, l, e, lo, hi, n0)) return;
+    const uint32_t m_tiles = count_tiles<64 * WN>(g, l);
+    if (blockIdx.x >= m_tiles * g.n_tiles) return;
+    if (!big_place<WN, ST == 4 ? 1 : WN == 4 ? 8 : 0>(g, m_tiles, blockIdx.x, l, e, lo, hi, n0)) return;
     const int blocks = (int)((hi - lo + 63) >> 6);
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
@@ -658,12 +625,11 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
     __shared__ float lscale[2 * 128];
     const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    const BigCount<2> m_tiles(g, l);
-    const uint32_t total = m_tiles.all * g.n_tiles;
+    const uint32_t m_tiles = count_tiles<128>(g, l), total = m_tiles * g.n_tiles;
     for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
         int e;
         int64_t lo, hi, n0;
-        if (!big_place<2>(g, m_tiles, t, l, e, lo, hi, n0)) continue;
+        if (!big_place<2, 8>(g, m_tiles, t, l, e, lo, hi, n0)) continue;
         __syncthreads();  // the tile before has been stored
         if (hi - lo <= 64)
             staged_tile<D, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
@@ -853,10 +819,11 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     if (g.K < 16 || mid > kMostTiles) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     const bool few = tiles(g, 16, 32) <= kMostTiles;
     const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
+    const bool deep = g.K > 2048;
     // Up to 32 rows a matrix: B's rows are (nearly all) read by one row tile,
-    // and non-temporal.  32 x 8, 64, 4096, 2048 76 against 86 otherwise;
-    // 256 x 8 (32 rows) 130, 133; 512 x 8 (64 rows) 162, 143; 64 x 2048 x 2048 5.5,
-    // 5.0.  Not where unaligned pieces share lines: 96 x 8, 64, 4095, 2048 150, 139.
+    // and non-temporal.  32 x 8, 64, 4096, 2048 76 against 86 otherwise; 160 x 8
+    // (20 rows) 110, 118; 512 x 8 (64 rows) 142, 132; 64 x 2048 x 2048 5.5, 5.0.
+    // Not where unaligned pieces share lines: 96 x 8, 64, 4095, 2048 150, 139.
     const bool once = !any && g.S <= 32 * groups;
     // Few tiles: the smallest ones, or most CUs stay idle.  A step up where 128
     // or 256 tiles are reached: 1 x 4096 x 4096 16x16 5.8, 16x32 7.3;
@@ -868,37 +835,40 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     // Few rows a matrix take them in any number.  One matrix: 16 rows 16x32
     // (16 x 14336 x 4096 13.6, 32x64 14.2, 128x128 17.5), 32 rows 32x64
     // (32 x 14336 x 4096 16.0, 128x128 21.3).  Experts: up to 8 rows on the
-    // average, where some have more, 16x32 (32 x 8, 64, 4096, 2048 76, 32x32 81,
-    // 128x128 117; 64 x 8 86, 86), up to 16 rows 32x32 (128 x 8 102, 16x32 115,
-    // 128x128 126; 160 x 8 (20 rows) 121, 134, 117).  Shorter sums do not pay the
-    // four waves of the latter: 128 x 8, 64, 2048, 2048 68, 128x128 60;
-    // 17 x 28672 x 2048 32x64 16.5, 128x128 13.9.
+    // average, where some have more, 16x32 (32 x 8, 64, 4096, 2048 76, 32x32 81;
+    // 64 x 8 86, 86), up to 16 rows 32x32 (128 x 8 102, 16x32 115, 128x128 114;
+    // 160 x 8 (20 rows) 121, 134, 110).  Shorter sums do not pay their four waves
+    // as long: 96 x 8, 128, 2048, 2048 (6 rows) 16x32 85, 128x128 86; 128 x 8 (8
+    // rows) 96, 89; 17 x 28672 x 2048 32x64 16.5, 128x128 13.9.
     if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(once, g, s);
-    if (tiles(g, 16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= 8 * groups))
+    if (tiles(g, 16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
         return launch_thin<D, 1, 2, 4>(once, g, s);
-    if (tiles(g, 32, 32) <= 256 || (experts && g.S <= 16 * groups && g.K > 2048))
+    if (tiles(g, 32, 32) <= 256 || (experts && g.S <= 16 * groups && deep))
         return launch_thin<D, 2, 2, 4>(once, g, s);
     // Unaligned rows, whose 128 x 128 tiles are slower, up to 512 tiles:
     // 256 x 4096 x 4097 30, 128x128 47; 1024 x 1024 x 1023 12.4, 13.3.
-    if (tiles(g, 32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && g.K > 2048))
+    if (tiles(g, 32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
         return launch_thin<D, 2, 4, 4>(once, g, s);
-    // 8192 x 8192 x 4095 403, with aligned rows 262; 32 x 8, 64, 4095, 2048 115
-    // (thin tiles 112), 96 x 8 119 (139), 24 x 8, 128, 1023, 2047 50 (58).
+    // 8192 x 8192 x 4095 403, with aligned rows 245; 32 x 8, 64, 4095, 2048 117
+    // (thin tiles 112), 96 x 8 119 (139), 24 x 8, 128, 1023, 2047 49 (58).
     if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
-    // One 128 x 128 tile a CU at most, or tiles that are mostly short and wait
-    // for memory: four steps in LDS.  1024 x 4096 x 4096 26 against 36 with two
-    // steps and two workgroups a CU, and 55 with 256 x 256 tiles;
-    // 256 x 8, 64, 4096, 2048 (32 rows) 133, 162, 166; 512 x 8 (64 rows) 144, 157, 171.
+    // One 128 x 128 tile a CU at most, or tiles that mostly wait for memory: four
+    // steps in LDS.  1024 x 4096 x 4096 26 against 36 with two steps and two
+    // workgroups a CU, and 55 with 256 x 256 tiles; 512 x 8, 64, 4096, 2048 (64
+    // rows) 132, 151, 137; 1024 x 8 (128 rows) 163, 180, 174; 1024 x 2, 8, 4096,
+    // 14336 (256 rows) 226, 223, 193 (but 512 x 2 151, 158, 138); shorter sums 512 x 8, 128, 2048, 1536 (32
+    // rows) 92, 96, 93; 16384 rows of 128 uneven experts, 2048 x 1536 144, 140, 132.
     if (once) return launch(gemm_i8_big<D, 2, 4, true>, g, 128, 128, 256, s);
-    if (mid <= 256 || (few && g.S < 96 * groups)) return launch(gemm_i8_big<D, 2, 4, false>, g, 128, 128, 256, s);
+    if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
+        return launch(gemm_i8_big<D, 2, 4, false>, g, 128, 128, 256, s);
     // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 46, with four steps 53,
     // with 256 x 256 tiles 57.  Also where 256-wide tiles would be empty for a
     // fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
     const int64_t wide = (g.N + 255) / 256 * 256, narrow = (g.N + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
         return launch(gemm_i8_big<D, 2, 2, false>, g, 128, 128, 256, s);
-    // 8192 x 8192 x 4096 251 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
-    // 71, 89; 4096 x 8, 64, 4096, 2048 (512 rows) 335, 425; 1024 x 8 (128 rows) 183, 195.
+    // 8192 x 8192 x 4096 245 against 298 with 128 x 128 tiles; 4096 x 4096 x 4096
+    // 64, 77; 4096 x 8, 64, 4096, 2048 (512 rows) 330, 407.
     return launch(gemm_i8_big<D, 4, 2, false>, g, 256, 256, 512, s);
 }
 
