@@ -618,7 +618,7 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  *
  * Alignment: none needed for A and B (C and the scales: the element's).  When
  * A, B, lda, ldb (and strideb) are multiples of 16 bytes the kernels for
- * aligned rows run, up to three times as fast; they read the rows in 16-byte
+ * aligned rows run, up to 1.7 times as fast; they read the rows in 16-byte
  * pieces, so that up to 15 bytes behind a row's last (K rounded up to 16) are
  * read and ignored, also behind the last row: within its 16-byte piece, never
  * past it.  Other rows are read exactly.
