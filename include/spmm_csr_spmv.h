@@ -558,7 +558,7 @@ int bsr_spmm(int64_t mb, int64_t kb, int32_t bs, int64_t nnzb,
  * moe_combine: Y[t] = sum_j weights[t, j] Ys[pos[t, j]], summed in fp32 in
  * order of j and rounded once; weights (fp32, T x slots) may be NULL: all
  * ones.  A slot with a place outside [0, S) contributes nothing (its weight
- * is not read); a token without any gets zeros.  0 * Inf in a routed slot is
+ * is ignored); a token without any gets zeros.  0 * Inf in a routed slot is
  * NaN, as the formula says.
  *
  * moe_combine_backward: from dY (T x H): dYs[pos[t, j]] = weights[t, j] dY[t]

@@ -548,6 +548,45 @@ def test_expert_products(case, pad, dtype):
     assert (out[live:] == -7).all()
 
 
+# M, N, K: few rows of many columns; 512 tiles of 32 x 64
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("stride", STRIDES)
+@pytest.mark.parametrize("M,N,K", [(13, 8300, 2100), (20, 8700, 2100), (32, 17000, 2064), (32, 17001, 130), (33, 9000, 2064),
+                                   (250, 4100, 300), (513, 2040, 80)])
+def test_product_of_few_rows(M, N, K, stride, dtype):
+    test_product(M, N, K, stride, dtype)
+
+
+# 8 to 16 rows an expert with long and short sums; many rows, several rounds of tiles on every XCD and a rest; one
+# expert with nearly all; a few rows each of experts with many and with none
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("case", [(200, 2, 32, 330, 2100, 0, "random", True), (150, 2, 33, 333, 2065, 0.1, "random", True),
+                                  (200, 2, 32, 330, 2000, 0, "random", True), (110, 2, 32, 500, 1000, 0.1, "random", True),
+                                  (3000, 3, 6, 1300, 144, 0.02, "random", True), (9001, 1, 7, 1290, 129, 0, "skew", False),
+                                  (700, 8, 90, 520, 100, 0, "skew", True), (1500, 4, 64, 600, 2050, 0, "skew", True),
+                                  (12000, 1, 5, 300, 64, 0.1, "random", False)])
+def test_expert_products_of_more_shapes(case, pad, dtype):
+    test_expert_products(case, pad, dtype)
+
+
+def test_strided_and_repeated_sources():
+    """The same token for all rows of an expert, in both orders, and weights whose experts lie apart."""
+    rng = rng_for("repeated")
+    E, N, K, R, S = 5, 300, 2100, 3, 320
+    A, B = codes(rng, R, K), codes(rng, E * N, K)
+    whole = torch.zeros(E, N + 7, 2112, dtype=torch.int8, device="cuda")
+    Bd = whole[:, 3:3 + N, :K]
+    Bd.copy_(dev(B).view(E, N, K))
+    sa, sb = (rng.random(R) + 0.5).astype(np.float32), (rng.random((E, N)) + 0.5).astype(np.float32)
+    offsets = np.array([0, 0, 64, 65, 320, 320], np.int32)
+    src = np.concatenate([np.full(64, 2), [0], np.sort(rng.integers(0, R, S - 65))[::-1]]).astype(np.int32)
+    out = sp.moe_gemm_i8(strided(A, 12), dev(sa), Bd, dev(sb), dev(offsets), src=dev(src), dtype=torch.float32)
+    e = np.repeat(np.arange(E), np.diff(offsets))
+    sums = np.einsum("pk,pnk->pn", A[src].astype(np.float64), B.reshape(E, N, K)[e].astype(np.float64))
+    product_close(out, sums, sa[src], sb[e], "f32")
+
+
 def test_expert_products_with_bad_offsets_and_sources():
     """Nothing is validated on the device: out-of-range offsets are clamped, sources outside A are skipped."""
     rng = rng_for("bad")
