@@ -547,7 +547,8 @@ int bsr_spmm(int64_t mb, int64_t kb, int32_t bs, int64_t nnzb,
  * token, a slot over an expert's capacity).  Slots of one expert keep their
  * order, so the result is unique and bit-exact.  num_experts in
  * [1, SP_MOE_MAX_EXPERTS]; n may be 0.  work: moe_sort_bufsize() bytes (0 for
- * small n: then NULL is fine), 4-byte aligned; its contents on entry do not
+ * small n: then NULL is fine), 4-byte aligned, apart from ids and the outputs
+ * (SP_ERR_WORKSPACE where it overlaps one); its contents on entry do not
  * matter; calls that share it must not overlap.
  *
  * moe_dispatch: Xs[pos[f]] = X[f / slots], a copy: X is T x H (rows ldx

@@ -116,7 +116,7 @@ def moe_sort(ids, num_experts, work=None, stream=None):
     [num_experts + 1], src int32 [n], pos int32 of ids' shape).  src[p] is the slot
     at place p (-1 from place offsets[-1] on), pos[f] the place of slot f; a slot
     whose id is outside [0, num_experts) is routed nowhere, its pos is -1.  `work` is
-    a uint8 device tensor of moe_sort_bufsize bytes (allocated when None)."""
+    a uint8 device tensor of moe_sort_bufsize bytes apart from ids (allocated when None)."""
     _whole(ids, _I32, ids.dim(), "ids")
     n, num_experts = ids.numel(), int(num_experts)
     need = _sort_bytes(n, num_experts)

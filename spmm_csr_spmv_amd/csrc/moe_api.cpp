@@ -15,6 +15,12 @@ bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 // rows rows ld apart: the last element's byte offset must fit 63 bits
 bool too_far(int64_t rows, int64_t ld) { return rows > 0 && ld > (kI64Max >> 4) / rows; }
 
+// whether [a, a + an) and [b, b + bn) share a byte
+bool share(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return an > 0 && bn > 0 && (x <= y ? y - x < an : x - y < bn);
+}
+
 int rows_args(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype) {
     if (T < 0 || T > kI32Max || slots < 1 || H < 0 || H > kI32Max || S < 0 || S > kI32Max) return SP_ERR_SIZE;
     if (T * slots > kI32Max) return SP_ERR_SIZE;
@@ -43,6 +49,11 @@ int moe_sort(int64_t n, int32_t num_experts, const int32_t* ids, int32_t* offset
     if (misaligned(ids, 4) || misaligned(offsets, 4) || misaligned(src, 4) || misaligned(pos, 4))
         return SP_ERR_UNSUPPORTED;
     if (need > 0 && (!work || work_bytes < need || misaligned(work, 4))) return SP_ERR_WORKSPACE;
+    // Counts written over the ids would make the second kernel place slots that the first did not count.
+    const size_t ids_bytes = (size_t)n * sizeof(int32_t);
+    if (share(work, need, ids, ids_bytes) || share(work, need, src, ids_bytes) || share(work, need, pos, ids_bytes) ||
+        share(work, need, offsets, ((size_t)num_experts + 1) * sizeof(int32_t)))
+        return SP_ERR_WORKSPACE;
     return spx::moe_sort_device(n, num_experts, ids, offsets, src, pos, work, (hipStream_t)stream);
 }
 
