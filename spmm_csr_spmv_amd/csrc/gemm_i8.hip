@@ -478,7 +478,7 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     }
 #undef SPX_STEP
 #undef SPX_AT
-    __syncthreads();  // the copies behind the last step have landed too
+    big_barrier<0>();  // the copies behind the last step have landed too: the sums take their LDS
 
     big_out<D, WN, F>(g, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, lo, n0, w, l);
 }
@@ -673,13 +673,17 @@ struct ThinOps {
             for (int j = 0; j < kA; ++j) v[j][d] &= m;
         }
     }
-    // A wave's LDS operations are done in order: no wait between them.
+    // The lanes of a wave read what others of them wrote.  A wave's LDS operations
+    // are done in the order of its instructions, so no wait is needed, only that
+    // the compiler keeps that order: the barriers emit nothing.
     __device__ __forceinline__ void multiply(i32x4 (&acc)[R][C], int8_t* lds, int l) const {
+        __builtin_amdgcn_wave_barrier();  // the operands of the 128 bytes before have been read
 #pragma unroll
         for (int j = 0; j < kA + kB; ++j) {
             const int r = 8 * j + (l >> 3);
             *reinterpret_cast<i32x4*>(lds + r * kBigK + (((l & 7) ^ big_swizzle(r)) << 4)) = v[j];
         }
+        __builtin_amdgcn_wave_barrier();
         i32x4 x[2][R + C];
 #pragma unroll
         for (int h = 0; h < 2; ++h)

@@ -188,10 +188,11 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
                 const uint64_t m = __ballot((id >> k) & 1);
                 same &= ((id >> k) & 1) ? m : ~m;
             }
+            const int rank = __popcll(same & ((1ull << lane) - 1));
+            const int p = mine[live ? id : 0] + rank;
+            __builtin_amdgcn_wave_barrier();  // the wave's lanes have all read it
             if (live) {
-                const int rank = __popcll(same & ((1ull << lane) - 1));
-                const int p = mine[id] + rank;
-                if (rank == 0) mine[id] = p + __popcll(same);  // the wave's lanes have all read it
+                if (rank == 0) mine[id] = p + __popcll(same);
                 src[p] = (int32_t)f;
                 pos[f] = p;
             } else if (f < we) {
