@@ -4,16 +4,18 @@ Like the rest of the package: the functions have the names of the C calls, check
 types, shapes, devices and strides, allocate what is not given, and raise
 SparseError on a non-zero status.  Row tensors may have any row distance as long
 as their last dimension is contiguous and rows do not overlap.  Everything is
-enqueued on `stream` (default: the current stream of the tensors' device), nothing
-synchronises, and nothing here is recorded for autograd: gradients are calls of
-their own (moe_combine for moe_dispatch's, moe_combine_backward for moe_combine's).
+enqueued on `stream` (default: the current stream of the tensors' device; with a
+stream given the operands are marked as used there, so that their memory is not
+handed out again before the call has read it), nothing synchronises, and nothing
+here is recorded for autograd: gradients are calls of their own (moe_combine for
+moe_dispatch's, moe_combine_backward for moe_combine's).
 """
 import ctypes
 import functools
 
 import torch
 
-from ._binding import SP_OK, SparseError, _on, _sz, lib
+from ._binding import SP_OK, SparseError, _on, _sz, _used_on, lib
 
 _Tensor = torch.Tensor
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -101,7 +103,11 @@ def _call(body, t, stream, *args):
     if stream is not None and stream.device.index != device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
     with torch.cuda.device(device), _on(stream):
-        return body(_current_stream(device), *args)
+        result = body(_current_stream(device), *args)
+    for a in args:
+        if isinstance(a, _Tensor):
+            _used_on(a, stream)
+    return result
 
 
 @functools.lru_cache(maxsize=256)

@@ -1,5 +1,6 @@
 """Calls at the edges of the mixture-of-experts operators: operands on other streams, inside one buffer, scales and
 sizes at the ends of their range, and launches with more work than workgroups."""
+import numpy as np
 import pytest
 import torch
 
@@ -15,6 +16,92 @@ def codes(g, *shape, most=127):
 
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ------------------------------------------------------------------ operands of another stream
+def busy(stream):
+    """Tens of milliseconds of work on `stream`."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+
+
+def test_operands_of_a_side_stream_call_are_kept():
+    """Memory of an operand that is dropped right after a call on a side stream is not handed out before the call has
+    read it."""
+    say("kept operands")
+    T, k, E, H, F = 600, 2, 4, 256, 192
+    rng = np.random.default_rng(3)
+    ids0 = torch.from_numpy(rng.integers(0, E, (T, k)).astype(np.int32)).cuda()
+    offsets, src, pos = sp.moe_sort(ids0, E)
+    x0 = torch.randn(T, H, device="cuda")
+    ys0 = torch.randn(T * k, H, device="cuda")
+    w0 = torch.rand(T, k, device="cuda")
+    q0, s0 = sp.quantize_rows_i8(x0)
+    B0, b0 = codes(gen(4), E, F, H), torch.rand(E, F, device="cuda")
+    many = torch.from_numpy(rng.integers(0, E, 9000).astype(np.int32)).cuda()
+    work0 = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    calls = {
+        "sort": (lambda s, i: sp.moe_sort(i, E, stream=s), (ids0,)),
+        "sort's work": (lambda s, i, m: sp.moe_sort(i, E, work=m, stream=s), (many, work0)),
+        "dispatch": (lambda s, x, p: sp.moe_dispatch(x, p, stream=s), (x0, pos)),
+        "combine": (lambda s, y, p, w: sp.moe_combine(y, p, w, stream=s), (ys0, pos, w0)),
+        "backward": (lambda s, g, y, p, w: sp.moe_combine_backward(g, y, p, w, stream=s), (x0, ys0, pos, w0)),
+        "quantize": (lambda s, x: sp.quantize_rows_i8(x, stream=s), (x0,)),
+        "gemm": (lambda s, q, a, B, b: sp.gemm_i8(q, a, B, b, stream=s), (q0, s0, B0[0], b0[0])),
+        "experts": (lambda s, q, a, B, b, o, f: sp.moe_gemm_i8(q, a, B, b, o, src=f, slots=k, stream=s),
+                    (q0, s0, B0, b0, offsets, src)),
+    }
+    side = torch.cuda.Stream()
+    for name, (call, kept) in calls.items():
+        want = call(None, *kept)
+        args = [t.clone(memory_format=torch.contiguous_format) for t in kept]
+        where = {t.data_ptr() for t in args}
+        sizes = [(t.shape, t.dtype) for t in args]
+        torch.cuda.synchronize()
+        busy(side)
+        got = call(side, *args)
+        del args
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in sizes]
+        waiting = not side.query()
+        handed_out = [t for t in again if t.data_ptr() in where]
+        for t in again:
+            t.zero_()
+        torch.cuda.synchronize()
+        assert waiting, "the side stream was done too early to show anything"
+        assert not handed_out, name
+        for u, v in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+            assert torch.equal(u, v), name
+
+
+def test_stream_given_in_a_capture():
+    """The operands of a call that is captured on the stream it is given, dropped and made anew between replays."""
+    say("stream in a capture")
+    T, k, E, H = 700, 2, 5, 160
+    rng = np.random.default_rng(8)
+    ids = torch.from_numpy(rng.integers(-1, E, (T, k)).astype(np.int32)).cuda()
+    x, w = torch.randn(T, H, device="cuda"), torch.rand(T, k, device="cuda")
+
+    def step(stream):
+        _, _, pos = sp.moe_sort(ids, E, stream=stream)
+        rows = sp.moe_dispatch(x, pos, out=torch.zeros(T * k, H, device="cuda"), stream=stream)
+        return sp.moe_combine(rows, pos, w, stream=stream)  # the rows' memory is free again after this
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        out = step(side)
+    for n in range(4):
+        x.normal_()
+        ids.copy_(torch.from_numpy(rng.integers(-1, E, (T, k)).astype(np.int32)))
+        want = step(None)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), n
 
 
 # ------------------------------------------------------------------ sums through a wave's own LDS
