@@ -603,7 +603,8 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  * and B N x K, K-contiguous rows (the layout of a linear layer's weight), a
  * scale per row of A (token) and per row of B (output channel).  The sums are
  * exact int32 (K <= SP_I8_MAX_K); the float of a sum times a_scale times
- * b_scale is rounded once to c_type.  K == 0 gives the empty sum.
+ * b_scale is rounded once to c_type, and overflows only where that product
+ * does.  K == 0 gives the empty sum.
  *
  * moe_gemm_i8: one matrix B[e] (N x K, strideb bytes apart) and b_scale[e]
  * (b_scale is num_experts x N, contiguous) per expert, applied to the rows

@@ -4,9 +4,10 @@
 // where p runs over the rows sorted by expert, e is the expert whose range
 // offsets[e] .. offsets[e + 1] holds p, and r is p, or the token src[p] / slots.
 // The sums are int32 and exact (K <= 131071: K 128^2 < 2^31), so the split of
-// K over instructions, waves and workgroups never changes a result; the float
-// of a sum is multiplied by a_scale, then by b_scale, and rounded once to C's type.
+// K over instructions and waves never changes a result; the float of a sum is
+// multiplied by a_scale, then by b_scale, and rounded once to C's type.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "moe.h"
@@ -156,9 +157,17 @@ __device__ __forceinline__ i32x4 load_short(const int8_t* row, int64_t k, int64_
     return v;
 }
 
-template <class D>
+// A sum is below 2^31, so times a scale above 2^96 it can pass fp32's range where
+// the result does not (rows whose largest value is near the type's).  Such a scale
+// goes in times 2^-32 and the result is multiplied by 2^32, both exact.  That path
+// (FAR) is taken where a tile, or the rows of a wave, hold such a scale: the last
+// factor on every product made 8192 x 8192 x 4096 take 248 us, without 243, so 244.
+__device__ __forceinline__ bool far_scale(float sa) { return fabsf(sa) > 0x1p96f; }
+template <class D, bool FAR>
 __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
-    return D::down((float)sum * sa * sb);
+    if (!FAR) return D::down((float)sum * sa * sb);
+    const bool far = far_scale(sa);
+    return D::down((float)sum * (far ? sa * 0x1p-32f : sa) * sb * (far ? 0x1p32f : 1.0f));
 }
 
 // ---------------------------------------------------------------------------
@@ -292,7 +301,8 @@ __device__ __forceinline__ void big_barrier() {
 }
 
 // Where a lane's copies read: rows kRows j + 8 w + l / 8 of the tile, chunk
-// (l % 8) ^ big_swizzle(row); the tile's rows of A and scales go to LDS.
+// (l % 8) ^ big_swizzle(row); the tile's rows of A and scales go to LDS, and behind
+// the rows a word of each wave that says whether it met a far scale.
 template <int WN, int F>
 struct BigRows {
     const int8_t *a[4], *b[4];
@@ -302,6 +312,7 @@ struct BigRows {
         using S = BigShape<WN, F>;
         const int crow = 8 * w + (l >> 3);
         chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
+        bool far = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = S::kRows * j + crow;
@@ -310,10 +321,13 @@ struct BigRows {
             a[j] = g.A + max(r, (int64_t)0) * g.lda;  // a row that is not there copies row 0; its sums are not stored
             if (j < S::kA && (l & 7) == 0) {
                 lrow[row] = (int32_t)r;
-                lscale[row] = g.a_scale[max(r, (int64_t)0)];
+                const float sa = g.a_scale[max(r, (int64_t)0)];
+                lscale[row] = sa;
+                far |= far_scale(sa);
             }
             b[j] = g.B + e * g.strideb + min(n0 + row, g.N - 1) * g.ldb;
         }
+        lrow[64 * WN + w] = __any(far);
         if (tid < 64 * WN) lscale[64 * WN + tid] = g.b_scale[e * g.N + min(n0 + tid, g.N - 1)];
     }
 };
@@ -336,12 +350,15 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
     int32_t* mine = reinterpret_cast<int32_t*>(buffer) + (w % kPer) * kSums;
     constexpr int N = Chunk<T>::N;
     const int64_t n = n0 + 64 * wn + 8 * (l & 7);
-    const bool inside = n0 + 64 * WN <= g.N;  // the whole tile's columns
+    int far = 0;  // whether any row of the tile has a far scale
+#pragma unroll
+    for (int i = 0; i < 2 * WN; ++i) far |= __builtin_amdgcn_readfirstlane(lrow[64 * WN + i]);
+    const bool inside = n0 + 64 * WN <= g.N && !far;  // the whole tile's columns, and ordinary scales
     float sb[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sb[i] = lscale[64 * WN + 64 * wn + 8 * (l & 7) + i];
-#pragma unroll
-    for (int i = 0; i < F; ++i) {
+    // one 32-row block; `whole` (a compile-time constant) where all is inside
+    const auto block = [&](int i, auto whole) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -350,14 +367,14 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
                 *reinterpret_cast<i32x4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
             }
         __builtin_amdgcn_wave_barrier();
-        const auto row_out = [&](int r, float sa, i32x4 v0, i32x4 v1, int64_t tr, bool whole) {
+        const auto row_out = [&](float sa, i32x4 v0, i32x4 v1, int64_t tr) {
             T* c = (T*)g.C + (lo + tr) * g.ldc + n;
             typename Chunk<T>::V o[8 / N];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
+            for (int x = 0; x < 8; ++x) o[x / N][x % N] = scaled<D, !whole.value>(x < 4 ? v0[x & 3] : v1[x & 3], sa, sb[x]);
 #pragma unroll
             for (int x = 0; x < 8 / N; ++x) {
-                if (whole)
+                if (whole.value)
                     *reinterpret_cast<typename Chunk<T>::U*>(c + x * N) = o[x];
                 else if (n + x * N < g.N)
                     chunk_store(c + x * N, g.N - n - x * N, o[x]);
@@ -365,7 +382,7 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
         };
         const int32_t* at = mine + (l >> 3) * kBigRow + 8 * (l & 7);
         const int tr0 = 32 * (2 * i + wm) + (l >> 3);
-        if (inside) {
+        if (whole.value) {
             i32x4 v[4][2];
             int r[4];
             float sa[4];
@@ -378,17 +395,24 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (r[q] >= 0) row_out(r[q], sa[q], v[q][0], v[q][1], tr0 + 8 * q, true);
+                if (r[q] >= 0) row_out(sa[q], v[q][0], v[q][1], tr0 + 8 * q);
         } else {
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 const i32x4 v0 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow);
                 const i32x4 v1 = *reinterpret_cast<const i32x4*>(at + 8 * q * kBigRow + 4);
                 const int r = lrow[tr0 + 8 * q];
-                if (r >= 0) row_out(r, lscale[tr0 + 8 * q], v0, v1, tr0 + 8 * q, false);
+                if (r >= 0) row_out(lscale[tr0 + 8 * q], v0, v1, tr0 + 8 * q);
             }
         }
         __builtin_amdgcn_wave_barrier();
+    };
+    if (inside) {
+#pragma unroll
+        for (int i = 0; i < F; ++i) block(i, std::true_type());
+    } else {
+#pragma unroll
+        for (int i = 0; i < F; ++i) block(i, std::false_type());
     }
 }
 
@@ -517,7 +541,7 @@ template <class D, int WN, int ST, bool ONCE>
 __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(GemmArgs g) {
     constexpr int kBytes = 64 * WN * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
-    __shared__ int32_t lrow[64 * WN];       // row of A of every row of the tile, or -1
+    __shared__ int32_t lrow[64 * WN + 2 * WN];  // row of A of every row of the tile, or -1; words of the waves
     __shared__ float lscale[2 * 64 * WN];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     int e;
@@ -621,7 +645,7 @@ template <class D>
 __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
     constexpr int kBytes = 128 * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
-    __shared__ int32_t lrow[128];
+    __shared__ int32_t lrow[128 + 4];
     __shared__ float lscale[2 * 128];
     const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
@@ -767,15 +791,21 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_thin(GemmArgs g) {
         const float* sb = g.b_scale + e * g.N + n;
         T* c = (T*)g.C + p * g.ldc + n;
         typedef T V4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-        if (n + 4 <= g.N) {
-            V4 o;
+        const auto out = [&](auto far) {
+            if (n + 4 <= g.N) {
+                V4 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = scaled<D>(sum[i], sa, sb[i]);
-            *reinterpret_cast<V4*>(c) = o;
-        } else {
-            for (int i = 0; i < 3; ++i)
-                if (n + i < g.N) c[i] = scaled<D>(sum[i], sa, sb[i]);
-        }
+                for (int i = 0; i < 4; ++i) o[i] = scaled<D, far.value>(sum[i], sa, sb[i]);
+                *reinterpret_cast<V4*>(c) = o;
+            } else {
+                for (int i = 0; i < 3; ++i)
+                    if (n + i < g.N) c[i] = scaled<D, far.value>(sum[i], sa, sb[i]);
+            }
+        };
+        if (__any(far_scale(sa)))
+            out(std::true_type());
+        else
+            out(std::false_type());
     }
 }
 

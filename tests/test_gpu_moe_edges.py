@@ -9,6 +9,8 @@ from gpu_util import say
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
+
 
 def codes(g, *shape, most=127):
     return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int8)
@@ -16,6 +18,35 @@ def codes(g, *shape, most=127):
 
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ------------------------------------------------------------------ scales at the ends of the range
+# one kernel each: 16 x 16, 16 x 32, 32 x 32, 32 x 64 tiles, 128 x 128 with four and two steps in LDS, 256 x 256, and
+# rows of fewer than 16 bytes
+@pytest.mark.parametrize("M,N,K", [(4, 40, 64), (8, 5000, 64), (20, 5000, 64), (60, 5000, 64), (700, 800, 64),
+                                   (2100, 2100, 16), (5000, 5000, 16), (4, 40, 9)])
+def test_large_scales_do_not_overflow_on_the_way(M, N, K):
+    """Sums times a_scale beyond fp32's range, and a b_scale that brings the product back into it: three fp32
+    roundings and nothing else.  The other way round, and both small, too."""
+    say("large scales", M, N, K)
+    g = gen(M)
+    A, B = codes(g, M, K), codes(g, N, K)
+    A[1], B[2] = 127, 127
+    sa = torch.rand(M, generator=g, device="cuda") + 0.5
+    sb = torch.rand(N, generator=g, device="cuda") + 0.5
+    sums = A.double() @ B.double().t()
+    for p, q in ((120.0, -60.0), (127.0, -30.0), (-60.0, 120.0), (-100.0, 30.0), (-126.0, 126.0), (-90.0, -40.0)):
+        for rows in (slice(None), slice(0, M, 3)):  # all rows, and some among ordinary ones
+            a = sa.clone()
+            a[rows] *= 2.0 ** p
+            b = sb * 2.0 ** q
+            want = sums * a.double()[:, None] * b.double()
+            got = sp.gemm_i8(A, a, B, b, dtype=torch.float32).double()
+            big = want.abs() >= 2.0 ** 128 * (1 - 4 * U)
+            assert not (got.isinf() & ~big).any() and not got.isnan().any()
+            # below the normal range each of three roundings is off by half of 2^-149, what follows scales it by b
+            tol = 3.001 * U * want.abs() + 2.0 ** -149 * (2 + b.double())
+            assert ((got - want).abs() <= tol)[~big].all(), (p, q)
 
 
 # ------------------------------------------------------------------ operands of another stream
