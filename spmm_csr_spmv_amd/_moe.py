@@ -110,6 +110,11 @@ def _call(body, t, stream, *args):
     return result
 
 
+def _int32(v):
+    """v as the C calls take it; what int32 cannot hold becomes its nearest end (ctypes would cut off the high bits)."""
+    return max(-2 ** 31, min(int(v), 2 ** 31 - 1))
+
+
 @functools.lru_cache(maxsize=256)
 def _sort_bytes(n, num_experts):
     size = _sz()
@@ -124,7 +129,7 @@ def moe_sort(ids, num_experts, work=None, stream=None):
     whose id is outside [0, num_experts) is routed nowhere, its pos is -1.  `work` is
     a uint8 device tensor of moe_sort_bufsize bytes apart from ids (allocated when None)."""
     _whole(ids, _I32, ids.dim(), "ids")
-    n, num_experts = ids.numel(), int(num_experts)
+    n, num_experts = ids.numel(), _int32(num_experts)
     need = _sort_bytes(n, num_experts)
     return _call(_sort, ids, stream, ids, n, num_experts, need, work)
 
@@ -363,7 +368,7 @@ def _moe_gemm(raw, A, a_scale, B, b_scale, offsets, src, slots, out, dtype, ldb,
     out = _product_out(out, dtype, S, N, A, B, a_scale, b_scale, offsets, src)
     _check("moe_gemm_i8",
            lib().moe_gemm_i8(S, E, N, K, A.data_ptr(), rows, _rows(A, "A"), a_scale.data_ptr(),
-                             src.data_ptr() if src is not None else None, int(slots), B.data_ptr(), ldb, strideb,
+                             src.data_ptr() if src is not None else None, _int32(slots), B.data_ptr(), ldb, strideb,
                              b_scale.data_ptr(), offsets.data_ptr(), _TYPES[out.dtype], out.data_ptr(),
                              _rows(out, "out"), raw))
     return out

@@ -135,6 +135,25 @@ def test_stream_given_in_a_capture():
         assert torch.equal(out, want), n
 
 
+# ------------------------------------------------------------------ numbers beyond 32 bits
+def test_counts_beyond_32_bits_are_not_cut():
+    say("counts")
+    ids = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    for n in (2 ** 32 + 5, 2 ** 32, -2 ** 32 + 5, 2 ** 31):
+        with pytest.raises(sp.SparseError) as e:
+            sp.moe_sort(ids, n)
+        assert e.value.code == 5
+    A, s = torch.ones(3, 16, dtype=torch.int8, device="cuda"), torch.tensor([1.0, 2.0, 3.0], device="cuda")
+    B, b = torch.ones(1, 4, 16, dtype=torch.int8, device="cuda"), torch.ones(1, 4, device="cuda")
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    src = torch.tensor([5, 4, 1], dtype=torch.int32, device="cuda")
+    got = sp.moe_gemm_i8(A, s, B, b, off, src=src, slots=2 ** 32 + 2, dtype=torch.float32)
+    assert (got == 16).all()  # src // slots is 0 everywhere
+    with pytest.raises(sp.SparseError) as e:
+        sp.moe_gemm_i8(A, s, B, b, off, src=src, slots=-2 ** 32 + 2)
+    assert e.value.code == 2
+
+
 # ------------------------------------------------------------------ sums through a wave's own LDS
 # each streaming tile (16 x 16, 16 x 32, 32 x 32, 32 x 64) with many steps a wave, aligned and not
 @pytest.mark.parametrize("gap", [0, 1])

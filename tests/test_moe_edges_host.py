@@ -23,3 +23,13 @@ def test_sort_refuses_a_workspace_over_its_arrays():
     for name, a in at.items():
         for work in (a, a + nbytes[name] - 4, a - size.value + 4):
             assert call(work) == WORKSPACE, (name, work - a)
+
+
+def test_numbers_beyond_32_bits_keep_their_size():
+    """What a C int cannot hold is refused as too large or too small, not taken for its low 32 bits."""
+    from spmm_csr_spmv_amd._moe import _int32
+
+    for v in (0, 1, -1, 1024, 2 ** 31 - 1, -2 ** 31):
+        assert _int32(v) == v
+    for v in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, 10 ** 30):
+        assert _int32(v) == 2 ** 31 - 1 and _int32(-v) == -2 ** 31
