@@ -74,20 +74,41 @@ def _rows(t, name):
 
 
 def _reach(t):
-    """Bytes from a tensor's first element to behind its last (row gaps count as used)."""
+    """Bytes from a tensor's first element to behind its last, gaps included."""
     if t.is_contiguous():
         return t.nbytes
     return (sum((n - 1) * d for n, d in zip(t.shape, t.stride())) + 1) * t.element_size() if t.numel() else 0
 
 
+def _line(t):
+    """(row distance, row length) in bytes of a tensor whose rows are contiguous, equally far apart and disjoint;
+    (0, 0) where they are not."""
+    ld, size = 0, t.element_size()
+    for n, d in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n > 1:
+            if ld and d % ld:
+                return 0, 0
+            ld = ld or d
+    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1) or ld < t.shape[-1]:
+        return 0, 0
+    return ld * size, t.shape[-1] * size
+
+
+def _columns_apart(a, b):
+    """Whether two tensors lie in different columns of rows of one distance, as two parts of one buffer do."""
+    (la, wa), (lb, wb) = _line(a), _line(b)
+    between = (b.data_ptr() - a.data_ptr()) % la if la else 0
+    return la == lb > 0 and between >= wa and between + wb <= la
+
+
 def _apart(out, name, *inputs):
-    """Refuses an output whose bytes overlap an input's."""
+    """Refuses an output that may share bytes with an input."""
     lo = out.data_ptr()
     hi = lo + _reach(out)
     for t in inputs:
         if t is not None:
             b = t.data_ptr()
-            if b < hi and lo < b + _reach(t):
+            if b < hi and lo < b + _reach(t) and not _columns_apart(out, t):
                 raise ValueError("%s overlaps an input" % name)
 
 

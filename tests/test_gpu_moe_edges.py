@@ -135,6 +135,56 @@ def test_stream_given_in_a_capture():
         assert torch.equal(out, want), n
 
 
+# ------------------------------------------------------------------ operands inside one buffer
+def test_operands_in_columns_of_one_buffer():
+    """Inputs and outputs that are disjoint columns of one buffer do not overlap."""
+    say("columns of one buffer")
+    T, H = 40, 24
+    pos = torch.arange(T, device="cuda", dtype=torch.int32).flip(0).view(T, 1).contiguous()
+    w = torch.rand(T, 1, device="cuda")
+    for a, b in ((0, H), (H + 3, 0)):  # input before the output and behind it
+        whole = torch.randn(T, 2 * H + 3, device="cuda")
+        x, out = whole[:, a:a + H], whole[:, b:b + H]
+        xc, before = x.clone(), whole.clone()
+        sp.moe_dispatch(x, pos, out=out)
+        assert torch.equal(out, xc.flip(0))
+        sp.moe_combine(x, pos, w, out=out)
+        assert torch.equal(out, w * xc.flip(0))
+        _, dw = sp.moe_combine_backward(x, xc, pos, w, dYs=out)
+        assert torch.equal(out, (w * xc).flip(0))
+        keep = torch.ones(2 * H + 3, dtype=torch.bool, device="cuda")
+        keep[b:b + H] = False
+        assert torch.equal(whole[:, keep], before[:, keep])
+    both = torch.randint(-100, 101, (T, 64), device="cuda", dtype=torch.int8)
+    A, B = both[:, :31], codes(gen(5), 16, 31)
+    ones = torch.ones(T, device="cuda")
+    want = A.double() @ B.double().t()
+    sp.gemm_i8(A, ones, B, ones[:16], out=both.view(torch.float16)[:, 16:32])  # bytes 32 .. 63 of every row
+    assert torch.equal(both.view(torch.float16)[:, 16:32], want.to(torch.float16))
+    # codes beside the rows they are made of
+    x = torch.randn(T, 16, device="cuda")
+    wide = torch.zeros(T, 20, device="cuda")
+    wide[:, :16] = x
+    q, s = sp.quantize_rows_i8(wide[:, :16], q=wide.view(torch.int8)[:, 64:])
+    assert torch.equal(q, sp.quantize_rows_i8(x)[0]) and torch.equal(wide[:, :16], x)
+
+
+def test_operands_that_share_bytes_are_refused():
+    say("shared bytes")
+    T, H = 40, 24
+    pos = torch.arange(T, device="cuda", dtype=torch.int32).view(T, 1)
+    whole = torch.zeros(T, 2 * H, device="cuda")
+    x = whole[:, :H]
+    for out in (whole[:, H - 1:2 * H - 1],                       # one column of each row
+                whole.view(-1)[5:5 + T * H].view(T, H),          # another row distance
+                whole.view(-1).as_strided((T - 1, H), (2 * H, 1), 2 * H - 3)):  # over a row's end into the next
+        with pytest.raises(ValueError, match="overlaps"):
+            sp.moe_dispatch(x, pos, out=out)
+    with pytest.raises(ValueError, match="overlaps"):  # the place list inside the output's rows
+        ints = torch.zeros(T * H, dtype=torch.int32, device="cuda")
+        sp.moe_combine(x, ints[:T].view(T, 1), out=ints.view(torch.float32).view(T, H))
+
+
 # ------------------------------------------------------------------ numbers beyond 32 bits
 def test_counts_beyond_32_bits_are_not_cut():
     say("counts")
