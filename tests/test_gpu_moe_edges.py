@@ -223,3 +223,78 @@ def test_streaming_tiles_of_many_steps(M, N, K, gap):
     for n in range(5):
         got = sp.gemm_i8(A, ones[:M], B, ones[:N], dtype=torch.float32)
         assert torch.equal(got.double(), want), n
+
+
+# ------------------------------------------------------------------ more work than workgroups
+# T behind 2^20 workgroups of 16, 4 and 1 tokens (the gradient: the same with twice the row), and rows of one element
+@pytest.mark.parametrize("T,H,dtype", [((1 << 24) + 51, 4, torch.float32), ((1 << 24) + 33, 1, torch.bfloat16),
+                                       ((1 << 22) + 77, 132, torch.float32), ((1 << 22) + 5, 137, torch.bfloat16),
+                                       ((1 << 20) + 777, 516, torch.float32), ((1 << 20) + 1, 1040, torch.float16),
+                                       ((1 << 20) + 300, 1088, torch.bfloat16)])
+def test_rows_in_several_rounds(T, H, dtype):
+    say("rows in rounds", T, H, dtype)
+    g = gen(T)
+    X = torch.randint(-8, 9, (T, H), generator=g, device="cuda", dtype=torch.int8).to(dtype)
+    X[:, 0] = (torch.arange(T, device="cuda") % 61).to(dtype)  # neighbours, and rows a round apart, differ
+    pos = torch.randperm(T, generator=g, device="cuda").to(torch.int32).view(T, 1)
+    at = pos.view(-1).long()
+    w = torch.randint(1, 4, (T, 1), generator=g, device="cuda").float()
+    Xs = torch.full_like(X, -99)
+    sp.moe_dispatch(X, pos, out=Xs)
+    assert torch.equal(Xs[at], X)
+    Y = torch.full_like(X, -99)
+    sp.moe_combine(Xs, pos, w, out=Y)
+    assert torch.equal(Y, w.to(dtype) * X)  # small whole numbers: exact
+    dXs, dw = sp.moe_combine_backward(X, Xs, pos, w, dYs=Y)
+    assert torch.equal(dXs[at], w.to(dtype) * X)
+    for b in range(0, T, 1 << 22):  # sums below 2^24: exact
+        x = X[b:b + (1 << 22)].float()
+        assert torch.equal(dw[b:b + (1 << 22), 0], (x * x).sum(1)), b
+
+
+# rows behind 2^20 workgroups of 16, 4 and 1 rows, in rows of a few elements, one chunk, held and read again
+@pytest.mark.parametrize("rows,K,dtype", [((1 << 24) + 100, 1, torch.bfloat16), ((1 << 24) + 17, 11, torch.float32),
+                                          ((1 << 22) + 9, 520, torch.bfloat16), ((1 << 20) + 555, 2056, torch.bfloat16),
+                                          ((1 << 20) + 3, 4104, torch.float32)])
+def test_quantised_rows_in_several_rounds(rows, K, dtype):
+    say("quantise in rounds", rows, K, dtype)
+    g = gen(K)
+    X = torch.randint(-126, 127, (rows, K), generator=g, device="cuda", dtype=torch.int8).to(dtype)
+    top = (127 * 2.0 ** (torch.arange(rows, device="cuda") % 5)).to(dtype)  # scales 1, 2, 4, 8, 16
+    X[:, K // 2] = top
+    q, s = sp.quantize_rows_i8(X)
+    assert torch.equal(s, top.float() / 127)
+    part = max(1, (1 << 28) // K)
+    for b in range(0, rows, part):
+        want = torch.round(X[b:b + part].float() / s[b:b + part, None])
+        assert torch.equal(q[b:b + part].float(), want), b
+
+
+@pytest.mark.parametrize("K", [1, 17])
+def test_tiles_in_several_rounds(K):
+    """More 128 x 128 tiles than workgroups: experts of one row, and a few of one and two blocks of 64."""
+    say("tiles in rounds", K)
+    E, N = 1024, 540000
+    rows = np.ones(E, np.int64)
+    rows[[3, 500]], rows[[0, 1023]], rows[7] = 100, 60, 0
+    offsets = np.concatenate([[0], np.cumsum(rows)])
+    S = int(offsets[-1])
+    g = gen(K)
+    A, B = codes(g, S, K), codes(g, E, N, K)
+    ones = torch.ones(E, N, device="cuda")
+    sa = torch.arange(S, device="cuda").float() % 3 + 1
+    C = sp.moe_gemm_i8(A, sa, B, ones, torch.from_numpy(offsets.astype(np.int32)).cuda(), dtype=torch.float32)
+    for e in range(E):
+        a = slice(offsets[e], offsets[e + 1])
+        want = (A[a].float() @ B[e].float().t()) * sa[a, None]  # whole numbers below 2^24: exact
+        assert torch.equal(C[a], want), e
+
+
+def test_one_row_of_more_tiles_than_workgroups():
+    say("one row in rounds")
+    N = (1 << 29) + 1000
+    g = gen(9)
+    B = codes(g, N, 1)
+    A = torch.full((1, 1), 3, dtype=torch.int8, device="cuda")
+    C = sp.gemm_i8(A, torch.ones(1, device="cuda"), B, torch.ones(N, device="cuda"), dtype=torch.float16)
+    assert torch.equal(C[0], 3 * B[:, 0].half())
