@@ -594,7 +594,8 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  * quantize_rows_i8: every row of X (rows x K, dtype as above, rows ldx apart)
  * to int8 codes with one fp32 scale: a = max |x|, scale = a / 127,
  * q = rint(127 x / a), ties to even, |q| <= 127; |q scale - x| <= a / 254 up to
- * rounding.  A row with a < 2^-119 (its scale would be a denormal) becomes
+ * rounding (of fp32 rows, 127 x and the quotient are rounded to fp32 before rint,
+ * so that a value within 2^-16 of halfway between codes may get either).  A row with a < 2^-119 (its scale would be a denormal) becomes
  * zeros with scale 0; a row that holds an Inf or a NaN becomes zeros with
  * scale NaN, so that every product with it is NaN.  q rows are ldq bytes
  * apart; the bytes between K and ldq keep their contents.

@@ -191,10 +191,10 @@ __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
 // B is the first MFMA operand, so that a lane's four consecutive sums lie in
 // one row of C; the sums go through LDS once more to be stored as whole lines.
 //
-// 8192 x 8192 x 8192 (WN = 4) takes 443 us, 2.48 POP/s; the MFMAs fill 65 % of
-// the cycles and the chip runs at 1.7 GHz under them (one tile alone: 71 % at
-// 2.4 GHz), so that power bounds it.  LDS operand reads take 27 % of them,
-// without conflicts.
+// 8192 x 8192 x 8192 (WN = 4) takes 461 us, 2.39 POP/s (443 to 468 on several
+// cards); the MFMAs fill 65 % of the cycles and the chip runs at 1.7 GHz under them
+// (one tile alone: 71 % at 2.4 GHz), so that power bounds it.  LDS operand reads
+// take 27 % of them, without conflicts.
 constexpr int kBigK = 128;            // bytes of K a step
 constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
 
@@ -570,9 +570,9 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_i8_big(Ge
 // Rows of any alignment and length: the 128 x 128 tiles, with the copies
 // through registers (global_load_lds wants aligned pieces): the next step's
 // loads are in flight while this one is multiplied, and go to the other LDS
-// buffer after it.  8192 x 8192 x 4095 takes 403 us, 1.36 POP/s, bound by the
-// unaligned loads (388 with aligned rows, 327 copied straight to LDS).  A
-// workgroup goes on to the next tile where there are more
+// buffer after it.  8192 x 8192 x 4095 takes 474 us, 1.16 POP/s, bound by the
+// unaligned loads (with aligned rows, copied straight to LDS, these tiles take
+// 313).  A workgroup goes on to the next tile where there are more
 // than the launch has workgroups.
 template <class D, int F>
 __device__ __forceinline__ void staged_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
@@ -671,11 +671,12 @@ __global__ __launch_bounds__(256, 2) void gemm_i8_staged(GemmArgs g) {
 // it puts these together to MFMA operands, through LDS that no other wave
 // uses: nothing waits for another wave before the int32 sums meet, exact in
 // any order.  32 tokens x 8 of 64 experts, 4096 x 2048 (R = 1, C = 2, W = 4):
-// 76 us, 7.0 TB/s of weights, what reads alone reach, with ONCE, non-temporal
-// loads of B where one row tile reads it (86 without).  Operands loaded as the
-// MFMA wants them, sixteen rows of 64 bytes an instruction, took 91 (118
-// non-temporal, which fetched each line twice), 64 x 4096 x 4096 so 12.1 against
-// 9.2, and with unaligned rows three times as long.
+// 72 us where 50 experts get a token (419 MB, 5.8 TB/s), 85 where 63 do (6.2; reads
+// alone reach 7.1), with ONCE, non-temporal loads of B where one row tile reads it
+// (81 and 97 without).  Operands loaded as the MFMA wants them, sixteen rows of 64
+// bytes an instruction, took a sixth longer (and half as long again non-temporal,
+// which fetched each line twice), 64 x 4096 x 4096 so 12.1 against 9.4, and with
+// unaligned rows three times as long.
 template <int R, int C, bool ONCE>
 struct ThinOps {
     static constexpr int kA = 2 * R, kB = 2 * C;
@@ -842,8 +843,12 @@ int launch_thin(bool once, const GemmArgs& g, hipStream_t s) {
                 : launch(gemm_i8_thin<D, R, C, W, false>, g, 16 * R, 16 * C, 64 * W, s);
 }
 
-// Which kernel.  Times are M x N x K, or tokens x choices, experts, K, N with
-// the weights read from memory each time, in us.
+// Which kernel.  Times are medians in us, M x N x K, or tokens x choices, experts,
+// K, N, of calls that follow each other in a graph, on normally distributed codes,
+// with 1 GB of weights in turn, so that they come from memory.  Routing is uneven
+// (scores favour experts with a standard deviation of 0.7, the scores' own being
+// 1) unless it says even (no favour): uneven routing leaves some experts unused
+// where there are few tokens, and makes the tiles of the others higher.
 template <class D>
 int gemm_t(GemmArgs g, hipStream_t s) {
     if (g.a_rows == 0) return SP_OK;  // no row of C has a row of A
@@ -855,54 +860,56 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
     const bool deep = g.K > 2048;
     // Up to 32 rows a matrix: B's rows are (nearly all) read by one row tile,
-    // and non-temporal.  32 x 8, 64, 4096, 2048 76 against 86 otherwise; 160 x 8
-    // (20 rows) 110, 118; 512 x 8 (64 rows) 142, 132; 64 x 2048 x 2048 5.5, 5.0.
-    // Not where unaligned pieces share lines: 96 x 8, 64, 4095, 2048 150, 139.
+    // and non-temporal.  32 x 8, 64, 4096, 2048 72 against 81 otherwise; 160 x 8
+    // (20 rows) 114, 119; 512 x 8 (64 rows) 144, 129; 64 x 2048 x 2048 5.5, 5.0.
+    // Not where unaligned pieces share lines: 96 x 8, 64, 4095, 2048 181, 152.
     const bool once = !any && g.S <= 32 * groups;
     // Few tiles: the smallest ones, or most CUs stay idle.  A step up where 128
-    // or 256 tiles are reached: 1 x 4096 x 4096 16x16 5.8, 16x32 7.3;
-    // 8 x 8192 x 4096 16x16 9.6, 16x32 9.3; 32 x 4096 x 4096 16x32 8.4,
-    // 32x32 9.1; 64 x 4096 x 4096 16x32 10.4, 32x32 9.1, 32x64 11.0;
-    // 128 x 4096 x 4096 32x32 12.6, 32x64 11.5, 128x128 23.7;
-    // 300 x 4096 x 1024 32x32 12, 32x64 14, 128x128 9.4.
+    // or 256 tiles are reached: 1 x 4096 x 4096 16x16 5.8, 16x32 7.4;
+    // 8 x 8192 x 4096 16x16 9.7, 16x32 9.4; 32 x 4096 x 4096 16x32 8.4,
+    // 32x32 9.2; 64 x 4096 x 4096 16x32 10.3, 32x32 9.4, 32x64 11.7;
+    // 128 x 4096 x 4096 32x32 12.4, 32x64 11.5, 128x128 23.4;
+    // 300 x 4096 x 1024 32x32 9.6, 32x64 13.9, 128x128 9.2.
     //
     // Few rows a matrix take them in any number.  One matrix: 16 rows 16x32
-    // (16 x 14336 x 4096 13.6, 32x64 14.2, 128x128 17.5), 32 rows 32x64
-    // (32 x 14336 x 4096 16.0, 128x128 21.3).  Experts: up to 8 rows on the
-    // average, where some have more, 16x32 (32 x 8, 64, 4096, 2048 76, 32x32 81;
-    // 64 x 8 86, 86), up to 16 rows 32x32 (128 x 8 102, 16x32 115, 128x128 114;
-    // 160 x 8 (20 rows) 121, 134, 110).  Shorter sums do not pay their four waves
-    // as long: 96 x 8, 128, 2048, 2048 (6 rows) 16x32 85, 128x128 86; 128 x 8 (8
-    // rows) 96, 89; 17 x 28672 x 2048 32x64 16.5, 128x128 13.9.
+    // (16 x 14336 x 4096 14.7, 32x64 15.3, 128x128 19.9), 32 rows 32x64
+    // (32 x 14336 x 4096 15.9, 32x32 16.5, 128x128 21.2).  Experts: up to 8 rows
+    // on the average, where some have more, 16x32 (32 x 8, 64, 4096, 2048 72,
+    // 32x32 77, 128x128 102; 64 x 8 91, 92, 113), up to 16 rows 32x32 (128 x 8
+    // 104, 16x32 117, 128x128 115; 160 x 8 (20 rows) 116, 136, 114, but even 106,
+    // 145, 121).  Shorter sums do not pay their four waves as long: 96 x 8, 128,
+    // 2048, 2048 (6 rows) 16x32 83, 128x128 88; 128 x 8 (8 rows) 92, 91, but even
+    // 98, 106; 17 x 28672 x 2048 32x64 16.5, 128x128 14.2.
     if (tiles(g, 16, 32) <= 128) return launch_thin<D, 1, 1, 8>(once, g, s);
     if (tiles(g, 16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
         return launch_thin<D, 1, 2, 4>(once, g, s);
     if (tiles(g, 32, 32) <= 256 || (experts && g.S <= 16 * groups && deep))
         return launch_thin<D, 2, 2, 4>(once, g, s);
     // Unaligned rows, whose 128 x 128 tiles are slower, up to 512 tiles:
-    // 256 x 4096 x 4097 30, 128x128 47; 1024 x 1024 x 1023 12.4, 13.3.
+    // 256 x 4096 x 4097 32, 128x128 54; 1024 x 1024 x 1023 13.1, 15.1.
     if (tiles(g, 32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
         return launch_thin<D, 2, 4, 4>(once, g, s);
-    // 8192 x 8192 x 4095 403, with aligned rows 245; 32 x 8, 64, 4095, 2048 117
-    // (thin tiles 112), 96 x 8 119 (139), 24 x 8, 128, 1023, 2047 49 (58).
+    // 8192 x 8192 x 4095 474, with aligned rows 250; 32 x 8, 64, 4095, 2048 119
+    // (thin tiles 107), 96 x 8 134 (152), 24 x 8, 128, 1023, 2047 52 (55).
     if (any) return launch(gemm_i8_staged<D>, g, 128, 128, 256, s);
     // One 128 x 128 tile a CU at most, or tiles that mostly wait for memory: four
-    // steps in LDS.  1024 x 4096 x 4096 26 against 36 with two steps and two
+    // steps in LDS.  1024 x 4096 x 4096 24 against 35 with two steps and two
     // workgroups a CU, and 55 with 256 x 256 tiles; 512 x 8, 64, 4096, 2048 (64
-    // rows) 132, 151, 137; 1024 x 8 (128 rows) 163, 180, 174; 1024 x 2, 8, 4096,
-    // 14336 (256 rows) 226, 223, 193 (but 512 x 2 151, 158, 138); shorter sums 512 x 8, 128, 2048, 1536 (32
-    // rows) 92, 96, 93; 16384 rows of 128 uneven experts, 2048 x 1536 144, 140, 132.
+    // rows) 129, 162, 159; 1024 x 8 (128 rows) 159, 199, 182; 1024 x 2, 8, 4096,
+    // 14336 (256 rows) 222, 228, 187; 512 x 2 (128 rows) 151, 163, 170, but even
+    // 165, 163, 138; shorter sums 512 x 8, 128, 2048, 1536 (32 rows) 90, 93, 94;
+    // 2048 x 8 (128 rows) 144, 144, 130.
     if (once) return launch(gemm_i8_big<D, 2, 4, true>, g, 128, 128, 256, s);
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
         return launch(gemm_i8_big<D, 2, 4, false>, g, 128, 128, 256, s);
-    // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 46, with four steps 53,
+    // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 43, with four steps 47,
     // with 256 x 256 tiles 57.  Also where 256-wide tiles would be empty for a
-    // fifth: 20000 x 2, 16, 512, 300 26, with 256 x 256 34.
+    // fifth: 20000 x 2, 16, 512, 300 25, with 256 x 256 33.
     const int64_t wide = (g.N + 255) / 256 * 256, narrow = (g.N + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
         return launch(gemm_i8_big<D, 2, 2, false>, g, 128, 128, 256, s);
-    // 8192 x 8192 x 4096 245 against 298 with 128 x 128 tiles; 4096 x 4096 x 4096
-    // 64, 77; 4096 x 8, 64, 4096, 2048 (512 rows) 330, 407.
+    // 8192 x 8192 x 4096 250 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
+    // 68, 82; 4096 x 8, 64, 4096, 2048 (512 rows) 341, even 335 against 415.
     return launch(gemm_i8_big<D, 4, 2, false>, g, 256, 256, 512, s);
 }
 

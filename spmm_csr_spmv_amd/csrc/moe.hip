@@ -28,7 +28,7 @@ constexpr int kSortWideE = 512;
 constexpr int kSortOneBlock = 4096;  // up to this many slots one workgroup does everything (6.9 us; two kernels 8.4)
 
 // The floor is bytes that take a microsecond; what the sort takes is its chain
-// of dependent steps: 3.7 us for one token's 8 slots, 3.0 (counts) + 10.2
+// of dependent steps: 3.8 us for one token's 8 slots, 3.0 (counts) + 10.4
 // (placement) for 524288 slots over 128 experts.
 //
 // Workgroups of the two-kernel path: 1024 slots each up to 128 of them (16384
@@ -40,7 +40,7 @@ constexpr int kSortHist = 1 << 17;
 int sort_blocks(int64_t n, int32_t E) {
     if (n <= kSortOneBlock) return 1;
     const int64_t nb = std::min<int64_t>((n + 1023) / 1024, std::max<int64_t>(128, std::min<int64_t>(256, n / 4096)));
-    return (int)std::min<int64_t>(nb, std::max<int64_t>(8, kSortHist / E));
+    return (int)std::min<int64_t>(nb, kSortHist / E);  // at least 128
 }
 
 __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
@@ -212,9 +212,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(const int32_t* 
 // is one, or no row is live) and its bits are zeroed, so that the loads need
 // no branch; its weight counts as zero.
 //
-// Memory bounds all three: 16384 x 4 rows of 4096 bf16 dispatched in 122 us
-// (5.5 TB/s, four fifths writes), combined in 112 (6.0), their gradients formed
-// in 219 (5.5); a copy reaches 5.6 TB/s.
+// Memory bounds all three: 16384 x 4 rows of 4096 bf16 dispatched in 124 us
+// (5.4 TB/s, four fifths writes), combined in 112 (6.0), their gradients formed
+// in 226 (5.3); a copy reaches 5.6 TB/s.
 //
 // A row's last chunk starts at H - N where a whole one does not fit: it then
 // repeats elements of the chunk before it, which are written twice with the

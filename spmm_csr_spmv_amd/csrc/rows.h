@@ -9,7 +9,8 @@ namespace spx {
 
 // A row is cut into 16-byte chunks.  Rows need not be 16-byte aligned: the
 // accesses carry the element's alignment only (the hardware takes them at any
-// address), and the last chunk of a row goes element by element when it is short.
+// address).  Where a whole last chunk does not fit, the row kernels take one that
+// ends with the row, and rows or tiles' edges shorter than a chunk go element by element.
 struct F32 {
     typedef float T;
     static __device__ __forceinline__ float up(float v) { return v; }
