@@ -83,6 +83,8 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 // Row tiles that the experts' rows make (the launch has room for more: it
 // does not know the offsets).  Every wave counts for itself, 64 experts at a time.
+// Offsets whose ranges overlap can make more than the launch has room for, and more
+// than 32 bits count: the bound keeps the loop of gemm_i8_staged below 2^31.
 template <int BM>
 __device__ __forceinline__ uint32_t count_tiles(const GemmArgs& g, int lane) {
     if (!g.offsets) return g.m_tiles;
@@ -92,7 +94,7 @@ __device__ __forceinline__ uint32_t count_tiles(const GemmArgs& g, int lane) {
         expert_rows(g, e0 + lane, a, b);
         n += __builtin_amdgcn_readlane(wave_scan(row_tiles_of<BM>(b - a)), 63);
     }
-    return n;
+    return min(n, g.m_tiles);
 }
 
 // Row tile number `tile` of the launch: expert e and rows [lo, hi) of its

@@ -298,3 +298,20 @@ def test_one_row_of_more_tiles_than_workgroups():
     A = torch.full((1, 1), 3, dtype=torch.int8, device="cuda")
     C = sp.gemm_i8(A, torch.ones(1, device="cuda"), B, torch.ones(N, device="cuda"), dtype=torch.float16)
     assert torch.equal(C[0], 3 * B[:, 0].half())
+
+
+@pytest.mark.parametrize("S,N,K", [(300, 520, 40), (300, 520, 48), (9000, 300, 33), (9000, 600, 64)])
+def test_overlapping_offsets_end(S, N, K):
+    """Every other one of 1024 experts claims all rows: what C holds is unspecified, but the tiles are no more than the
+    launch has room for and nothing around C is written."""
+    say("overlapping offsets", S, N, K)
+    E = 1024
+    g = gen(K)
+    A, B = codes(g, S, K), codes(g, E, N, K)
+    offsets = torch.arange(E + 1, device="cuda", dtype=torch.int32) % 2 * S
+    whole = torch.full((S + 2, N + 5), -7.0, device="cuda")
+    out = whole[1:-1, 2:2 + N]
+    sp.moe_gemm_i8(A, torch.ones(S, device="cuda"), B, torch.ones(E, N, device="cuda"), offsets, out=out)
+    assert (out == out.round()).all()  # sums, or what was there
+    out.fill_(-7.0)
+    assert (whole == -7.0).all()
