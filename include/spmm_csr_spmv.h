@@ -594,11 +594,12 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  * quantize_rows_i8: every row of X (rows x K, dtype as above, rows ldx apart)
  * to int8 codes with one fp32 scale: a = max |x|, scale = a / 127,
  * q = rint(127 x / a), ties to even, |q| <= 127; |q scale - x| <= a / 254 up to
- * rounding (of fp32 rows, 127 x and the quotient are rounded to fp32 before rint,
- * so that a value within 2^-16 of halfway between codes may get either).  A row with a < 2^-119 (its scale would be a denormal) becomes
- * zeros with scale 0; a row that holds an Inf or a NaN becomes zeros with
- * scale NaN, so that every product with it is NaN.  q rows are ldq bytes
- * apart; the bytes between K and ldq keep their contents.
+ * rounding (of fp32 rows, 127 x and the quotient are rounded to fp32 before
+ * rint, so that a value within 2^-16 of halfway between codes may get either).
+ * A row with a < 2^-119 (its scale would be a denormal) becomes zeros with
+ * scale 0; a row that holds an Inf or a NaN becomes zeros with scale NaN, so
+ * that every product with it is NaN.  q rows are ldq bytes apart; the bytes
+ * between K and ldq keep their contents.
  *
  * gemm_i8: C[m, n] = a_scale[m] b_scale[n] sum_k A[m, k] B[n, k], with A M x K
  * and B N x K, K-contiguous rows (the layout of a linear layer's weight), a
@@ -621,7 +622,7 @@ int moe_combine_backward(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t
  *
  * Alignment: none needed for A and B (C and the scales: the element's).  When
  * A, B, lda, ldb (and strideb) are multiples of 16 bytes the kernels for
- * aligned rows run, up to 1.7 times as fast; they read the rows in 16-byte
+ * aligned rows run, up to 1.9 times as fast; they read the rows in 16-byte
  * pieces, so that up to 15 bytes behind a row's last (K rounded up to 16) are
  * read and ignored, also behind the last row: within its 16-byte piece, never
  * past it.  Other rows are read exactly.

@@ -167,9 +167,12 @@ __device__ __forceinline__ i32x4 load_short(const int8_t* row, int64_t k, int64_
 __device__ __forceinline__ bool far_scale(float sa) { return fabsf(sa) > 0x1p96f; }
 template <class D, bool FAR>
 __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
-    if (!FAR) return D::down((float)sum * sa * sb);
-    const bool far = far_scale(sa);
-    return D::down((float)sum * (far ? sa * 0x1p-32f : sa) * sb * (far ? 0x1p32f : 1.0f));
+    // The product is an fp32 number before it is rounded to C's type: left to itself
+    // the compiler fuses the two for fp16 in some tiles and not in others, and the
+    // last bit then depends on where in C a value stands.
+#pragma clang fp contract(off)
+    if (FAR && far_scale(sa)) return D::down((float)sum * (sa * 0x1p-32f) * sb * 0x1p32f);
+    return D::down((float)sum * sa * sb);
 }
 
 // ---------------------------------------------------------------------------

@@ -49,6 +49,25 @@ def test_large_scales_do_not_overflow_on_the_way(M, N, K):
             assert ((got - want).abs() <= tol)[~big].all(), (p, q)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(4, 4000, 64), (8, 5000, 64), (20, 5000, 64), (60, 5003, 64), (700, 1000, 64),
+                                   (2100, 2100, 128), (3000, 5001, 16), (600, 2500, 9), (3000, 4000, 33)])
+def test_products_are_rounded_alike_everywhere(M, N, K, dtype):
+    """The float of a sum times a_scale times b_scale in fp32, then rounded: the same bits wherever in C a value stands,
+    in whole tiles and at their edges, and beside rows with large scales."""
+    say("rounding", M, N, K, dtype)
+    g = gen(M)
+    A, B = codes(g, M, K), codes(g, N, K)
+    a = torch.randn(M, generator=g, device="cuda").exp()
+    b = torch.randn(N, generator=g, device="cuda") * 0.01
+    want = ((A.double() @ B.double().t()).float() * a[:, None] * b).to(dtype)
+    assert torch.equal(sp.gemm_i8(A, a, B, b, dtype=dtype), want)
+    a[M // 3] = 2.0 ** 110
+    got = sp.gemm_i8(A, a, B, b, dtype=dtype)
+    others = torch.arange(M, device="cuda") != M // 3
+    assert torch.equal(got[others], want[others])
+
+
 # ------------------------------------------------------------------ operands of another stream
 def busy(stream):
     """Tens of milliseconds of work on `stream`."""
