@@ -163,7 +163,7 @@ __device__ __forceinline__ i32x4 load_short(const int8_t* row, int64_t k, int64_
 // the result does not (rows whose largest value is near the type's).  Such a scale
 // goes in times 2^-32 and the result is multiplied by 2^32, both exact.  That path
 // (FAR) is taken where a tile, or the rows of a wave, hold such a scale: the last
-// factor on every product made 8192 x 8192 x 4096 take 248 us, without 243, so 244.
+// factor on every product made 8192 x 8192 x 4096 take 248 us, without 240, so 240.
 __device__ __forceinline__ bool far_scale(float sa) { return fabsf(sa) > 0x1p96f; }
 template <class D, bool FAR>
 __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
@@ -355,9 +355,7 @@ __device__ __forceinline__ void big_out(const GemmArgs& g, const i32x16 (&acc)[F
     int32_t* mine = reinterpret_cast<int32_t*>(buffer) + (w % kPer) * kSums;
     constexpr int N = Chunk<T>::N;
     const int64_t n = n0 + 64 * wn + 8 * (l & 7);
-    int far = 0;  // whether any row of the tile has a far scale
-#pragma unroll
-    for (int i = 0; i < 2 * WN; ++i) far |= __builtin_amdgcn_readfirstlane(lrow[64 * WN + i]);
+    const bool far = __any(lrow[64 * WN + (l & (2 * WN - 1))]);  // whether any row of the tile has a far scale
     const bool inside = n0 + 64 * WN <= g.N && !far;  // the whole tile's columns, and ordinary scales
     float sb[8];
 #pragma unroll
