@@ -578,6 +578,7 @@ int bsr_spmm(int64_t mb, int64_t kb, int32_t bs, int64_t nnzb,
  */
 enum { SP_F32 = 0, SP_BF16 = 1, SP_F16 = 2 }; /* element types */
 enum { SP_MOE_MAX_EXPERTS = 1024 };
+enum { SP_ACT_SILU = 0, SP_ACT_GELU_TANH = 1 }; /* activations of the gated products */
 
 int moe_sort_bufsize(int64_t n, int32_t num_experts, size_t* bytes);
 int moe_sort(int64_t n, int32_t num_experts, const int32_t* ids, int32_t* offsets, int32_t* src, int32_t* pos,
@@ -640,6 +641,104 @@ int moe_gemm_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8
                 const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
                 int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t c_type, void* C, int64_t ldc,
                 void* stream);
+
+/* --------------------------------------------------------- gated products in 8-bit integers
+ * gated_i8, moe_gated_i8: both projections of a gated feed-forward block, its activation and
+ * their product in one kernel.  B (of each expert) has 2 N rows: N of the gate, then N of the
+ * other projection, b_scale likewise; with g and u the products that gemm_i8 (moe_gemm_i8)
+ * would give at columns n and N + n, as fp32 numbers,
+ *   C[p, n] = a(g) u,  a(g) = g / (1 + exp(-p(g)))
+ *   SP_ACT_SILU       p(g) = g
+ *   SP_ACT_GELU_TANH  p(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3)
+ * in fp32, rounded once to c_type.  Everything else (C is M x N or S x N, sources, offsets,
+ * rows that keep their contents, alignment, errors) is as for gemm_i8 and moe_gemm_i8;
+ * SP_ERR_UNSUPPORTED also for another act.
+ */
+int gated_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B,
+             int64_t ldb, const float* b_scale, int32_t act, int32_t c_type, void* C, int64_t ldc, void* stream);
+int moe_gated_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
+                 const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
+                 int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t act, int32_t c_type, void* C,
+                 int64_t ldc, void* stream);
+
+/* --------------------------------------------------------- products of experts in 16 bits, with gradients
+ * moe_gemm: C[p, n] = sum_k A[r, k] B[e, n, k], rows, sources and offsets as for moe_gemm_i8, all of
+ * dtype SP_BF16 or SP_F16, sums in fp32, rounded once.  offsets NULL: one matrix (num_experts 1)
+ * over all S rows.
+ *
+ * moe_gated: C[p, n] = a(g) u as for moe_gated_i8, of g and u in fp32.  With pre (S x 2 N, may be
+ * NULL) the pre-activations [g u] of every row that is written are kept there, rounded to dtype, for
+ * the gradient.
+ *
+ * moe_gemm_backward: from dC (S x N): dA[p] = sum_n dC[p, n] B[e, n] (S x K, by sorted row: with
+ * sources, moe_combine adds up a token's) and dB[e] = sum over e's rows p of dC[p]^T A[r] (N x K a
+ * matrix, zeros for an expert without rows).  Either may be NULL and is then not formed (nor is B, or
+ * A, read).  dA has a row for every p below offsets[num_experts]; rows behind keep their contents.
+ * A row whose source is outside [0, a_rows) counts as a row of zeros in dB.
+ *
+ * moe_gated_backward: the same from dH (S x N) and pre (S x 2 N, as moe_gated left it):
+ * dpre = [dH u a'(g)  dH a(g)], formed in fp32 and rounded to dtype for the matrix cores; dA and dB
+ * (2 N x K a matrix) are those of moe_gemm_backward for dpre.
+ *
+ * Sums over rows are formed in a fixed order: results are reproducible.  work: *_bufsize() bytes (0:
+ * NULL is fine), 16-byte aligned; its contents on entry do not matter; calls that share it must not
+ * overlap.  Rows need 2-byte alignment only, any length and any distance; where the operands' addresses and
+ * distances are multiples of 16 bytes faster kernels run, which may read (and ignore) up to 15 bytes behind a row's
+ * last, within its 16-byte piece.  Outputs must not overlap inputs or one another.  None of these calls allocates or
+ * synchronises; all can be captured.
+ * Errors: SP_ERR_NULL, SP_ERR_SIZE (S above INT32_MAX - 1023, a distance below a row's length),
+ * SP_ERR_UNSUPPORTED (dtype, act, N or K above 2^29, num_experts, alignment), SP_ERR_WORKSPACE, SP_ERR_HIP.
+ */
+int moe_gemm(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, const void* A, int64_t a_rows,
+             int64_t lda, const int32_t* src, int32_t slots, const void* B, int64_t ldb, int64_t strideb,
+             const int32_t* offsets, void* C, int64_t ldc, void* stream);
+int moe_gemm_backward_bufsize(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, size_t* bytes);
+int moe_gemm_backward(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, const void* dC, int64_t ldc,
+                      const void* A, int64_t a_rows, int64_t lda, const int32_t* src, int32_t slots, const void* B,
+                      int64_t ldb, int64_t strideb, const int32_t* offsets, void* dA, int64_t ldda, void* dB,
+                      int64_t lddb, int64_t stridedb, void* work, size_t work_bytes, void* stream);
+int moe_gated(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, const void* A, int64_t a_rows,
+              int64_t lda, const int32_t* src, int32_t slots, const void* B, int64_t ldb, int64_t strideb,
+              const int32_t* offsets, int32_t act, void* pre, int64_t ldp, void* C, int64_t ldc, void* stream);
+int moe_gated_backward_bufsize(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, size_t* bytes);
+int moe_gated_backward(int64_t S, int32_t num_experts, int64_t N, int64_t K, int32_t dtype, int32_t act, const void* dH,
+                       int64_t ldh, const void* pre, int64_t ldp, const void* A, int64_t a_rows, int64_t lda,
+                       const int32_t* src, int32_t slots, const void* B, int64_t ldb, int64_t strideb,
+                       const int32_t* offsets, void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t stridedb,
+                       void* work, size_t work_bytes, void* stream);
+
+/* --------------------------------------------------------- root-mean-square norm
+ * rms_norm: for every row of X (rows x H, dtype): s = X + residual, rounded to dtype and stored in
+ * sum (without a residual, which may be NULL, s = X, and sum may be NULL),
+ *   Y = s i weight,  i = 1 / sqrt(mean(s^2) + eps)
+ * in fp32, rounded once.  weight: H values of w_type, which is dtype or SP_F32; NULL: ones.
+ * eps >= 0.  A sum of squares beyond fp32's range is formed again from scaled values, so that i is right
+ * for all finite rows whose root mean square and eps are not both denormal.  sum may be X or residual themselves (the
+ * same address and distance); other outputs must not overlap inputs or one another.
+ *
+ * rms_norm_i8: Y as int8 codes q with a scale per row, as quantize_rows_i8 makes them of the
+ * unrounded Y (same rules for tiny rows, Inf and NaN, same layout): what gemm_i8, gated_i8 and
+ * moe_gated_i8 read.  The codes are those of s weight (rounded to fp32), from which Y differs by the row's i.
+ *
+ * rms_norm_backward: from dY and the stored sum (X without a residual), with n = s i:
+ *   dX = i (dY weight - n mean(dY weight n)) + dsum    (dsum, the sum's own gradient, may be NULL)
+ * the gradient of X and of residual alike, in fp32, rounded once; and dweight[h] = sum over rows of
+ * dY n (H fp32 values, in a fixed order; NULL: not wanted; zeros when rows is 0).  work: as
+ * rms_norm_backward_bufsize() says where dweight is wanted, 16-byte aligned; calls that share it must not overlap.
+ *
+ * Rows need the element's alignment only, any length and any distance >= H.  None of these calls allocates or
+ * synchronises; all are deterministic and can be captured.
+ * Errors: SP_ERR_NULL, SP_ERR_SIZE, SP_ERR_UNSUPPORTED (types, eps, alignment), SP_ERR_WORKSPACE, SP_ERR_HIP.
+ */
+int rms_norm(int64_t rows, int64_t H, int32_t dtype, const void* X, int64_t ldx, const void* residual, int64_t ldr,
+             const void* weight, int32_t w_type, float eps, void* sum, int64_t lds, void* Y, int64_t ldy, void* stream);
+int rms_norm_i8(int64_t rows, int64_t H, int32_t dtype, const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                const void* weight, int32_t w_type, float eps, void* sum, int64_t lds, int8_t* q, int64_t ldq,
+                float* scale, void* stream);
+int rms_norm_backward_bufsize(int64_t rows, int64_t H, int32_t dtype, size_t* bytes);
+int rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const void* dY, int64_t lddy, const void* sum, int64_t lds,
+                      const void* weight, int32_t w_type, float eps, const void* dsum, int64_t ldd, void* dX,
+                      int64_t lddx, float* dweight, void* work, size_t work_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,8 +7,11 @@ accumulate), CSR -> BSR with a fill-ratio gate, BSR SpMV, windowed rows
 (WCSR) with a windowed SpMM on MFMA, and a tuning cache; for mixtures of
 experts the sort of tokens by expert, their rows moved there and back with
 weights and gradients, and int8 products with a scale per token and channel,
-over one matrix or one per expert.  All arithmetic runs in the library's HIP kernels; this package only marshals
-torch tensors into the C calls.  There is no CPU fallback:
+over one matrix or one per expert; around them the root-mean-square norm with the
+residual's addition (in the rows' type or in int8, and its gradient), the gated
+feed-forward products in int8 and in 16 bits and the experts' products in 16
+bits, with their gradients.  All arithmetic runs in the library's HIP kernels;
+this package only marshals torch tensors into the C calls.  There is no CPU fallback:
 without the built library every call raises.
 """
 from ._binding import (  # noqa: F401
@@ -53,4 +56,15 @@ from ._moe import (  # noqa: F401
     moe_gemm_i8,
     moe_sort,
     quantize_rows_i8,
+)
+from ._layer import (  # noqa: F401
+    gated_i8,
+    moe_gated,
+    moe_gated_backward,
+    moe_gated_i8,
+    moe_gemm,
+    moe_gemm_backward,
+    rms_norm,
+    rms_norm_backward,
+    rms_norm_i8,
 )

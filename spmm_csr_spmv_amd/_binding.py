@@ -34,7 +34,9 @@ EXPORTS = ("sp_status_string", "sp_version", "csr_build_from_coo_bufsize", "csr_
            "csr_to_wcsr_analyze", "csr_to_wcsr_fill", "wcsr_spmm", "sp_plan_view_create",
            "csr_build_from_coo_noalloc", "bsr_spmv_rowwise", "wcsr_tasks_bufsize", "wcsr_tasks_build",
            "wcsr_spmm_tasks_bufsize", "wcsr_spmm_tasks", "moe_sort_bufsize", "moe_sort", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "quantize_rows_i8", "gemm_i8", "moe_gemm_i8")
+           "moe_combine_backward", "quantize_rows_i8", "gemm_i8", "moe_gemm_i8", "gated_i8", "moe_gated_i8", "moe_gemm",
+           "moe_gemm_backward_bufsize", "moe_gemm_backward", "moe_gated", "moe_gated_backward_bufsize",
+           "moe_gated_backward", "rms_norm", "rms_norm_i8", "rms_norm_backward_bufsize", "rms_norm_backward")
 
 
 class SparseError(RuntimeError):
@@ -145,6 +147,22 @@ def lib():
         L.gemm_i8.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _i32, _p, _i64, _p]
         L.moe_gemm_i8.argtypes = [_i64, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i32, _p, _i64, _i64, _p, _p, _i32, _p,
                                   _i64, _p]
+        L.gated_i8.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _i32, _i32, _p, _i64, _p]
+        L.moe_gated_i8.argtypes = [_i64, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i32, _p, _i64, _i64, _p, _p, _i32,
+                                   _i32, _p, _i64, _p]
+        _operands = [_p, _i64, _i64, _p, _i32, _p, _i64, _i64, _p]  # A .. offsets
+        _gradients = [_p, _i64, _p, _i64, _i64, _p, _sz, _p]  # dA .. stream
+        L.moe_gemm.argtypes = [_i64, _i32, _i64, _i64, _i32] + _operands + [_p, _i64, _p]
+        L.moe_gated.argtypes = [_i64, _i32, _i64, _i64, _i32] + _operands + [_i32, _p, _i64, _p, _i64, _p]
+        L.moe_gemm_backward_bufsize.argtypes = [_i64, _i32, _i64, _i64, _i32, ctypes.POINTER(_sz)]
+        L.moe_gated_backward_bufsize.argtypes = [_i64, _i32, _i64, _i64, _i32, ctypes.POINTER(_sz)]
+        L.moe_gemm_backward.argtypes = [_i64, _i32, _i64, _i64, _i32, _p, _i64] + _operands + _gradients
+        L.moe_gated_backward.argtypes = [_i64, _i32, _i64, _i64, _i32, _i32, _p, _i64, _p, _i64] + _operands + _gradients
+        L.rms_norm.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _i32, _f, _p, _i64, _p, _i64, _p]
+        L.rms_norm_i8.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _i32, _f, _p, _i64, _p, _i64, _p, _p]
+        L.rms_norm_backward_bufsize.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+        L.rms_norm_backward.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _i32, _f, _p, _i64, _p, _i64, _p, _p,
+                                        _sz, _p]
         for name in EXPORTS:
             if name not in ("sp_status_string", "sp_version"):
                 getattr(L, name).restype = ctypes.c_int

@@ -1,0 +1,232 @@
+// Products of 16-bit rows (bf16, fp16; fp32 sums) sorted by expert, over one matrix or one per expert,
+// and their gradients:
+//   C = A B_e^T           rows of expert e; gated: a(A G_e^T) (A U_e^T) with B_e = [G_e; U_e]
+//   dA = dC B_e           the same tiles with B's rows as steps of the sum
+//   dB_e = dC^T A         over the expert's rows: both operands' rows are steps of the sum
+// The gated product's gradient is that of a product with 2 N columns, whose dC
+// a kernel of its own forms from dH and the kept pre-activations.
+#include "gemm_tiles.h"
+
+namespace spx {
+
+namespace {
+
+// ---------------------------------------------------------------- dB
+struct GradArgs {
+    int64_t S, M, N;          // rows; rows and columns of a matrix of dB
+    const int8_t* P;          // dC, S x M, rows ldp bytes apart
+    int64_t ldp;
+    const int8_t* Q;          // A, rows of N, ldq bytes apart
+    int64_t q_rows, ldq;
+    const int32_t* src;       // or NULL: row p goes with row p of A
+    FastDiv slots;
+    const int32_t* offsets;   // or NULL: one matrix, rows 0 .. S
+    int32_t E;
+    void* C;                  // dB, rows ldc and experts stridec elements apart
+    int64_t ldc, stridec;
+    float* part;              // splits > 1: [splits][E][M][N]
+    int32_t splits;           // of an expert's rows
+    uint32_t m_tiles, n_tiles;
+};
+
+// Tiles of dB, 64 WN square, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
+// are split and the parts' fp32 sums added afterwards in the order of the splits.
+template <class Kind, class D, int WN, bool STAGED>
+__global__ __launch_bounds__(128 * WN, 2) void gemm_rows_sum(GradArgs g) {
+    constexpr int kBytes = 64 * WN * kBigK, F = WN;
+    __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
+    __shared__ int32_t lrow[64 * WN];
+    const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    const uint32_t per = g.m_tiles * g.n_tiles, total = per * (uint32_t)g.splits * (uint32_t)g.E;
+    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+        const uint32_t v = t, part = v / per, in = v % per;
+        const int e = (int)(part / g.splits), split = (int)(part % g.splits);
+        const int64_t m0 = (int64_t)(in % g.m_tiles) * (64 * WN), n0 = (int64_t)(in / g.m_tiles) * (64 * WN);
+        int a = 0, b = (int)g.S;
+        if (g.offsets) expert_rows(g.offsets, g.E, g.S, e, a, b);
+        a = __builtin_amdgcn_readfirstlane(a);
+        b = __builtin_amdgcn_readfirstlane(b);
+        const int each = (int)(((uint32_t)(b - a) + g.splits * 64u - 1) / (g.splits * 64u)) * 64;
+        const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b), rows = min(each, b - from);
+        if (t != blockIdx.x) __syncthreads();  // the tile before has been stored
+        if (tid < 64 * WN) lrow[tid] = m0 + tid < g.M ? 0 : -1;
+        BigTransposed<WN> sa, sb;
+        sa.place(g.P + from * g.ldp, g.ldp, rows, m0, g.M, w, l);
+        const int8_t* q = g.src ? g.Q : g.Q + from * g.ldq;
+        sb.place(q, g.ldq, g.src ? rows : (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0), n0, g.N, w, l);
+        if (g.src) {
+            sb.src = g.src + from;
+            sb.slots = g.slots;
+            sb.a_rows = g.q_rows;
+        }
+        typename Kind::S16 acc[F][2];
+        const int steps = (rows + 63) >> 6;
+        if constexpr (STAGED) {
+            sa.any(g.P + from * g.ldp, m0, l);
+            sb.any(q, n0, l);
+            staged_sums<Kind, F, true, true>(acc, m, sa, sb, steps, w, l);
+        } else {
+            big_sums<Kind, WN, 2, F, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
+        }
+        const float* none = nullptr;
+        if (g.splits > 1) {
+            const BigOut o{g.part + ((int64_t)split * g.E + e) * g.M * g.N, g.N, g.N, m0, n0, nullptr, 0, 0};
+            big_out<Kind, F32, WN, F, false>(o, acc, b0, b1, a0, a1, lrow, none, w, l);
+        } else {
+            const BigOut o{(typename D::T*)g.C + e * g.stridec, g.ldc, g.N, m0, n0, nullptr, 0, 0};
+            big_out<Kind, D, WN, F, false>(o, acc, b0, b1, a0, a1, lrow, none, w, l);
+        }
+    }
+}
+
+// dB = the parts' sum, in the order of the splits.
+template <class D>
+__global__ __launch_bounds__(256) void add_parts_kernel(GradArgs g) {
+    const int64_t each = g.E * g.M * g.N, rows = g.E * g.M, chunks = (g.N + 3) / 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / chunks, c = i % chunks * 4;
+        const int n = (int)min((int64_t)4, g.N - c);
+        const float* p = g.part + row * g.N + c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < g.splits; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] += j < n ? p[s * each + j] : 0.0f;
+        typename D::T* o = (typename D::T*)g.C + row / g.M * g.stridec + row % g.M * g.ldc + c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) o[j] = D::down(sum[j]);
+    }
+}
+
+// ---------------------------------------------------------------- the gate's gradient
+// dpre[p] = [dg du] of the rows that some expert has, rows ldd elements apart; rounded to the operands' type,
+// which the matrix cores want.
+template <class D>
+__global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N, int32_t E, const int32_t* offsets, int act,
+                                                            const typename D::T* __restrict__ dH, int64_t ldh,
+                                                            const typename D::T* __restrict__ pre, int64_t ldp,
+                                                            typename D::T* __restrict__ out, int64_t ldd) {
+    typedef typename D::T T;
+    constexpr int C = Chunk<T>::N;
+    const int64_t rows = offsets ? min((int64_t)max(offsets[E], 0), S) : S, chunks = (N + C - 1) / C;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * 256) {
+        const int64_t p = i / chunks, c = i % chunks * C, left = N - c;
+        const auto dh = chunk_load(dH + p * ldh + c, left), g = chunk_load(pre + p * ldp + c, left),
+                   u = chunk_load(pre + p * ldp + N + c, left);
+        typename Chunk<T>::V dg, du;
+#pragma unroll
+        for (int x = 0; x < C; ++x) {
+            float a, b;
+            gated_backward(D::up(dh[x]), D::up(g[x]), D::up(u[x]), act, a, b);
+            dg[x] = round_alone<D>(a);
+            du[x] = round_alone<D>(b);
+        }
+        chunk_store(out + p * ldd + c, left, dg);
+        chunk_store(out + p * ldd + N + c, left, du);
+    }
+}
+
+// ---------------------------------------------------------------- launch
+template <class Kind, class D, bool GATED, bool TB>
+int gemm16_t(const GemmArgs& g, hipStream_t s) {
+    return gemm_launch(gemm_staged<Kind, D, GATED, TB>, g, 128, GATED ? 64 : 128, 256, s);
+}
+
+int grad_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
+    (void)S, (void)E, (void)M, (void)N;
+    return 1;
+}
+
+template <class Kind, class D>
+int rows_sum_t(GradArgs g, hipStream_t s) {
+    g.m_tiles = (uint32_t)((g.M + 127) / 128);
+    g.n_tiles = (uint32_t)((g.N + 127) / 128);
+    const int64_t n = (int64_t)g.m_tiles * g.n_tiles * g.splits * g.E;
+    if (n >= (int64_t)1 << 31) return SP_ERR_SIZE;
+    hipLaunchKernelGGL((gemm_rows_sum<Kind, D, 2, true>), dim3((unsigned)std::min(n, kMostTiles)), dim3(256), 0, s, g);
+    if (hipGetLastError() != hipSuccess) return SP_ERR_HIP;
+    if (g.splits > 1) {
+        const int64_t chunks = g.E * g.M * ((g.N + 3) / 4);
+        hipLaunchKernelGGL((add_parts_kernel<D>), dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 20)), dim3(256), 0,
+                           s, g);
+        if (hipGetLastError() != hipSuccess) return SP_ERR_HIP;
+    }
+    return SP_OK;
+}
+
+// go(kind, type)
+template <class Go>
+int by_type(int32_t dtype, Go go) {
+    return dtype == SP_BF16 ? go(KindBf16(), Bf16()) : go(KindF16(), F16());
+}
+
+int64_t pre_stride(int64_t N) { return (2 * N + 63) / 64 * 64; }  // rows on 128-byte lines
+
+size_t parts_bytes(const Products& p, int64_t M) {
+    const int splits = grad_splits(p.S, p.E, M, p.K);
+    return splits > 1 ? (size_t)splits * p.E * M * p.K * sizeof(float) : 0;
+}
+
+// dA and dB (either may be NULL) from dC, S x M.
+int product_backward(const Products& p, int64_t M, const void* dC, int64_t ldc, void* dA, int64_t ldda, void* dB,
+                     int64_t lddb, int64_t stridedb, float* part, hipStream_t s) {
+    if (dA && p.S > 0 && p.K > 0) {
+        GemmArgs g{p.S, p.K, 2 * M, (const int8_t*)dC, p.S, 2 * ldc, nullptr, nullptr, 1, (const int8_t*)p.B, 2 * p.ldb,
+                   2 * p.strideb, nullptr, p.offsets, p.E, dA, ldda};
+        const int rc = by_type(p.dtype, [&](auto k, auto d) { return gemm16_t<decltype(k), decltype(d), false, true>(g, s); });
+        if (rc) return rc;
+    }
+    if (dB && M > 0 && p.K > 0) {
+        GradArgs g{p.S, M, p.K, (const int8_t*)dC, 2 * ldc, (const int8_t*)p.A, p.a_rows, 2 * p.lda, p.src,
+                   FastDiv::by(p.slots), p.offsets, p.E, dB, lddb, stridedb, part, grad_splits(p.S, p.E, M, p.K)};
+        return by_type(p.dtype, [&](auto k, auto d) { return rows_sum_t<decltype(k), decltype(d)>(g, s); });
+    }
+    return SP_OK;
+}
+
+}  // namespace
+
+int moe_gemm_device(const Products& p, int32_t gate, void* pre, int64_t ldp, void* C, int64_t ldc, hipStream_t s) {
+    if (p.a_rows == 0) return SP_OK;  // no row of C has a row of A
+    GemmArgs g{p.S, p.N, 2 * p.K, (const int8_t*)p.A, p.a_rows, 2 * p.lda, nullptr, p.src, p.slots, (const int8_t*)p.B,
+               2 * p.ldb, 2 * p.strideb, nullptr, p.offsets, p.E, C, ldc, pre, ldp, gate};
+    return by_type(p.dtype, [&](auto k, auto d) {
+        return gate < 0 ? gemm16_t<decltype(k), decltype(d), false, false>(g, s)
+                        : gemm16_t<decltype(k), decltype(d), true, false>(g, s);
+    });
+}
+
+size_t moe_gemm_backward_bytes(const Products& p) { return parts_bytes(p, p.N); }
+
+int moe_gemm_backward_device(const Products& p, const void* dC, int64_t ldc, void* dA, int64_t ldda, void* dB,
+                             int64_t lddb, int64_t stridedb, void* work, hipStream_t s) {
+    return product_backward(p, p.N, dC, ldc, dA, ldda, dB, lddb, stridedb, (float*)work, s);
+}
+
+size_t moe_gated_backward_bytes(const Products& p) {
+    return parts_bytes(p, 2 * p.N) + (size_t)p.S * pre_stride(p.N) * 2;
+}
+
+int moe_gated_backward_device(const Products& p, int32_t act, const void* dH, int64_t ldh, const void* pre, int64_t ldp,
+                              void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t stridedb, void* work,
+                              hipStream_t s) {
+    const int64_t ldd = pre_stride(p.N);
+    void* dpre = work;
+    float* part = (float*)((char*)work + (size_t)p.S * ldd * 2);
+    if (p.S > 0 && p.N > 0) {
+        const int64_t chunks = p.S * ((p.N + 7) / 8);
+        const unsigned grid = (unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 20);
+        by_type(p.dtype, [&](auto, auto d) {
+            typedef decltype(d) D;
+            typedef typename D::T T;
+            hipLaunchKernelGGL((gate_backward_kernel<D>), dim3(grid), dim3(256), 0, s, p.S, p.N, p.E, p.offsets, act,
+                               (const T*)dH, ldh, (const T*)pre, ldp, (T*)dpre, ldd);
+            return 0;
+        });
+        if (hipGetLastError() != hipSuccess) return SP_ERR_HIP;
+    }
+    return product_backward(p, 2 * p.N, dpre, ldd, dA, ldda, dB, lddb, stridedb, part, s);
+}
+
+}  // namespace spx

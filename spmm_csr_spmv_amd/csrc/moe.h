@@ -1,5 +1,5 @@
-// Declarations of the mixture-of-experts operators, shared by their entry
-// points (moe_api.cpp) and kernels.  Not part of the public ABI.
+// Declarations of the mixture-of-experts operators and the norm, shared by their entry
+// points (moe_api.cpp, layer_api.cpp) and kernels.  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -25,7 +25,47 @@ int quantize_rows_i8_device(int64_t rows, int64_t K, int32_t dtype, const void* 
                             float* scale, hipStream_t s);
 int gemm_i8_device(int64_t S, int32_t E, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
                    const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
-                   int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t c_type, void* C, int64_t ldc,
-                   hipStream_t s);
+                   int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t gate, int32_t c_type, void* C,
+                   int64_t ldc, hipStream_t s);  // gate: an activation (B then has 2 N rows a matrix), or -1
+
+// Operands of the 16-bit products (gemm_16.hip); distances in elements.
+struct Products {
+    int64_t S;  // sorted rows
+    int32_t E;
+    int64_t N, K;  // columns of C (gated: B has 2 N rows a matrix), length of the sums
+    int32_t dtype;
+    const void* A;
+    int64_t a_rows, lda;
+    const int32_t* src;
+    int32_t slots;
+    const void* B;
+    int64_t ldb, strideb;
+    const int32_t* offsets;
+};
+int moe_gemm_device(const Products& p, int32_t gate, void* pre, int64_t ldp, void* C, int64_t ldc, hipStream_t s);
+size_t moe_gemm_backward_bytes(const Products& p);
+int moe_gemm_backward_device(const Products& p, const void* dC, int64_t ldc, void* dA, int64_t ldda, void* dB,
+                             int64_t lddb, int64_t stridedb, void* work, hipStream_t s);
+size_t moe_gated_backward_bytes(const Products& p);
+int moe_gated_backward_device(const Products& p, int32_t act, const void* dH, int64_t ldh, const void* pre, int64_t ldp,
+                              void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t stridedb, void* work,
+                              hipStream_t s);
+
+// Rows of the norm (norm.hip).
+struct NormRows {
+    int64_t rows, H;
+    int32_t dtype, w_type;
+    const void* X;  // backward: the stored sum
+    int64_t ldx;
+    const void* R;  // the residual, backward: the sum's own gradient; or NULL
+    int64_t ldr;
+    const void* weight;  // or NULL
+    float eps;
+};
+// scale: int8 codes in Y; or NULL
+int rms_norm_device(const NormRows& n, void* sum, int64_t lds, void* Y, int64_t ldy, float* scale, hipStream_t s);
+size_t rms_norm_backward_bytes(int64_t rows, int64_t H, int32_t dtype);
+int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, void* dX, int64_t lddx, float* dweight,
+                             void* work, hipStream_t s);
 
 }  // namespace spx

@@ -1,25 +1,12 @@
 // extern "C" entry points of the mixture-of-experts operators: argument
 // checks, then the launch.  None of them allocates or synchronises.
+#include "checks.h"
 #include "moe.h"
 #include "spmm_csr_spmv.h"
 
+using namespace spx;
+
 namespace {
-
-constexpr int64_t kI32Max = 2147483647;
-constexpr int64_t kI64Max = 9223372036854775807LL;
-
-bool bad_dtype(int32_t t) { return t != SP_F32 && t != SP_BF16 && t != SP_F16; }
-size_t elem(int32_t t) { return t == SP_F32 ? 4 : 2; }
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
-// rows rows ld apart: the last element's byte offset must fit 63 bits
-bool too_far(int64_t rows, int64_t ld) { return rows > 0 && ld > (kI64Max >> 4) / rows; }
-
-// whether [a, a + an) and [b, b + bn) share a byte
-bool share(const void* a, size_t an, const void* b, size_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return an > 0 && bn > 0 && (x <= y ? y - x < an : x - y < bn);
-}
 
 int rows_args(int64_t T, int32_t slots, int64_t H, int64_t S, int32_t dtype) {
     if (T < 0 || T > kI32Max || slots < 1 || H < 0 || H > kI32Max || S < 0 || S > kI32Max) return SP_ERR_SIZE;
@@ -106,16 +93,18 @@ int quantize_rows_i8(int64_t rows, int64_t K, int32_t dtype, const void* X, int6
     return spx::quantize_rows_i8_device(rows, K, dtype, X, ldx, q, ldq, scale, (hipStream_t)stream);
 }
 
-int moe_gemm_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
-                const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
-                int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t c_type, void* C, int64_t ldc,
-                void* stream) {
+static int moe_product_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows,
+                          int64_t lda, const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B,
+                          int64_t ldb, int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t gate,
+                          int32_t c_type, void* C, int64_t ldc, void* stream) {
+    const int64_t b_rows = gate < 0 ? N : 2 * N;
     if (S < 0 || S > kI32Max || a_rows < 0 || a_rows > kI32Max || N < 0 || N > kI32Max || K < 0 || slots < 1)
         return SP_ERR_SIZE;
     if (K > SP_I8_MAX_K || num_experts < 1 || num_experts > SP_MOE_MAX_EXPERTS || bad_dtype(c_type))
         return SP_ERR_UNSUPPORTED;
-    if (lda < K || ldb < K || ldc < N || too_far(a_rows, lda) || too_far(N, ldb) || too_far(S, ldc)) return SP_ERR_SIZE;
-    if (num_experts > 1 && N > 0 && (strideb < 0 || strideb < (N - 1) * ldb + K || too_far(num_experts, strideb)))
+    if (lda < K || ldb < K || ldc < N || too_far(a_rows, lda) || too_far(b_rows, ldb) || too_far(S, ldc))
+        return SP_ERR_SIZE;
+    if (num_experts > 1 && N > 0 && (strideb < 0 || strideb < (b_rows - 1) * ldb + K || too_far(num_experts, strideb)))
         return SP_ERR_SIZE;
     if (S == 0 || N == 0) return SP_OK;
     if (!offsets || !C || !b_scale || (a_rows > 0 && !a_scale) || (K > 0 && (!B || (a_rows > 0 && !A))))
@@ -124,19 +113,49 @@ int moe_gemm_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8
         misaligned(src, 4))
         return SP_ERR_UNSUPPORTED;
     return spx::gemm_i8_device(S, num_experts, N, K, A, a_rows, lda, a_scale, src, slots, B, ldb, strideb, b_scale,
-                               offsets, c_type, C, ldc, (hipStream_t)stream);
+                               offsets, gate, c_type, C, ldc, (hipStream_t)stream);
+}
+
+static int product_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* a_scale,
+                      const int8_t* B, int64_t ldb, const float* b_scale, int32_t gate, int32_t c_type, void* C,
+                      int64_t ldc, void* stream) {
+    if (M < 0 || M > kI32Max || N < 0 || N > kI32Max || K < 0) return SP_ERR_SIZE;
+    if (K > SP_I8_MAX_K || bad_dtype(c_type)) return SP_ERR_UNSUPPORTED;
+    if (lda < K || ldb < K || ldc < N || too_far(M, lda) || too_far(gate < 0 ? N : 2 * N, ldb) || too_far(M, ldc))
+        return SP_ERR_SIZE;
+    if (M == 0 || N == 0) return SP_OK;
+    if (!C || !a_scale || !b_scale || (K > 0 && (!A || !B))) return SP_ERR_NULL;
+    if (misaligned(C, elem(c_type)) || misaligned(a_scale, 4) || misaligned(b_scale, 4)) return SP_ERR_UNSUPPORTED;
+    return spx::gemm_i8_device(M, 1, N, K, A, M, lda, a_scale, nullptr, 1, B, ldb, 0, b_scale, nullptr, gate, c_type, C,
+                               ldc, (hipStream_t)stream);
+}
+
+int moe_gemm_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
+                const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
+                int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t c_type, void* C, int64_t ldc,
+                void* stream) {
+    return moe_product_i8(S, num_experts, N, K, A, a_rows, lda, a_scale, src, slots, B, ldb, strideb, b_scale, offsets,
+                          -1, c_type, C, ldc, stream);
 }
 
 int gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B,
             int64_t ldb, const float* b_scale, int32_t c_type, void* C, int64_t ldc, void* stream) {
-    if (M < 0 || M > kI32Max || N < 0 || N > kI32Max || K < 0) return SP_ERR_SIZE;
-    if (K > SP_I8_MAX_K || bad_dtype(c_type)) return SP_ERR_UNSUPPORTED;
-    if (lda < K || ldb < K || ldc < N || too_far(M, lda) || too_far(N, ldb) || too_far(M, ldc)) return SP_ERR_SIZE;
-    if (M == 0 || N == 0) return SP_OK;
-    if (!C || !a_scale || !b_scale || (K > 0 && (!A || !B))) return SP_ERR_NULL;
-    if (misaligned(C, elem(c_type)) || misaligned(a_scale, 4) || misaligned(b_scale, 4)) return SP_ERR_UNSUPPORTED;
-    return spx::gemm_i8_device(M, 1, N, K, A, M, lda, a_scale, nullptr, 1, B, ldb, 0, b_scale, nullptr, c_type, C, ldc,
-                               (hipStream_t)stream);
+    return product_i8(M, N, K, A, lda, a_scale, B, ldb, b_scale, -1, c_type, C, ldc, stream);
+}
+
+int moe_gated_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int8_t* A, int64_t a_rows, int64_t lda,
+                 const float* a_scale, const int32_t* src, int32_t slots, const int8_t* B, int64_t ldb,
+                 int64_t strideb, const float* b_scale, const int32_t* offsets, int32_t act, int32_t c_type, void* C,
+                 int64_t ldc, void* stream) {
+    if (bad_act(act)) return SP_ERR_UNSUPPORTED;
+    return moe_product_i8(S, num_experts, N, K, A, a_rows, lda, a_scale, src, slots, B, ldb, strideb, b_scale, offsets,
+                          act, c_type, C, ldc, stream);
+}
+
+int gated_i8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B,
+             int64_t ldb, const float* b_scale, int32_t act, int32_t c_type, void* C, int64_t ldc, void* stream) {
+    if (bad_act(act)) return SP_ERR_UNSUPPORTED;
+    return product_i8(M, N, K, A, lda, a_scale, B, ldb, b_scale, act, c_type, C, ldc, stream);
 }
 
 }  // extern "C"

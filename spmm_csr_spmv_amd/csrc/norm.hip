@@ -1,0 +1,487 @@
+// Root-mean-square norm of rows, with the residual's addition before it:
+//   s = x + r (rounded to the rows' type; s = x without r)
+//   i = 1 / sqrt(mean s^2 + eps),  y = s i w
+// y in the rows' type, or as int8 codes with a scale per row as the 8-bit products read them
+// (a = max |y|, scale = a / 127, q = rint(127 y / a)); and its gradient, with n = s i and dn = dy w:
+//   ds = i (dn - n mean(dn n)) + dsum,  dw = sum over rows of dy n
+// The norm is that of the stored sum s, so that the gradient, which has only s, is this function's.
+//
+// A row's lanes hold it in registers between the sums and the results, so that each
+// byte is read and written once; longer rows are read again (from L2).  Sums are fp32, added
+// across lanes in a fixed order.  Squares beyond fp32's range: a row whose sum of squares is
+// not below 2^120 (or, with an eps near zero, not above 2^-60) is summed again scaled by 2^-96 (2^96).
+#include <algorithm>
+
+#include "device_common.h"
+#include "moe.h"
+#include "rows.h"
+
+namespace spx {
+
+namespace {
+
+constexpr float kTiny = 0x1p-119f;  // rows whose largest magnitude is below it have the scale 0
+constexpr int kHeld = 4;            // chunks of a row that a lane holds
+
+struct NormArgs {
+    int64_t rows, H;
+    const void* X;            // backward: s
+    int64_t ldx;
+    const void* R;            // or NULL; backward: dsum
+    int64_t ldr;
+    const void* weight;       // or NULL: ones
+    float eps;
+    void* sum;                // or NULL
+    int64_t lds;
+    void* Y;                  // rows, or int8 codes; backward: ds
+    int64_t ldy;
+    float* scale;             // int8 codes only
+    const void* dY;           // backward only, as what follows
+    int64_t lddy;
+    float* part;              // [parts][H]: sums of dy n over some rows each, or NULL
+    float* rstd;              // or NULL: i of every row
+};
+
+// Sum and maximum over the TPR lanes that share a row, in every one of them.
+template <int TPR, class F>
+__device__ __forceinline__ float across(float v, float (&part)[4], F f) {
+    v = f(v, swz_xor<1>(v));
+    v = f(v, swz_xor<2>(v));
+    v = f(v, swz_xor<4>(v));
+    v = f(v, swz_xor<8>(v));
+    if (TPR >= 64) {
+        v = f(v, swz_xor<16>(v));
+        v = f(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)),
+              __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)));
+    }
+    if (TPR == 256) {
+        __syncthreads();  // part[] has been read
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = f(f(part[0], part[1]), f(part[2], part[3]));
+    }
+    return v;
+}
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+// A NaN stays one.
+struct Most {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a >= b || a != a ? a : b; }
+};
+
+// The factor that brings a row's sum of squares into range; 1 where it is there.
+__device__ __forceinline__ float range_factor(float ss, float eps) {
+    return !(ss < 0x1p120f) ? 0x1p-96f : ss < 0x1p-60f && eps < 0x1p-100f ? 0x1p96f : 1.0f;
+}
+// i / f for a sum of squares of values that were multiplied by f.
+__device__ __forceinline__ float inverse_rms(float ss, float H, float eps, float f) {
+    return 1.0f / sqrtf(ss / fmaxf(H, 1.0f) + eps * f * f);
+}
+
+// N weights from column k on, len of them inside the row.
+template <class W, int N>
+__device__ __forceinline__ void weights_at(const void* weight, int64_t k, int64_t len, float (&w)[N]) {
+    if (!weight) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = 1.0f;
+        return;
+    }
+    const typename W::T* p = (const typename W::T*)weight + k;
+    if (len >= N) {
+        typedef typename W::T V __attribute__((ext_vector_type(N), aligned(sizeof(typename W::T))));
+        const V v = *reinterpret_cast<const V*>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = W::up(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = i < len ? W::up(p[i]) : 0.0f;
+    }
+}
+
+template <int TPR>
+__device__ __forceinline__ int64_t first_row() {
+    const int sub = threadIdx.x / TPR;
+    return (int64_t)blockIdx.x * (256 / TPR) + (TPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+}
+
+template <class D, class W, int TPR, bool I8>
+__global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
+    typedef typename D::T T;
+    typedef typename Chunk<T>::V V;
+    constexpr int N = Chunk<T>::N;
+    __shared__ float part[4];
+    const int lane = threadIdx.x % TPR;
+    const int64_t chunks = (g.H + N - 1) / N;
+    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * (256 / TPR)) {
+        const T* x = (const T*)g.X + row * g.ldx;
+        const T* r = g.R ? (const T*)g.R + row * g.ldr : nullptr;
+        T* sum = g.sum ? (T*)g.sum + row * g.lds : nullptr;
+        const T* stored = sum ? sum : x;
+        float held[kHeld][N];  // s w
+        float ss = 0.0f, most = 0.0f;
+        const auto sums = [&](const float (&s)[N], const float (&t)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                ss = fmaf(s[i], s[i], ss);
+                if (I8) most = Most()(fabsf(t[i]), most);
+            }
+        };
+        // s of chunk c, formed and stored
+        const auto first = [&](int64_t c, float (&t)[N]) {
+            const int64_t k = c * N, len = g.H - k;
+            V v = chunk_load(x + k, len);
+            if (r) {
+                const V q = chunk_load(r + k, len);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = D::down(D::up(v[i]) + D::up(q[i]));
+            }
+            if (sum) chunk_store(sum + k, len, v);
+            float s[N];
+            weights_at<W, N>(g.weight, k, len, t);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                s[i] = D::up(v[i]);
+                t[i] *= s[i];
+            }
+            sums(s, t);
+        };
+        // s w of chunk c times f, from the stored sum
+        const auto again = [&](int64_t c, float f, float (&s)[N], float (&t)[N]) {
+            const int64_t k = c * N, len = g.H - k;
+            const V v = chunk_load(stored + k, len);
+            weights_at<W, N>(g.weight, k, len, t);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                s[i] = D::up(v[i]) * f;
+                t[i] *= s[i];
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (lane + h * TPR < chunks) first(lane + h * TPR, held[h]);
+        for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
+            float t[N];
+            first(c, t);
+        }
+        ss = across<TPR>(ss, part, Add());
+        if (I8) most = across<TPR>(most, part, Most());
+        float f = range_factor(ss, g.eps);
+        if (I8 && !(most < 0x1p120f)) f = 0x1p-96f;
+        if (f != 1.0f) {  // rare: the same for all lanes of the row
+            ss = most = 0.0f;
+            for (int64_t c = lane; c < chunks; c += TPR) {
+                float s[N], t[N];
+                again(c, f, s, t);
+                sums(s, t);
+            }
+            ss = across<TPR>(ss, part, Add());
+            if (I8) most = across<TPR>(most, part, Most());
+        }
+        const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
+        float top = 1.0f, by = 1.0f;
+        bool live = false;
+        if constexpr (I8) {
+            // the codes are those of t = s w f: the row's factor cancels
+            const float a = most * unit;
+            live = a >= kTiny && a < __builtin_inff();
+            top = live ? most : 1.0f;
+            by = 1.0f / top;
+            if (lane == 0) g.scale[row] = live ? a / 127.0f : a < kTiny ? 0.0f : __builtin_nanf("");
+        }
+        // chunk c of the result, t times `times` (or its codes)
+        const auto out = [&](int64_t c, const float (&t)[N], float times) {
+            const int64_t k = c * N, len = g.H - k;
+            if constexpr (!I8) {
+                V o;
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = D::down(t[i] * times);
+                chunk_store((T*)g.Y + row * g.ldy + k, len, o);
+            } else {
+                // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits;
+                // the product with a rounded 1 / top is off by less than 1e-4 of a code: near a half divide
+                constexpr float kMagic = 12582912.0f;
+                uint32_t n[N];
+                float off = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float t127 = t[i] * 127.0f, y = fmaf(t127, by, kMagic);
+                    off = fmaxf(off, fabsf(fmaf(t127, by, -(y - kMagic))));
+                    n[i] = __float_as_uint(y);
+                }
+                if (__any(off > 0.4999f)) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) n[i] = __float_as_uint(t[i] * 127.0f / top + kMagic);
+                }
+                typedef uint32_t QU __attribute__((ext_vector_type(N / 4), aligned(1)));
+                QU o;
+#pragma unroll
+                for (int i = 0; i < N; i += 4)
+                    o[i / 4] = live ? (n[i] & 255u) | (n[i + 1] & 255u) << 8 | (n[i + 2] & 255u) << 16 | n[i + 3] << 24 : 0u;
+                int8_t* q = (int8_t*)g.Y + row * g.ldy + k;
+                if (len >= N) {
+                    *reinterpret_cast<QU*>(q) = o;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N - 1; ++i)
+                        if (i < len) q[i] = (int8_t)(o[i / 4] >> (8 * (i % 4)));
+                }
+            }
+        };
+        const bool plain = f == 1.0f;
+        // scaled rows: s i first, as s w may be out of range where s i w is not
+        const float before = plain ? 1.0f : I8 ? f : inv, times = plain ? inv : 1.0f;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (plain && lane + h * TPR < chunks) out(lane + h * TPR, held[h], inv);
+        for (int64_t c = lane + (plain ? kHeld * TPR : 0); c < chunks; c += TPR) {
+            float s[N], t[N];
+            again(c, before, s, t);
+            out(c, t, times);
+        }
+    }
+}
+
+// The gradient.  Rows of up to kHeld chunks a lane are held, and a lane adds up its columns' dy n over
+// the rows of its workgroup, whose sums go to part[blockIdx.x] (PARTS).  Longer rows leave i in rstd.
+template <class D, class W, int TPR, bool PARTS>
+__global__ __launch_bounds__(256) void rms_norm_backward_kernel(NormArgs g) {
+    typedef typename D::T T;
+    typedef typename Chunk<T>::V V;
+    constexpr int N = Chunk<T>::N, R = 256 / TPR;
+    __shared__ float part[4];
+    const int lane = threadIdx.x % TPR;
+    const int64_t chunks = (g.H + N - 1) / N;
+    float acc[PARTS ? kHeld : 1][N];
+#pragma unroll
+    for (auto& a : acc)
+#pragma unroll
+        for (float& v : a) v = 0.0f;
+    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * R) {
+        const T* x = (const T*)g.X + row * g.ldx;
+        const T* y = (const T*)g.dY + row * g.lddy;
+        const T* d = g.R ? (const T*)g.R + row * g.ldr : nullptr;
+        V hx[kHeld], hy[kHeld], hd[kHeld];
+        float ss = 0.0f, dot = 0.0f;  // of s^2 and of dn s
+        const auto sums = [&](int64_t c, const V& vx, const V& vy, float f) {
+            float w[N];
+            weights_at<W, N>(g.weight, c * N, g.H - c * N, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float s = D::up(vx[i]) * f;
+                ss = fmaf(s, s, ss);
+                dot = fmaf(D::up(vy[i]) * w[i], s, dot);
+            }
+        };
+        const auto rest = [&](int64_t from, float f) {
+            for (int64_t c = from; c < chunks; c += TPR) sums(c, chunk_load(x + c * N, g.H - c * N), chunk_load(y + c * N, g.H - c * N), f);
+        };
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int64_t k = (int64_t)(lane + h * TPR) * N;
+            if (k < g.H) {
+                hx[h] = chunk_load(x + k, g.H - k);
+                hy[h] = chunk_load(y + k, g.H - k);
+                if (d) hd[h] = chunk_load(d + k, g.H - k);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (lane + h * TPR < chunks) sums(lane + h * TPR, hx[h], hy[h], 1.0f);
+        if (!PARTS) rest(lane + kHeld * TPR, 1.0f);
+        ss = across<TPR>(ss, part, Add());
+        dot = across<TPR>(dot, part, Add());
+        const float f = range_factor(ss, g.eps);
+        if (f != 1.0f) {
+            ss = dot = 0.0f;
+            rest(lane, f);
+            ss = across<TPR>(ss, part, Add());
+            dot = across<TPR>(dot, part, Add());
+        }
+        const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
+        const float mean = dot * unit / (float)g.H;  // of dn n
+        if (!PARTS && g.rstd && lane == 0) g.rstd[row] = inv;
+        const auto out = [&](int64_t c, const V& vx, const V& vy, const V& vd, float (&sum)[N]) {
+            const int64_t k = c * N, len = g.H - k;
+            float w[N];
+            weights_at<W, N>(g.weight, k, len, w);
+            V o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float n = D::up(vx[i]) * inv, dy = D::up(vy[i]);
+                float v = inv * fmaf(-n, mean, dy * w[i]);
+                if (d) v += D::up(vd[i]);
+                o[i] = D::down(v);
+                sum[i] = fmaf(dy, n, sum[i]);
+            }
+            chunk_store((T*)g.Y + row * g.ldy + k, len, o);
+        };
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (lane + h * TPR < chunks) out(lane + h * TPR, hx[h], hy[h], hd[h], acc[PARTS ? h : 0]);
+        if (!PARTS)
+            for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
+                const int64_t k = c * N, len = g.H - k;
+                const V vx = chunk_load(x + k, len), vy = chunk_load(y + k, len);
+                out(c, vx, vy, d ? chunk_load(d + k, len) : vx, acc[0]);
+            }
+    }
+    if constexpr (PARTS) {
+        if (!g.part) return;
+        float* to = g.part + (int64_t)blockIdx.x * g.H;
+        if constexpr (R == 1) {
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int64_t k = (int64_t)(lane + h * TPR) * N + i;
+                    if (k < g.H) to[k] = acc[h][i];
+                }
+        } else {
+            // the workgroup's R rows at a time added in their order
+            constexpr int kCols = TPR * kHeld * N;
+            __shared__ float all[R][kCols];
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+                for (int i = 0; i < N; ++i) all[threadIdx.x / TPR][(lane + h * TPR) * N + i] = acc[h][i];
+            __syncthreads();
+            for (int k = threadIdx.x; k < g.H; k += 256) {
+                float v = all[0][k];
+                for (int j = 1; j < R; ++j) v += all[j][k];
+                to[k] = v;
+            }
+        }
+    }
+}
+
+// part[blockIdx.y] = the sums over a range of rows of dy s i, i from rstd; a thread a column.
+template <class D>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs g, int64_t each) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k >= g.H) return;
+    const int64_t from = blockIdx.y * each, to = min(from + each, g.rows);
+    const typename D::T *x = (const typename D::T*)g.X + k, *y = (const typename D::T*)g.dY + k;
+    float v = 0.0f;
+#pragma unroll 4
+    for (int64_t r = from; r < to; ++r) v = fmaf(D::up(y[r * g.lddy]), D::up(x[r * g.ldx]) * g.rstd[r], v);
+    g.part[blockIdx.y * g.H + k] = v;
+}
+
+// dweight = the parts' sum: 16 columns a workgroup, 16 threads to a column, each every 16th part, added in order.
+__global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ part, int64_t parts, int64_t H,
+                                                         float* __restrict__ dweight) {
+    __shared__ float all[16][17];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t k = (int64_t)blockIdx.x * 16 + c;
+    float v = 0.0f;
+    if (k < H)
+#pragma unroll 4
+        for (int64_t p = r; p < parts; p += 16) v += part[p * H + k];
+    all[r][c] = v;
+    __syncthreads();
+    if (r == 0 && k < H) {
+        for (int j = 1; j < 16; ++j) v += all[j][c];
+        dweight[k] = v;
+    }
+}
+
+// ---------------------------------------------------------------- launch
+int status(hipError_t e) { return e == hipSuccess ? SP_OK : SP_ERR_HIP; }
+int chunk_of(int32_t dtype) { return dtype == SP_F32 ? 4 : 8; }
+// Lanes a row: the fewest whose registers hold it.
+int norm_lanes(int64_t H, int32_t dtype) {
+    const int64_t chunks = (H + chunk_of(dtype) - 1) / chunk_of(dtype);
+    return chunks <= 16 * kHeld ? 16 : chunks <= 64 * kHeld ? 64 : 256;
+}
+bool held(int64_t H, int32_t dtype) { return (H + chunk_of(dtype) - 1) / chunk_of(dtype) <= 256 * kHeld; }
+
+constexpr int64_t kMostGroups = 1 << 20;  // workgroups; more rows take several rounds
+
+// Workgroups of the gradient, and so parts of dweight.
+int64_t backward_groups(int64_t rows, int64_t H, int32_t dtype) {
+    const int64_t per = 256 / norm_lanes(H, dtype);
+    return std::min<int64_t>((rows + per - 1) / per, 1024);
+}
+// Rows a part of norm_columns_kernel.
+int64_t column_rows(int64_t rows) { return std::max<int64_t>(16, (rows + 255) / 256); }
+
+template <int L>
+struct Lanes {
+    static constexpr int value = L;
+};
+// go(type, weight's type, lanes)
+template <class Go>
+int norm_by(int32_t dtype, int32_t w_type, int64_t H, Go go) {
+    const auto lanes = [&](auto d, auto w) {
+        const int n = norm_lanes(H, dtype);
+        return n == 16 ? go(d, w, Lanes<16>()) : n == 64 ? go(d, w, Lanes<64>()) : go(d, w, Lanes<256>());
+    };
+    if (dtype == SP_F32) return lanes(F32(), F32());
+    if (dtype == SP_BF16) return w_type == SP_F32 ? lanes(Bf16(), F32()) : lanes(Bf16(), Bf16());
+    return w_type == SP_F32 ? lanes(F16(), F32()) : lanes(F16(), F16());
+}
+
+}  // namespace
+
+int rms_norm_device(const NormRows& n, void* sum, int64_t lds, void* Y, int64_t ldy, float* scale, hipStream_t s) {
+    NormArgs g{};
+    g.rows = n.rows, g.H = n.H, g.X = n.X, g.ldx = n.ldx, g.R = n.R, g.ldr = n.ldr, g.weight = n.weight, g.eps = n.eps;
+    g.sum = sum, g.lds = lds, g.Y = Y, g.ldy = ldy, g.scale = scale;
+    return norm_by(n.dtype, n.w_type, n.H, [&](auto d, auto w, auto l) {
+        typedef decltype(d) D;
+        typedef decltype(w) W;
+        constexpr int L = decltype(l)::value, per = 256 / L;
+        const dim3 grid((unsigned)std::min<int64_t>((g.rows + per - 1) / per, kMostGroups));
+        if (scale)
+            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, true>), grid, dim3(256), 0, s, g);
+        else
+            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, false>), grid, dim3(256), 0, s, g);
+        return status(hipGetLastError());
+    });
+}
+
+size_t rms_norm_backward_bytes(int64_t rows, int64_t H, int32_t dtype) {
+    if (held(H, dtype)) return (size_t)backward_groups(rows, H, dtype) * H * sizeof(float);
+    const int64_t each = column_rows(rows);
+    return ((size_t)rows + (size_t)((rows + each - 1) / each) * H) * sizeof(float);
+}
+
+int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, void* dX, int64_t lddx, float* dweight,
+                             void* work, hipStream_t s) {
+    NormArgs g{};
+    g.rows = n.rows, g.H = n.H, g.X = n.X, g.ldx = n.ldx, g.R = n.R, g.ldr = n.ldr, g.weight = n.weight, g.eps = n.eps;
+    g.dY = dY, g.lddy = lddy, g.Y = dX, g.ldy = lddx;
+    const bool whole = held(n.H, n.dtype);
+    int64_t parts = 0;
+    if (n.rows > 0) {
+        const int64_t each = column_rows(n.rows);
+        parts = whole ? backward_groups(n.rows, n.H, n.dtype) : (n.rows + each - 1) / each;
+        if (dweight) {
+            if (!whole) g.rstd = (float*)work;
+            g.part = (float*)work + (whole ? 0 : n.rows);
+        }
+        const int rc = norm_by(n.dtype, n.w_type, n.H, [&](auto d, auto w, auto l) {
+            typedef decltype(d) D;
+            typedef decltype(w) W;
+            constexpr int L = decltype(l)::value;
+            if (whole) {
+                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, true>), dim3((unsigned)parts), dim3(256), 0, s, g);
+            } else if constexpr (L == 256) {
+                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, false>),
+                                   dim3((unsigned)std::min<int64_t>(g.rows, kMostGroups)), dim3(256), 0, s, g);
+                if (g.rstd && hipGetLastError() == hipSuccess)
+                    hipLaunchKernelGGL((norm_columns_kernel<D>), dim3((unsigned)((g.H + 255) / 256), (unsigned)parts),
+                                       dim3(256), 0, s, g, each);
+            }
+            return status(hipGetLastError());
+        });
+        if (rc) return rc;
+    }
+    if (!dweight) return SP_OK;
+    hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((n.H + 15) / 16)), dim3(256), 0, s, (const float*)work + (whole ? 0 : n.rows),
+                       parts, n.H, dweight);
+    return status(hipGetLastError());
+}
+
+}  // namespace spx

@@ -27,6 +27,15 @@ struct F16 {
     static __device__ __forceinline__ _Float16 down(float v) { return (_Float16)v; }
 };
 
+// v rounded to D's type after it was an fp32 number: left to itself the compiler fuses a product and its rounding to fp16
+// in some places and not in others, even where contraction is off, and the last bit of a value then depends on where in a
+// result it stands.
+template <class D>
+__device__ __forceinline__ typename D::T round_alone(float v) {
+    asm("" : "+v"(v));
+    return D::down(v);
+}
+
 template <class T>
 struct Chunk {
     static constexpr int N = 16 / (int)sizeof(T);
