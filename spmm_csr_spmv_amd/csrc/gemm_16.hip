@@ -30,52 +30,60 @@ struct GradArgs {
 };
 
 // Tiles of dB, 64 WN square, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
-// are split and the parts' fp32 sums added afterwards in the order of the splits.
-template <class Kind, class D, int WN, bool STAGED>
+// are split and the parts' fp32 sums (PART) added afterwards in the order of the splits.
+template <class Kind, class D, int WN, bool STAGED, bool PART, bool GATHER>
+__device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uint32_t total, const BigBuffers<2>& m,
+                                              int32_t* lrow, int tid, int w, int l) {
+    // eight tiles in a row, which share a tile's columns of A, on one XCD
+    const uint32_t v = t < total / 64 * 64 ? t / 64 * 64 + t % 8 * 8 + t / 8 % 8 : t;
+    const uint32_t per = g.m_tiles * g.n_tiles, part = v / per, in = v % per;
+    const int e = (int)(part / g.splits), split = (int)(part % g.splits);
+    const int64_t m0 = (int64_t)(in % g.m_tiles) * (64 * WN), n0 = (int64_t)(in / g.m_tiles) * (64 * WN);
+    int a = 0, b = (int)g.S;
+    if (g.offsets) expert_rows(g.offsets, g.E, g.S, e, a, b);
+    a = __builtin_amdgcn_readfirstlane(a);
+    b = __builtin_amdgcn_readfirstlane(b);
+    const int each = (int)(((uint32_t)(b - a) + g.splits * 64u - 1) / (g.splits * 64u)) * 64;
+    const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b), rows = min(each, b - from);
+    if (tid < 64 * WN) lrow[tid] = m0 + tid < g.M ? 0 : -1;
+    BigTransposed<WN, false> sa;
+    BigTransposed<WN, GATHER> sb;
+    sa.template place<STAGED>(g.P + from * g.ldp, g.ldp, rows, m0, g.M, w, l);
+    if constexpr (GATHER) {
+        sb.template place<STAGED>(g.Q, g.ldq, rows, n0, g.N, w, l);
+        sb.src = g.src + from;
+        sb.slots = g.slots;
+        sb.a_rows = g.q_rows;
+    } else {
+        sb.template place<STAGED>(g.Q + from * g.ldq, g.ldq, (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0), n0,
+                                  g.N, w, l);
+    }
+    typename Kind::S16 acc[WN][2];
+    const int steps = (rows + 63) >> 6;
+    if constexpr (STAGED)
+        staged_sums<Kind, WN, true, true>(acc, m, sa, sb, steps, w, l);
+    else
+        big_sums<Kind, WN, 2, WN, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
+    BigOut o{(typename D::T*)g.C + e * g.stridec, g.ldc, g.N, m0, n0, nullptr, 0, 0};
+    if (PART) o.C = g.part + ((int64_t)split * g.E + e) * g.M * g.N, o.ldc = g.N;
+    const float* none = nullptr;
+    big_out<Kind, std::conditional_t<PART, F32, D>, WN, WN, false>(o, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, none, w, l);
+}
+
+template <class Kind, class D, int WN, bool STAGED, bool PART, bool GATHER>
 __global__ __launch_bounds__(128 * WN, 2) void gemm_rows_sum(GradArgs g) {
-    constexpr int kBytes = 64 * WN * kBigK, F = WN;
+    constexpr int kBytes = 64 * WN * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
     __shared__ int32_t lrow[64 * WN];
     const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    const uint32_t per = g.m_tiles * g.n_tiles, total = per * (uint32_t)g.splits * (uint32_t)g.E;
-    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
-        const uint32_t v = t, part = v / per, in = v % per;
-        const int e = (int)(part / g.splits), split = (int)(part % g.splits);
-        const int64_t m0 = (int64_t)(in % g.m_tiles) * (64 * WN), n0 = (int64_t)(in / g.m_tiles) * (64 * WN);
-        int a = 0, b = (int)g.S;
-        if (g.offsets) expert_rows(g.offsets, g.E, g.S, e, a, b);
-        a = __builtin_amdgcn_readfirstlane(a);
-        b = __builtin_amdgcn_readfirstlane(b);
-        const int each = (int)(((uint32_t)(b - a) + g.splits * 64u - 1) / (g.splits * 64u)) * 64;
-        const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b), rows = min(each, b - from);
-        if (t != blockIdx.x) __syncthreads();  // the tile before has been stored
-        if (tid < 64 * WN) lrow[tid] = m0 + tid < g.M ? 0 : -1;
-        BigTransposed<WN> sa, sb;
-        sa.place(g.P + from * g.ldp, g.ldp, rows, m0, g.M, w, l);
-        const int8_t* q = g.src ? g.Q : g.Q + from * g.ldq;
-        sb.place(q, g.ldq, g.src ? rows : (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0), n0, g.N, w, l);
-        if (g.src) {
-            sb.src = g.src + from;
-            sb.slots = g.slots;
-            sb.a_rows = g.q_rows;
-        }
-        typename Kind::S16 acc[F][2];
-        const int steps = (rows + 63) >> 6;
-        if constexpr (STAGED) {
-            sa.any(g.P + from * g.ldp, m0, l);
-            sb.any(q, n0, l);
-            staged_sums<Kind, F, true, true>(acc, m, sa, sb, steps, w, l);
-        } else {
-            big_sums<Kind, WN, 2, F, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
-        }
-        const float* none = nullptr;
-        if (g.splits > 1) {
-            const BigOut o{g.part + ((int64_t)split * g.E + e) * g.M * g.N, g.N, g.N, m0, n0, nullptr, 0, 0};
-            big_out<Kind, F32, WN, F, false>(o, acc, b0, b1, a0, a1, lrow, none, w, l);
-        } else {
-            const BigOut o{(typename D::T*)g.C + e * g.stridec, g.ldc, g.N, m0, n0, nullptr, 0, 0};
-            big_out<Kind, D, WN, F, false>(o, acc, b0, b1, a0, a1, lrow, none, w, l);
+    const uint32_t total = g.m_tiles * g.n_tiles * (uint32_t)g.splits * (uint32_t)g.E;
+    if constexpr (!STAGED) {  // as many workgroups as tiles
+        rows_sum_tile<Kind, D, WN, STAGED, PART, GATHER>(g, blockIdx.x, total, m, lrow, tid, w, l);
+    } else {
+        for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+            if (t != blockIdx.x) __syncthreads();  // the tile before has been stored
+            rows_sum_tile<Kind, D, WN, STAGED, PART, GATHER>(g, t, total, m, lrow, tid, w, l);
         }
     }
 }
@@ -128,9 +136,44 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N
 }
 
 // ---------------------------------------------------------------- launch
+template <class Kind, class D, int R, int C, int W, bool GATED>
+int launch_thin(bool once, const GemmArgs& g, hipStream_t s) {
+    constexpr int kWide = GATED ? 8 * C : 16 * C;
+    return once ? gemm_launch(gemm_thin<Kind, D, R, C, W, true, GATED>, g, 16 * R, kWide, 64 * W, s)
+                : gemm_launch(gemm_thin<Kind, D, R, C, W, false, GATED>, g, 16 * R, kWide, 64 * W, s);
+}
+
 template <class Kind, class D, bool GATED, bool TB>
 int gemm16_t(const GemmArgs& g, hipStream_t s) {
-    return gemm_launch(gemm_staged<Kind, D, GATED, TB>, g, 128, GATED ? 64 : 128, 256, s);
+    // bn rows of B (TB: columns) a tile
+    const auto tiles = [&](int64_t bm, int64_t bn) { return spx::tiles(g, bm, GATED ? bn / 2 : bn); };
+    const auto launch = [&](auto kernel, int64_t bm, int64_t bn, int threads) {
+        return gemm_launch(kernel, g, bm, GATED ? bn / 2 : bn, threads, s);
+    };
+    const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
+    const int64_t mid = tiles(128, 128);
+    const bool any = !aligned16(g);
+    if (g.K < 16 || mid > kMostTiles) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
+    const bool few = tiles(16, 32) <= kMostTiles;
+    const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
+    const bool deep = g.K > 2048;
+    const bool once = !any && g.S <= 32 * groups;
+    if constexpr (!TB) {
+        if (tiles(16, 32) <= 128) return launch_thin<Kind, D, 1, GATED ? 2 : 1, 8, GATED>(once, g, s);
+        if (tiles(16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
+            return launch_thin<Kind, D, 1, 2, 4, GATED>(once, g, s);
+        if (tiles(32, 32) <= 256 || (experts && g.S <= 16 * groups && deep))
+            return launch_thin<Kind, D, 2, 2, 4, GATED>(once, g, s);
+        if (tiles(32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
+            return launch_thin<Kind, D, 2, 4, 4, GATED>(once, g, s);
+    }
+    if (any) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
+    if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
+        return launch(gemm_big<Kind, D, 2, 4, false, GATED, TB>, 128, 128, 256);
+    const int64_t cols = GATED ? 2 * g.N : g.N, wide = (cols + 255) / 256 * 256, narrow = (cols + 127) / 128 * 128;
+    if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
+        return launch(gemm_big<Kind, D, 2, 2, false, GATED, TB>, 128, 128, 256);
+    return launch(gemm_big<Kind, D, 4, 2, false, GATED, TB>, 256, 256, 512);
 }
 
 int grad_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
@@ -140,12 +183,26 @@ int grad_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
 
 template <class Kind, class D>
 int rows_sum_t(GradArgs g, hipStream_t s) {
-    g.m_tiles = (uint32_t)((g.M + 127) / 128);
-    g.n_tiles = (uint32_t)((g.N + 127) / 128);
-    const int64_t n = (int64_t)g.m_tiles * g.n_tiles * g.splits * g.E;
-    if (n >= (int64_t)1 << 31) return SP_ERR_SIZE;
-    hipLaunchKernelGGL((gemm_rows_sum<Kind, D, 2, true>), dim3((unsigned)std::min(n, kMostTiles)), dim3(256), 0, s, g);
-    if (hipGetLastError() != hipSuccess) return SP_ERR_HIP;
+    const bool any = ((uintptr_t)g.P | (uintptr_t)g.Q | (uintptr_t)g.ldp | (uintptr_t)g.ldq) % 16 != 0;
+    const auto launch = [&](auto kernel, int64_t size, int threads) {
+        g.m_tiles = (uint32_t)((g.M + size - 1) / size);
+        g.n_tiles = (uint32_t)((g.N + size - 1) / size);
+        const int64_t n = (int64_t)g.m_tiles * g.n_tiles * g.splits * g.E;
+        if (n >= (int64_t)1 << 31) return SP_ERR_SIZE;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(n, kMostTiles)), dim3(threads), 0, s, g);
+        return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
+    };
+    const int64_t mid = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.E * g.splits;
+    const auto go = [&](auto part, auto gather) {
+        constexpr bool P = decltype(part)::value, G = decltype(gather)::value;
+        return any || mid > kMostTiles ? launch(gemm_rows_sum<Kind, D, 2, true, P, G>, 128, 256)
+               : mid < 512             ? launch(gemm_rows_sum<Kind, D, 2, false, P, G>, 128, 256)
+                                       : launch(gemm_rows_sum<Kind, D, 4, false, P, G>, 256, 512);
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    const int rc = g.splits > 1 ? (g.src ? go(yes, yes) : go(yes, no)) : (g.src ? go(no, yes) : go(no, no));
+    if (rc) return rc;
     if (g.splits > 1) {
         const int64_t chunks = g.E * g.M * ((g.N + 3) / 4);
         hipLaunchKernelGGL((add_parts_kernel<D>), dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 20)), dim3(256), 0,

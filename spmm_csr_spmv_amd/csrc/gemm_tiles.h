@@ -323,61 +323,59 @@ struct FastDiv {
     }
 };
 
-// Where a lane's copy j of a step reads an operand whose rows are steps of the sum.
-template <int WN>
+// Where a lane's copy j of a step reads an operand whose rows are steps of the sum.  GATHER: row i of the sum is the
+// row of slot src[i]; the sources are read with scalar loads, which do not queue behind the copies in flight.
+template <int WN, bool GATHER>
 struct BigTransposed {
-    const int8_t* base;          // the first row's bytes from the tile's first column on, this lane's own chunk
+    static constexpr int kWave = 8 / WN;  // rows of one copy of a wave
+    const int8_t* base;          // the lane's chunk in its row of copy 0 (GATHER: in row 0)
     int64_t ld;
     int rows, row0;              // rows of the sum; the lane's row of copy 0
-    int cols;                    // elements from the lane's chunk to the row's end (load)
-    const int32_t* src;          // or NULL: the rows' slots from the first row on
+    int cols;                    // load: elements from the lane's chunk to the row's end
+    int w;                       // GATHER only, as what follows
+    const int32_t* src;          // the rows' slots
     FastDiv slots;
-    int64_t a_rows;              // rows that a gathered operand has
-    int w;
-    static constexpr int kWave = 8 / WN;  // rows of one copy of a wave
-    // first: row 0; width: the rows' elements; n0: the tile's first column
+    int64_t a_rows;              // rows that there are
+    // first: row 0; width: the rows' elements; n0: the tile's first column; STAGED: for load(), else for at()
+    template <bool STAGED>
     __device__ __forceinline__ void place(const int8_t* first, int64_t ld_, int rows_, int64_t n0, int64_t width, int w_,
                                           int l) {
         constexpr int kChunks = 8 * WN;
         w = w_;
-        const int rw = l / kChunks;
-        row0 = w * kWave + rw;
+        row0 = w * kWave + l / kChunks;
         const int chunk = (l % kChunks) ^ (4 * (row0 & 3));
         cols = (int)min(width - n0 - chunk * 8, (int64_t)8);
-        base = first + min(2 * n0 + 16 * chunk, (2 * width - 1) & ~(int64_t)15);
+        const int64_t at = 2 * n0 + 16 * chunk;
+        base = first + (STAGED ? at : min(at, (2 * width - 1) & ~(int64_t)15)) + (GATHER ? 0 : row0 * ld_);
         ld = ld_;
         rows = rows_;
-        src = nullptr;
     }
-    __device__ __forceinline__ void any(const int8_t* first, int64_t n0, int l) {  // load() wants its own chunk
-        base = first + 2 * n0 + 16 * ((l % (8 * WN)) ^ (4 * (row0 & 3)));
-    }
-    __device__ __forceinline__ int64_t row(int j, int step) const {  // -1: none
-        const int r = step * 64 + 16 * j + row0;
-        if (!src) return r < rows ? r : -1;
-        // the same for all lanes but for which of the wave's rows is theirs: scalar loads, which do not
-        // queue behind the copies in flight
-        const __attribute__((address_space(4))) int32_t* s = (const __attribute__((address_space(4))) int32_t*)src;
-        const int u = step * 64 + 16 * j + w * kWave;
-        int f = -1;
+    // The lane's chunk of its row of copy j; NULL where there is no such row.
+    __device__ __forceinline__ const int8_t* row(int j, int step) const {
+        const int u = step * 64 + 16 * j;
+        if constexpr (!GATHER) {
+            return u + row0 < rows ? base + (int64_t)u * ld : nullptr;
+        } else {
+            const __attribute__((address_space(4))) int32_t* s = (const __attribute__((address_space(4))) int32_t*)src;
+            int64_t off = -1;
 #pragma unroll
-        for (int i = 0; i < kWave; ++i) {
-            const int v = u + i < rows ? s[u + i] : -1;
-            f = row0 == w * kWave + i ? v : f;
+            for (int i = 0; i < kWave; ++i) {
+                const int at = u + w * kWave + i, f = at < rows ? s[at] : -1, t = slots(max(f, 0));
+                const int64_t o = f >= 0 && t < a_rows ? t * ld : -1;
+                off = row0 == w * kWave + i ? o : off;
+            }
+            return off >= 0 ? base + off : nullptr;
         }
-        const int t = slots(max(f, 0));
-        return f >= 0 && t < a_rows ? t : -1;
     }
     __device__ __forceinline__ const int8_t* at(int j, int step) const {
-        const int64_t r = row(j, step);
-        return r >= 0 ? base + r * ld : big_zeros;
+        const int8_t* p = row(j, step);
+        return p ? p : big_zeros;
     }
     template <bool>
     __device__ __forceinline__ i32x4 load(int j, int step, bool) const {
-        const int64_t r = row(j, step);
+        const int8_t* p = row(j, step);
         i32x4 v = {0, 0, 0, 0};
-        if (r < 0 || cols <= 0) return v;
-        const int8_t* p = base + r * ld;
+        if (!p || cols <= 0) return v;
         if (cols == 8) return *reinterpret_cast<const i32x4_u*>(p);
 #pragma unroll
         for (int i = 0; i < 7; ++i)
@@ -813,8 +811,8 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
     if constexpr (TB) {
-        BigTransposed<WN> sb;
-        sb.place(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
+        BigTransposed<WN, false> sb;
+        sb.template place<false>(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
         big_sums<Kind, WN, ST, F, false, true, ONCE>(acc, m, sa, sb, steps, left, tid, w, l);
     } else {
         BigDirect sb;
@@ -897,9 +895,8 @@ __device__ __forceinline__ void staged_tile(const GemmArgs& g, int e, int64_t lo
     typename Kind::S16 acc[F][2];
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     if constexpr (TB) {
-        BigTransposed<2> sb;
-        sb.place(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
-        sb.any(g.B + e * g.strideb, n0, l);
+        BigTransposed<2, false> sb;
+        sb.template place<true>(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
         staged_sums<Kind, F, false, true>(acc, m, sa, sb, steps, w, l);
     } else {
         BigDirect sb;
