@@ -11,6 +11,7 @@
 // across lanes in a fixed order.  Squares beyond fp32's range: a row whose sum of squares is
 // not below 2^120 (or, with an eps near zero, not above 2^-60) is summed again scaled by 2^-96 (2^96).
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "moe.h"
@@ -21,7 +22,7 @@ namespace spx {
 namespace {
 
 constexpr float kTiny = 0x1p-119f;  // rows whose largest magnitude is below it have the scale 0
-constexpr int kHeld = 4;            // chunks of a row that a lane holds
+constexpr int kHeld = 2;            // chunks of a row that a lane holds
 
 struct NormArgs {
     int64_t rows, H;
@@ -38,30 +39,57 @@ struct NormArgs {
     float* scale;             // int8 codes only
     const void* dY;           // backward only, as what follows
     int64_t lddy;
-    float* part;              // [parts][H]: sums of dy n over some rows each, or NULL
+    float* part;              // [parts][part_stride(H)]: sums of dy n over some rows each, or NULL
     float* rstd;              // or NULL: i of every row
 };
 
-// Sum and maximum over the TPR lanes that share a row, in every one of them.
-template <int TPR, class F>
-__device__ __forceinline__ float across(float v, float (&part)[4], F f) {
-    v = f(v, swz_xor<1>(v));
-    v = f(v, swz_xor<2>(v));
-    v = f(v, swz_xor<4>(v));
-    v = f(v, swz_xor<8>(v));
-    if (TPR >= 64) {
-        v = f(v, swz_xor<16>(v));
-        v = f(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)),
-              __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)));
+__host__ __device__ constexpr int64_t part_stride(int64_t n) { return (n + 3) / 4 * 4; }
+
+// The TPR lanes that share a row reduce two values at a time, in a fixed order, every lane getting both results.
+// Two places in LDS take turns, so that one barrier a call suffices.
+template <int TPR>
+struct Across {
+    static constexpr int kWaves = TPR / 64 > 0 ? TPR / 64 : 1;
+    float (*part)[2][kWaves];  // [2]
+    int turn;
+    template <class F>
+    static __device__ __forceinline__ float wave(float v, F f) {
+        v = f(v, swz_xor<1>(v));
+        v = f(v, swz_xor<2>(v));
+        v = f(v, swz_xor<4>(v));
+        v = f(v, swz_xor<8>(v));
+        if (TPR >= 64) {
+            v = f(v, swz_xor<16>(v));
+            v = f(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)),
+                  __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)));
+        }
+        return v;
     }
-    if (TPR == 256) {
-        __syncthreads();  // part[] has been read
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = f(f(part[0], part[1]), f(part[2], part[3]));
+    template <class F>
+    static __device__ __forceinline__ float waves(const float* v, F f) {
+        float w[kWaves];
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) w[i] = v[i];
+#pragma unroll
+        for (int d = 1; d < kWaves; d *= 2)
+#pragma unroll
+            for (int i = 0; i < kWaves; i += 2 * d) w[i] = f(w[i], w[i + d]);
+        return w[0];
     }
-    return v;
-}
+    template <class F, class G>
+    __device__ __forceinline__ void operator()(float& a, float& b, F f, G g) {
+        a = wave(a, f);
+        b = wave(b, g);
+        if (kWaves > 1) {
+            auto& p = part[turn];
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) p[0][threadIdx.x >> 6] = a, p[1][threadIdx.x >> 6] = b;
+            __syncthreads();
+            a = waves(p[0], f);
+            b = waves(p[1], g);
+        }
+    }
+};
 struct Add {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
@@ -99,21 +127,42 @@ __device__ __forceinline__ void weights_at(const void* weight, int64_t k, int64_
     }
 }
 
+// Threads of a workgroup, and rows that it takes at a time.
+template <int TPR>
+constexpr int kThreads = TPR > 256 ? TPR : 256;
+template <int TPR>
+constexpr int kRows = kThreads<TPR> / TPR;
+
 template <int TPR>
 __device__ __forceinline__ int64_t first_row() {
     const int sub = threadIdx.x / TPR;
-    return (int64_t)blockIdx.x * (256 / TPR) + (TPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+    return (int64_t)blockIdx.x * kRows<TPR> + (TPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
 }
 
-template <class D, class W, int TPR, bool I8>
-__global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
+// A chunk of a row, len elements of which are inside.  LINES: whole, and rows lie on 128-byte lines, of which no other
+// row has a part: non-temporal.
+template <class T, bool LINES>
+__device__ __forceinline__ typename Chunk<T>::V norm_load(const T* p, int64_t len) {
+    return LINES ? chunk_stream(p) : chunk_load(p, len);
+}
+template <class T, bool LINES>
+__device__ __forceinline__ void norm_store(T* p, int64_t len, typename Chunk<T>::V v) {
+    if (LINES)
+        chunk_stream(p, v);
+    else
+        chunk_store(p, len, v);
+}
+
+template <class D, class W, int TPR, bool LINES, bool I8>
+__global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
     typedef typename D::T T;
     typedef typename Chunk<T>::V V;
     constexpr int N = Chunk<T>::N;
-    __shared__ float part[4];
+    __shared__ float part[2][2][Across<TPR>::kWaves];
+    Across<TPR> across{part, 0};
     const int lane = threadIdx.x % TPR;
     const int64_t chunks = (g.H + N - 1) / N;
-    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * (256 / TPR)) {
+    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * kRows<TPR>) {
         const T* x = (const T*)g.X + row * g.ldx;
         const T* r = g.R ? (const T*)g.R + row * g.ldr : nullptr;
         T* sum = g.sum ? (T*)g.sum + row * g.lds : nullptr;
@@ -128,15 +177,13 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
             }
         };
         // s of chunk c, formed and stored
-        const auto first = [&](int64_t c, float (&t)[N]) {
+        const auto first = [&](int64_t c, V v, V q, float (&t)[N]) {
             const int64_t k = c * N, len = g.H - k;
-            V v = chunk_load(x + k, len);
             if (r) {
-                const V q = chunk_load(r + k, len);
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[i] = D::down(D::up(v[i]) + D::up(q[i]));
             }
-            if (sum) chunk_store(sum + k, len, v);
+            if (sum) norm_store<T, LINES>(sum + k, len, v);
             float s[N];
             weights_at<W, N>(g.weight, k, len, t);
 #pragma unroll
@@ -157,15 +204,23 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
                 t[i] *= s[i];
             }
         };
+        const auto load = [&](const T* p, int64_t c) { return norm_load<T, LINES>(p + c * N, g.H - c * N); };
+        V vx[kHeld], vr[kHeld];
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
-            if (lane + h * TPR < chunks) first(lane + h * TPR, held[h]);
+            if (lane + h * TPR < chunks) {
+                vx[h] = load(x, lane + h * TPR);
+                if (r) vr[h] = load(r, lane + h * TPR);
+            }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (lane + h * TPR < chunks) first(lane + h * TPR, vx[h], vr[h], held[h]);
         for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
             float t[N];
-            first(c, t);
+            const V v = load(x, c);
+            first(c, v, r ? load(r, c) : v, t);
         }
-        ss = across<TPR>(ss, part, Add());
-        if (I8) most = across<TPR>(most, part, Most());
+        across(ss, most, Add(), Most());
         float f = range_factor(ss, g.eps);
         if (I8 && !(most < 0x1p120f)) f = 0x1p-96f;
         if (f != 1.0f) {  // rare: the same for all lanes of the row
@@ -175,8 +230,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
                 again(c, f, s, t);
                 sums(s, t);
             }
-            ss = across<TPR>(ss, part, Add());
-            if (I8) most = across<TPR>(most, part, Most());
+            across(ss, most, Add(), Most());
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
         float top = 1.0f, by = 1.0f;
@@ -196,7 +250,7 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
                 V o;
 #pragma unroll
                 for (int i = 0; i < N; ++i) o[i] = D::down(t[i] * times);
-                chunk_store((T*)g.Y + row * g.ldy + k, len, o);
+                norm_store<T, LINES>((T*)g.Y + row * g.ldy + k, len, o);
             } else {
                 // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits;
                 // the product with a rounded 1 / top is off by less than 1e-4 of a code: near a half divide
@@ -242,114 +296,135 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
     }
 }
 
-// The gradient.  Rows of up to kHeld chunks a lane are held, and a lane adds up its columns' dy n over
-// the rows of its workgroup, whose sums go to part[blockIdx.x] (PARTS).  Longer rows leave i in rstd.
-template <class D, class W, int TPR, bool PARTS>
-__global__ __launch_bounds__(256) void rms_norm_backward_kernel(NormArgs g) {
+// The gradient.  Rows of up to kHeld chunks a lane are held (PARTS): the next row's loads are in flight while a row is
+// worked on, and a lane adds up its columns' dy n over the rows of its workgroup, whose sums go to
+// part[blockIdx.x].  Longer rows are read again and leave i in rstd.
+template <class D, class W, int TPR, bool LINES, bool PARTS>
+__global__ __launch_bounds__(kThreads<TPR>, 3) void rms_norm_backward_kernel(NormArgs g) {
     typedef typename D::T T;
     typedef typename Chunk<T>::V V;
-    constexpr int N = Chunk<T>::N, R = 256 / TPR;
-    __shared__ float part[4];
+    constexpr int N = Chunk<T>::N, R = kRows<TPR>;
+    __shared__ float part[2][2][Across<TPR>::kWaves];
+    Across<TPR> across{part, 0};
     const int lane = threadIdx.x % TPR;
-    const int64_t chunks = (g.H + N - 1) / N;
-    float acc[PARTS ? kHeld : 1][N];
+    const int64_t chunks = (g.H + N - 1) / N, step = (int64_t)gridDim.x * R;
+    float acc[PARTS ? kHeld : 1][N], w[PARTS ? kHeld : 1][N];
 #pragma unroll
-    for (auto& a : acc)
+    for (int h = 0; h < (PARTS ? kHeld : 1); ++h)
 #pragma unroll
-        for (float& v : a) v = 0.0f;
-    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * R) {
-        const T* x = (const T*)g.X + row * g.ldx;
-        const T* y = (const T*)g.dY + row * g.lddy;
-        const T* d = g.R ? (const T*)g.R + row * g.ldr : nullptr;
-        V hx[kHeld], hy[kHeld], hd[kHeld];
+        for (int i = 0; i < N; ++i) acc[h][i] = w[h][i] = 0.0f;
+    const auto weights = [&](int64_t c, float (&v)[N]) { weights_at<W, N>(g.weight, c * N, g.H - c * N, v); };
+    if (PARTS)
+#pragma unroll
+        for (int h = 0; h < (PARTS ? kHeld : 1); ++h)
+            if (lane + h * TPR < chunks) weights(lane + h * TPR, w[h]);
+    const auto at = [&](const void* p, int64_t ld, int64_t row, int64_t c) { return (const T*)p + row * ld + c * N; };
+    const auto load = [&](const T* p, int64_t c) { return norm_load<T, LINES>(p, g.H - c * N); };
+    struct Held {
+        V x[kHeld], y[kHeld], d[kHeld];
+    };
+    const auto hold = [&](Held& b, int64_t row) {
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int64_t c = lane + h * TPR;
+            if (c < chunks) {
+                b.x[h] = load(at(g.X, g.ldx, row, c), c);
+                b.y[h] = load(at(g.dY, g.lddy, row, c), c);
+                if (g.R) b.d[h] = load(at(g.R, g.ldr, row, c), c);
+            }
+        }
+    };
+    int64_t row = first_row<TPR>();
+    Held next;
+    if (PARTS && row < g.rows) hold(next, row);
+    for (; row < g.rows; row += step) {
+        const Held now = next;
+        if (PARTS && row + step < g.rows) hold(next, row + step);
         float ss = 0.0f, dot = 0.0f;  // of s^2 and of dn s
-        const auto sums = [&](int64_t c, const V& vx, const V& vy, float f) {
-            float w[N];
-            weights_at<W, N>(g.weight, c * N, g.H - c * N, w);
+        const auto sums = [&](const V& vx, const V& vy, const float (&u)[N], float f) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float s = D::up(vx[i]) * f;
                 ss = fmaf(s, s, ss);
-                dot = fmaf(D::up(vy[i]) * w[i], s, dot);
+                dot = fmaf(D::up(vy[i]) * u[i], s, dot);
             }
         };
         const auto rest = [&](int64_t from, float f) {
-            for (int64_t c = from; c < chunks; c += TPR) sums(c, chunk_load(x + c * N, g.H - c * N), chunk_load(y + c * N, g.H - c * N), f);
-        };
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
-            const int64_t k = (int64_t)(lane + h * TPR) * N;
-            if (k < g.H) {
-                hx[h] = chunk_load(x + k, g.H - k);
-                hy[h] = chunk_load(y + k, g.H - k);
-                if (d) hd[h] = chunk_load(d + k, g.H - k);
+            for (int64_t c = from; c < chunks; c += TPR) {
+                float u[N];
+                weights(c, u);
+                sums(chunk_load(at(g.X, g.ldx, row, c), g.H - c * N), chunk_load(at(g.dY, g.lddy, row, c), g.H - c * N), u, f);
             }
-        }
+        };
+        if (PARTS) {
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (lane + h * TPR < chunks) sums(lane + h * TPR, hx[h], hy[h], 1.0f);
-        if (!PARTS) rest(lane + kHeld * TPR, 1.0f);
-        ss = across<TPR>(ss, part, Add());
-        dot = across<TPR>(dot, part, Add());
+            for (int h = 0; h < (PARTS ? kHeld : 1); ++h)
+                if (lane + h * TPR < chunks) sums(now.x[h], now.y[h], w[h], 1.0f);
+        } else {
+            rest(lane, 1.0f);
+        }
+        across(ss, dot, Add(), Add());
         const float f = range_factor(ss, g.eps);
         if (f != 1.0f) {
             ss = dot = 0.0f;
             rest(lane, f);
-            ss = across<TPR>(ss, part, Add());
-            dot = across<TPR>(dot, part, Add());
+            across(ss, dot, Add(), Add());
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
         const float mean = dot * unit / (float)g.H;  // of dn n
         if (!PARTS && g.rstd && lane == 0) g.rstd[row] = inv;
-        const auto out = [&](int64_t c, const V& vx, const V& vy, const V& vd, float (&sum)[N]) {
-            const int64_t k = c * N, len = g.H - k;
-            float w[N];
-            weights_at<W, N>(g.weight, k, len, w);
+        const auto out = [&](int64_t c, const V& vx, const V& vy, const V& vd, const float (&u)[N], float (&sum)[N]) {
             V o;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float n = D::up(vx[i]) * inv, dy = D::up(vy[i]);
-                float v = inv * fmaf(-n, mean, dy * w[i]);
-                if (d) v += D::up(vd[i]);
+                float v = inv * fmaf(-n, mean, dy * u[i]);
+                if (g.R) v += D::up(vd[i]);
                 o[i] = D::down(v);
                 sum[i] = fmaf(dy, n, sum[i]);
             }
-            chunk_store((T*)g.Y + row * g.ldy + k, len, o);
+            norm_store<T, LINES>((T*)g.Y + row * g.ldy + c * N, g.H - c * N, o);
         };
+        if (PARTS) {
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (lane + h * TPR < chunks) out(lane + h * TPR, hx[h], hy[h], hd[h], acc[PARTS ? h : 0]);
-        if (!PARTS)
-            for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
-                const int64_t k = c * N, len = g.H - k;
-                const V vx = chunk_load(x + k, len), vy = chunk_load(y + k, len);
-                out(c, vx, vy, d ? chunk_load(d + k, len) : vx, acc[0]);
+            for (int h = 0; h < (PARTS ? kHeld : 1); ++h)
+                if (lane + h * TPR < chunks) out(lane + h * TPR, now.x[h], now.y[h], now.d[h], w[h], acc[h]);
+        } else {
+            for (int64_t c = lane; c < chunks; c += TPR) {
+                const int64_t len = g.H - c * N;
+                const V vx = chunk_load(at(g.X, g.ldx, row, c), len), vy = chunk_load(at(g.dY, g.lddy, row, c), len);
+                weights(c, w[0]);
+                out(c, vx, vy, g.R ? chunk_load(at(g.R, g.ldr, row, c), len) : vx, w[0], acc[0]);
             }
+        }
     }
     if constexpr (PARTS) {
         if (!g.part) return;
-        float* to = g.part + (int64_t)blockIdx.x * g.H;
+        typedef float F4 __attribute__((ext_vector_type(4)));
+        F4* to = reinterpret_cast<F4*>(g.part + (int64_t)blockIdx.x * part_stride(g.H));
+        const int64_t quads = part_stride(g.H) / 4;
         if constexpr (R == 1) {
 #pragma unroll
             for (int h = 0; h < kHeld; ++h)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int64_t k = (int64_t)(lane + h * TPR) * N + i;
-                    if (k < g.H) to[k] = acc[h][i];
+                for (int i = 0; i < N; i += 4) {
+                    const int64_t q = (int64_t)(lane + h * TPR) * (N / 4) + i / 4;
+                    if (q < quads) to[q] = F4{acc[h][i], acc[h][i + 1], acc[h][i + 2], acc[h][i + 3]};
                 }
         } else {
-            // the workgroup's R rows at a time added in their order
-            constexpr int kCols = TPR * kHeld * N;
-            __shared__ float all[R][kCols];
+            // what the workgroup's R rows at a time came to, added in their order
+            constexpr int kQuads = TPR * kHeld * N / 4;
+            __shared__ F4 all[R][kQuads];
 #pragma unroll
             for (int h = 0; h < kHeld; ++h)
 #pragma unroll
-                for (int i = 0; i < N; ++i) all[threadIdx.x / TPR][(lane + h * TPR) * N + i] = acc[h][i];
+                for (int i = 0; i < N; i += 4)
+                    all[threadIdx.x / TPR][(lane + h * TPR) * (N / 4) + i / 4] = F4{acc[h][i], acc[h][i + 1], acc[h][i + 2], acc[h][i + 3]};
             __syncthreads();
-            for (int k = threadIdx.x; k < g.H; k += 256) {
-                float v = all[0][k];
-                for (int j = 1; j < R; ++j) v += all[j][k];
-                to[k] = v;
+            for (int q = threadIdx.x; q < quads; q += kThreads<TPR>) {
+                F4 v = all[0][q];
+                for (int j = 1; j < R; ++j) v += all[j][q];
+                to[q] = v;
             }
         }
     }
@@ -365,42 +440,52 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs g, int64_t e
     float v = 0.0f;
 #pragma unroll 4
     for (int64_t r = from; r < to; ++r) v = fmaf(D::up(y[r * g.lddy]), D::up(x[r * g.ldx]) * g.rstd[r], v);
-    g.part[blockIdx.y * g.H + k] = v;
+    g.part[blockIdx.y * part_stride(g.H) + k] = v;
 }
 
-// dweight = the parts' sum: 16 columns a workgroup, 16 threads to a column, each every 16th part, added in order.
+// dweight = the parts' sum: 16 columns a workgroup, 64 threads to four of them, each every 64th part, added in order.
 __global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ part, int64_t parts, int64_t H,
                                                          float* __restrict__ dweight) {
-    __shared__ float all[16][17];
-    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-    const int64_t k = (int64_t)blockIdx.x * 16 + c;
-    float v = 0.0f;
+    typedef float F4 __attribute__((ext_vector_type(4)));
+    __shared__ F4 all[64][4];
+    const int c = threadIdx.x & 3, r = threadIdx.x >> 2;
+    const int64_t k = (int64_t)blockIdx.x * 16 + 4 * c, ld = part_stride(H);
+    F4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (k < H)
-#pragma unroll 4
-        for (int64_t p = r; p < parts; p += 16) v += part[p * H + k];
+#pragma unroll 8
+        for (int64_t p = r; p < parts; p += 64) v += *reinterpret_cast<const F4*>(part + p * ld + k);
     all[r][c] = v;
     __syncthreads();
-    if (r == 0 && k < H) {
-        for (int j = 1; j < 16; ++j) v += all[j][c];
-        dweight[k] = v;
-    }
+    if (threadIdx.x >= 16) return;
+    const float* f = reinterpret_cast<const float*>(all) + threadIdx.x;
+    float sum = 0.0f;
+#pragma unroll 16
+    for (int j = 0; j < 64; ++j) sum += f[16 * j];
+    const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    if (at < H) dweight[at] = sum;
 }
 
 // ---------------------------------------------------------------- launch
 int status(hipError_t e) { return e == hipSuccess ? SP_OK : SP_ERR_HIP; }
 int chunk_of(int32_t dtype) { return dtype == SP_F32 ? 4 : 8; }
-// Lanes a row: the fewest whose registers hold it.
-int norm_lanes(int64_t H, int32_t dtype) {
+// Lanes a row: the fewest whose registers hold it, up to 1024; the gradient's, which hold more, up to 512.
+constexpr int kMostForward = 1024, kMostBackward = 512;
+int norm_lanes(int64_t H, int32_t dtype, int most) {
     const int64_t chunks = (H + chunk_of(dtype) - 1) / chunk_of(dtype);
-    return chunks <= 16 * kHeld ? 16 : chunks <= 64 * kHeld ? 64 : 256;
+    return chunks <= 16 * kHeld ? 16 : chunks <= 64 * kHeld ? 64 : chunks <= 256 * kHeld ? 256 : most;
 }
-bool held(int64_t H, int32_t dtype) { return (H + chunk_of(dtype) - 1) / chunk_of(dtype) <= 256 * kHeld; }
+bool held(int64_t H, int32_t dtype) { return (H + chunk_of(dtype) - 1) / chunk_of(dtype) <= kMostBackward * kHeld; }
+// Whether rows are whole lines that no other row shares.
+bool on_lines(const void* p, int64_t ld, int64_t H, int32_t dtype) {
+    const int64_t size = dtype == SP_F32 ? 4 : 2;
+    return ((uintptr_t)p | (uintptr_t)(ld * size) | (uintptr_t)(H * size)) % 128 == 0;
+}
 
 constexpr int64_t kMostGroups = 1 << 20;  // workgroups; more rows take several rounds
 
 // Workgroups of the gradient, and so parts of dweight.
 int64_t backward_groups(int64_t rows, int64_t H, int32_t dtype) {
-    const int64_t per = 256 / norm_lanes(H, dtype);
+    const int lanes = norm_lanes(H, dtype, kMostBackward), per = std::max(256, lanes) / lanes;
     return std::min<int64_t>((rows + per - 1) / per, 1024);
 }
 // Rows a part of norm_columns_kernel.
@@ -410,12 +495,16 @@ template <int L>
 struct Lanes {
     static constexpr int value = L;
 };
-// go(type, weight's type, lanes)
-template <class Go>
-int norm_by(int32_t dtype, int32_t w_type, int64_t H, Go go) {
+// go(type, weight's type, lanes, on lines)
+template <int MOST, class Go>
+int norm_by(int32_t dtype, int32_t w_type, int64_t H, bool lines, Go go) {
     const auto lanes = [&](auto d, auto w) {
-        const int n = norm_lanes(H, dtype);
-        return n == 16 ? go(d, w, Lanes<16>()) : n == 64 ? go(d, w, Lanes<64>()) : go(d, w, Lanes<256>());
+        const int n = norm_lanes(H, dtype, MOST);
+        const auto with = [&](auto l) { return lines ? go(d, w, l, std::true_type()) : go(d, w, l, std::false_type()); };
+        return n == 16    ? go(d, w, Lanes<16>(), std::false_type())
+               : n == 64  ? with(Lanes<64>())
+               : n == 256 ? with(Lanes<256>())
+                          : with(Lanes<MOST>());
     };
     if (dtype == SP_F32) return lanes(F32(), F32());
     if (dtype == SP_BF16) return w_type == SP_F32 ? lanes(Bf16(), F32()) : lanes(Bf16(), Bf16());
@@ -428,23 +517,26 @@ int rms_norm_device(const NormRows& n, void* sum, int64_t lds, void* Y, int64_t 
     NormArgs g{};
     g.rows = n.rows, g.H = n.H, g.X = n.X, g.ldx = n.ldx, g.R = n.R, g.ldr = n.ldr, g.weight = n.weight, g.eps = n.eps;
     g.sum = sum, g.lds = lds, g.Y = Y, g.ldy = ldy, g.scale = scale;
-    return norm_by(n.dtype, n.w_type, n.H, [&](auto d, auto w, auto l) {
+    const bool lines = on_lines(n.X, n.ldx, n.H, n.dtype) && on_lines(n.R, n.R ? n.ldr : 0, n.H, n.dtype) &&
+                       on_lines(sum, sum ? lds : 0, n.H, n.dtype) && (scale || on_lines(Y, ldy, n.H, n.dtype));
+    return norm_by<kMostForward>(n.dtype, n.w_type, n.H, lines, [&](auto d, auto w, auto l, auto on) {
         typedef decltype(d) D;
         typedef decltype(w) W;
-        constexpr int L = decltype(l)::value, per = 256 / L;
-        const dim3 grid((unsigned)std::min<int64_t>((g.rows + per - 1) / per, kMostGroups));
+        constexpr int L = decltype(l)::value;
+        constexpr bool kLines = decltype(on)::value;
+        const dim3 grid((unsigned)std::min<int64_t>((g.rows + kRows<L> - 1) / kRows<L>, kMostGroups));
         if (scale)
-            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, true>), grid, dim3(256), 0, s, g);
+            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, kLines, true>), grid, dim3(kThreads<L>), 0, s, g);
         else
-            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, false>), grid, dim3(256), 0, s, g);
+            hipLaunchKernelGGL((rms_norm_kernel<D, W, L, kLines, false>), grid, dim3(kThreads<L>), 0, s, g);
         return status(hipGetLastError());
     });
 }
 
 size_t rms_norm_backward_bytes(int64_t rows, int64_t H, int32_t dtype) {
-    if (held(H, dtype)) return (size_t)backward_groups(rows, H, dtype) * H * sizeof(float);
+    if (held(H, dtype)) return (size_t)backward_groups(rows, H, dtype) * part_stride(H) * sizeof(float);
     const int64_t each = column_rows(rows);
-    return ((size_t)rows + (size_t)((rows + each - 1) / each) * H) * sizeof(float);
+    return ((size_t)part_stride(rows) + (size_t)((rows + each - 1) / each) * part_stride(H)) * sizeof(float);
 }
 
 int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, void* dX, int64_t lddx, float* dweight,
@@ -453,23 +545,27 @@ int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, vo
     g.rows = n.rows, g.H = n.H, g.X = n.X, g.ldx = n.ldx, g.R = n.R, g.ldr = n.ldr, g.weight = n.weight, g.eps = n.eps;
     g.dY = dY, g.lddy = lddy, g.Y = dX, g.ldy = lddx;
     const bool whole = held(n.H, n.dtype);
-    int64_t parts = 0;
+    const int64_t each = column_rows(n.rows);
+    const int64_t parts = n.rows == 0 ? 0 : whole ? backward_groups(n.rows, n.H, n.dtype) : (n.rows + each - 1) / each;
+    float* const part = (float*)work + (whole ? 0 : part_stride(n.rows));
+    if (dweight) {
+        g.part = part;
+        if (!whole) g.rstd = (float*)work;
+    }
     if (n.rows > 0) {
-        const int64_t each = column_rows(n.rows);
-        parts = whole ? backward_groups(n.rows, n.H, n.dtype) : (n.rows + each - 1) / each;
-        if (dweight) {
-            if (!whole) g.rstd = (float*)work;
-            g.part = (float*)work + (whole ? 0 : n.rows);
-        }
-        const int rc = norm_by(n.dtype, n.w_type, n.H, [&](auto d, auto w, auto l) {
+        const bool lines = on_lines(n.X, n.ldx, n.H, n.dtype) && on_lines(n.R, n.R ? n.ldr : 0, n.H, n.dtype) &&
+                           on_lines(dY, lddy, n.H, n.dtype) && on_lines(dX, lddx, n.H, n.dtype);
+        const int rc = norm_by<kMostBackward>(n.dtype, n.w_type, n.H, lines && whole, [&](auto d, auto w, auto l, auto on) {
             typedef decltype(d) D;
             typedef decltype(w) W;
             constexpr int L = decltype(l)::value;
+            constexpr bool kLines = decltype(on)::value;
             if (whole) {
-                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, true>), dim3((unsigned)parts), dim3(256), 0, s, g);
-            } else if constexpr (L == 256) {
-                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, false>),
-                                   dim3((unsigned)std::min<int64_t>(g.rows, kMostGroups)), dim3(256), 0, s, g);
+                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, kLines, true>), dim3((unsigned)parts), dim3(kThreads<L>), 0,
+                                   s, g);
+            } else if constexpr (L == kMostBackward && !kLines) {
+                hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, false, false>),
+                                   dim3((unsigned)std::min<int64_t>(g.rows, kMostGroups)), dim3(kThreads<L>), 0, s, g);
                 if (g.rstd && hipGetLastError() == hipSuccess)
                     hipLaunchKernelGGL((norm_columns_kernel<D>), dim3((unsigned)((g.H + 255) / 256), (unsigned)parts),
                                        dim3(256), 0, s, g, each);
@@ -479,8 +575,7 @@ int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, vo
         if (rc) return rc;
     }
     if (!dweight) return SP_OK;
-    hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((n.H + 15) / 16)), dim3(256), 0, s, (const float*)work + (whole ? 0 : n.rows),
-                       parts, n.H, dweight);
+    hipLaunchKernelGGL(norm_parts_kernel, dim3((unsigned)((n.H + 15) / 16)), dim3(256), 0, s, part, parts, n.H, dweight);
     return status(hipGetLastError());
 }
 
