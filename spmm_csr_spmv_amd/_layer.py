@@ -373,7 +373,7 @@ def _moe_gemm_backward(raw, dC, A, B, offsets, src, slots, dA, dB, work):
     sizes = _sizes(A, B, offsets, src, _columns(B, False))
     ld = _rows_like(dC, "dC", A, sizes[0], sizes[2])
     dA, dB, outputs = _gradients(sizes, A, B, dA, dB, dC, offsets, src)
-    need = 0 if dB is None else _bytes("moe_gemm_backward_bufsize", *sizes)
+    need = 0 if dA is None and dB is None else _bytes("moe_gemm_backward_bufsize", *sizes)
     work, nbytes = _work(work, need, A.device, dC, A, B, offsets, src, dA, dB)
     rc = lib().moe_gemm_backward(*sizes, dC.data_ptr(), ld, *_operand_args(A, B, offsets, src, slots), *outputs,
                                  _ptr(work), nbytes, raw)

@@ -107,6 +107,28 @@ __global__ __launch_bounds__(256) void add_parts_kernel(GradArgs g) {
     }
 }
 
+// dA = the parts' sum, in the order of the splits, for the rows that some expert has; a workgroup a row.
+template <class D>
+__global__ __launch_bounds__(256) void add_row_parts_kernel(GemmArgs g) {
+    for (int64_t p = blockIdx.x; p < g.S; p += gridDim.x) {
+        int mine = !g.offsets;
+        for (int e = threadIdx.x; e < g.E && !mine; e += 256) {
+            int a, b;
+            expert_rows(g, e, a, b);
+            mine = a <= p && p < b;
+        }
+        if (!__syncthreads_or(mine)) continue;
+        const float* from = g.part + p * g.N;
+        typename D::T* to = (typename D::T*)g.C + p * g.ldc;
+        for (int64_t n = threadIdx.x; n < g.N; n += 256) {
+            float sum = from[n];
+#pragma unroll 4
+            for (int s = 1; s < g.splits; ++s) sum += from[s * g.S * g.N + n];
+            to[n] = D::down(sum);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the gate's gradient
 // dpre[p] = [dg du] of the rows that some expert has, rows ldd elements apart; rounded to the operands' type,
 // which the matrix cores want.
@@ -153,7 +175,7 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
     const int64_t mid = tiles(128, 128);
     const bool any = !aligned16(g);
-    if (g.K < 16 || mid > kMostTiles) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
+    if ((g.K < 16 && g.splits <= 1) || mid > kMostTiles) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
     const bool few = tiles(16, 32) <= kMostTiles;
     const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
     const bool deep = g.K > 2048;
@@ -167,6 +189,15 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
         if (tiles(32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
             return launch_thin<Kind, D, 2, 4, 4, GATED>(once, g, s);
     }
+    if constexpr (TB) {
+        if (g.splits > 1) {
+            const int rc = any ? launch(gemm_staged<Kind, F32, false, true, true>, 128, 128, 256)
+                               : launch(gemm_big<Kind, F32, 2, 2, false, false, true, true>, 128, 128, 256);
+            if (rc) return rc;
+            hipLaunchKernelGGL((add_row_parts_kernel<D>), dim3((unsigned)std::min<int64_t>(g.S, 1 << 20)), dim3(256), 0, s, g);
+            return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
+        }
+    }
     if (any) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
         return launch(gemm_big<Kind, D, 2, 4, false, GATED, TB>, 128, 128, 256);
@@ -176,9 +207,19 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     return launch(gemm_big<Kind, D, 4, 2, false, GATED, TB>, 256, 256, 512);
 }
 
+// Parts that the sums of dA = dC B are cut into: as many as give 512 workgroups, of 128 rows of B at least each.
+int row_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
+    const int64_t tiles = std::max<int64_t>((S / 128 + std::min<int64_t>(E, S)) * ((N + 127) / 128), 1), steps = (M + 63) / 64;
+    const int64_t want = std::min<int64_t>({512 / tiles, steps / 2, 32});
+    if (want < 2) return 1;
+    const int64_t each = (steps + want - 1) / want;
+    return (int)((steps + each - 1) / each);  // none is empty
+}
+
+// Parts that an expert's rows are cut into for dB: as many as give 512 workgroups, of 256 rows at least each on the average.
 int grad_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
-    (void)S, (void)E, (void)M, (void)N;
-    return 1;
+    const int64_t tiles = std::max<int64_t>((M + 127) / 128 * ((N + 127) / 128) * E, 1);
+    return (int)std::max<int64_t>(std::min<int64_t>({512 / tiles, S / E / 256, 64}), 1);
 }
 
 template <class Kind, class D>
@@ -220,9 +261,11 @@ int by_type(int32_t dtype, Go go) {
 
 int64_t pre_stride(int64_t N) { return (2 * N + 63) / 64 * 64; }  // rows on 128-byte lines
 
+// Workspace of product_backward, whose two products use it one after the other.
 size_t parts_bytes(const Products& p, int64_t M) {
-    const int splits = grad_splits(p.S, p.E, M, p.K);
-    return splits > 1 ? (size_t)splits * p.E * M * p.K * sizeof(float) : 0;
+    const int rows = row_splits(p.S, p.E, M, p.K), sums = grad_splits(p.S, p.E, M, p.K);
+    const size_t a = rows > 1 ? (size_t)rows * p.S * p.K : 0, b = sums > 1 ? (size_t)sums * p.E * M * p.K : 0;
+    return std::max(a, b) * sizeof(float);
 }
 
 // dA and dB (either may be NULL) from dC, S x M.
@@ -231,6 +274,8 @@ int product_backward(const Products& p, int64_t M, const void* dC, int64_t ldc, 
     if (dA && p.S > 0 && p.K > 0) {
         GemmArgs g{p.S, p.K, 2 * M, (const int8_t*)dC, p.S, 2 * ldc, nullptr, nullptr, 1, (const int8_t*)p.B, 2 * p.ldb,
                    2 * p.strideb, nullptr, p.offsets, p.E, dA, ldda};
+        g.part = part;
+        g.splits = row_splits(p.S, p.E, M, p.K);
         const int rc = by_type(p.dtype, [&](auto k, auto d) { return gemm16_t<decltype(k), decltype(d), false, true>(g, s); });
         if (rc) return rc;
     }

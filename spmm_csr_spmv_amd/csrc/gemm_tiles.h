@@ -85,6 +85,8 @@ struct GemmArgs {
     int64_t ldp;
     int32_t act;
     uint32_t m_tiles, n_tiles; // m_tiles is an upper bound when offsets are given; the product fits 31 bits
+    float* part;              // the sums of a part of K each: [splits][S][N], or NULL
+    int32_t splits;
 };
 
 
@@ -225,6 +227,17 @@ __device__ __forceinline__ typename D::T scaled(int sum, float sa, float sb) {
     return round_alone<D>((float)sum * sa * sb);
 }
 
+// The bytes of v from byte n (0 .. 16) on, zeros behind them.
+__device__ __forceinline__ i32x4 shift_down(i32x4 v, int n) {
+    typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+    u64x2 x = __builtin_bit_cast(u64x2, v);
+    if (n >= 8) x = u64x2{x[1], 0};
+    const int bits = 8 * (n >= 8 ? n - 8 : n);
+    const uint64_t carry = bits ? x[1] << (64 - bits & 63) : 0;
+    x = bits >= 64 ? u64x2{0, 0} : u64x2{x[0] >> bits | carry, x[1] >> bits};
+    return __builtin_bit_cast(i32x4, x);
+}
+
 // Column i of a tile's rows of B: row of B's matrix.  Gated: blocks of 32 gate rows and the 32 up rows of the
 // same columns of C in turn.
 template <bool GATED>
@@ -296,13 +309,11 @@ struct BigDirect {
         const int64_t k = (int64_t)step * kBigK + chunk;
         if (K < 16) return load_short(p[j & 3], k, K);
         i32x4 v = load_any(p[j & 3], k, K);
-        if (!mask) return v;
-        if (ALONE) {
-            const int64_t drop = k - (K - 16);
-            return drop <= 0 ? v : drop >= 16 ? i32x4{0, 0, 0, 0} : __builtin_bit_cast(i32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * drop));
-        }
+        if (mask) {
+            if (ALONE) return shift_down(v, (int)min(max(k - (K - 16), (int64_t)0), (int64_t)16));
 #pragma unroll
-        for (int d = 0; d < 4; ++d) v[d] &= low_mask(k, K, d);
+            for (int d = 0; d < 4; ++d) v[d] &= low_mask(k, K, d);
+        }
         return v;
     }
 };
@@ -331,7 +342,8 @@ struct BigTransposed {
     const int8_t* base;          // the lane's chunk in its row of copy 0 (GATHER: in row 0)
     int64_t ld;
     int rows, row0;              // rows of the sum; the lane's row of copy 0
-    int cols;                    // load: elements from the lane's chunk to the row's end
+    int cols;                    // load: elements from the lane's chunk to the row's end, 8 at most
+    bool inside, narrow;         // load: all the tile's chunks are whole; rows shorter than a chunk
     int w;                       // GATHER only, as what follows
     const int32_t* src;          // the rows' slots
     FastDiv slots;
@@ -344,7 +356,9 @@ struct BigTransposed {
         w = w_;
         row0 = w * kWave + l / kChunks;
         const int chunk = (l % kChunks) ^ (4 * (row0 & 3));
-        cols = (int)min(width - n0 - chunk * 8, (int64_t)8);
+        cols = (int)max(min(width - n0 - chunk * 8, (int64_t)8), (int64_t)0);
+        inside = n0 + 64 * WN <= width;
+        narrow = width < 8;
         const int64_t at = 2 * n0 + 16 * chunk;
         base = first + (STAGED ? at : min(at, (2 * width - 1) & ~(int64_t)15)) + (GATHER ? 0 : row0 * ld_);
         ld = ld_;
@@ -371,16 +385,20 @@ struct BigTransposed {
         const int8_t* p = row(j, step);
         return p ? p : big_zeros;
     }
+    // Branches that all lanes take alike only: loads behind others would wait for one another.  A chunk that the
+    // row's end cuts is loaded with the elements before it and moved down.
     template <bool>
     __device__ __forceinline__ i32x4 load(int j, int step, bool) const {
         const int8_t* p = row(j, step);
-        i32x4 v = {0, 0, 0, 0};
-        if (!p || cols <= 0) return v;
-        if (cols == 8) return *reinterpret_cast<const i32x4_u*>(p);
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < cols) v[i >> 1] |= (int32_t)((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1)));
-        return v;
+        if (inside) return *reinterpret_cast<const i32x4_u*>(p ? p : big_zeros);
+        if (narrow) {
+            i32x4 v = {0, 0, 0, 0};
+            for (int i = 0; i < 7; ++i)
+                if (p && i < cols) v[i >> 1] |= (int32_t)((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1)));
+            return v;
+        }
+        const int8_t* at = p && cols > 0 ? p + 2 * cols - 16 : big_zeros;
+        return shift_down(*reinterpret_cast<const i32x4_u*>(at), 16 - 2 * cols);
     }
 };
 
@@ -801,6 +819,17 @@ __device__ __forceinline__ void big_out(const BigOut& g, const typename Kind::S1
     }
 }
 
+// The steps of part `split` of a sum whose B's rows are steps: C is then the part's sums.  No part is empty.
+__device__ __forceinline__ GemmArgs part_of(GemmArgs g, int split) {
+    const int64_t steps = (g.K + kBigK - 1) / kBigK, each = (steps + g.splits - 1) / g.splits, from = split * each;
+    g.A += from * kBigK;
+    g.B += from * (kBigK / 2) * g.ldb;
+    g.K = min(g.K - from * kBigK, each * kBigK);
+    g.C = g.part + split * g.S * g.N;
+    g.ldc = g.N;
+    return g;
+}
+
 // One tile of rows by expert.  TB: B's rows are the steps of the sum (g.K / 2 of them, g.N elements each).
 template <class Kind, class D, int WN, int ST, bool ONCE, bool GATED, bool TB, int F>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
@@ -852,8 +881,9 @@ __device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t m_tiles, u
     return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
 }
 
-template <class Kind, class D, int WN, int ST, bool ONCE, bool GATED, bool TB>
-__global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_big(GemmArgs g) {
+template <class Kind, class D, int WN, int ST, bool ONCE, bool GATED, bool TB, bool PART = false>
+__global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_big(GemmArgs args) {
+    const GemmArgs g = PART ? part_of(args, blockIdx.y) : args;
     constexpr int kBytes = 64 * WN * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
     __shared__ int32_t lrow[64 * WN + 2 * WN];  // row of A of every row of the tile, or -1; words of the waves
@@ -906,8 +936,9 @@ __device__ __forceinline__ void staged_tile(const GemmArgs& g, int e, int64_t lo
     big_out<Kind, D, 2, F, GATED>(big_out_of(g, lo, n0), acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, w, l);
 }
 
-template <class Kind, class D, bool GATED, bool TB>
-__global__ __launch_bounds__(256, 2) void gemm_staged(GemmArgs g) {
+template <class Kind, class D, bool GATED, bool TB, bool PART = false>
+__global__ __launch_bounds__(256, 2) void gemm_staged(GemmArgs args) {
+    const GemmArgs g = PART ? part_of(args, blockIdx.y) : args;
     constexpr int kBytes = 128 * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
     __shared__ int32_t lrow[128 + 4];
@@ -1144,7 +1175,8 @@ int gemm_launch(K kernel, GemmArgs g, int64_t bm, int64_t bn, int threads, hipSt
     if (n >= (int64_t)1 << 31) return SP_ERR_SIZE;
     g.m_tiles = (uint32_t)row_tiles(g, bm);
     g.n_tiles = (uint32_t)((g.N + bn - 1) / bn);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(n, kMostTiles)), dim3(threads), 0, s, g);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(n, kMostTiles), (unsigned)std::max(g.splits, 1)), dim3(threads), 0,
+                       s, g);
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 

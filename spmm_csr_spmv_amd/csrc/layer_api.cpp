@@ -160,7 +160,7 @@ int moe_gemm_backward(int64_t S, int32_t num_experts, int64_t N, int64_t K, int3
     if (ldc < N || too_far(S, ldc)) return SP_ERR_SIZE;
     if (!dC && S > 0 && N > 0) return SP_ERR_NULL;
     if (misaligned(dC, 2)) return SP_ERR_UNSUPPORTED;
-    if (dB) rc = workspace(work, work_bytes, moe_gemm_backward_bytes(p));
+    if (dA || dB) rc = workspace(work, work_bytes, moe_gemm_backward_bytes(p));
     return rc ? rc : moe_gemm_backward_device(p, dC, ldc, dA, ldda, dB, lddb, stridedb, work, (hipStream_t)stream);
 }
 
