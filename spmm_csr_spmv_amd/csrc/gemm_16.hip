@@ -29,25 +29,25 @@ struct GradArgs {
     uint32_t m_tiles, n_tiles;
 };
 
-// Tiles of dB, 64 WN square, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
+// Square tiles of dB, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
 // are split and the parts' fp32 sums (PART) added afterwards in the order of the splits.
-template <class Kind, class D, int WN, bool STAGED, bool PART, bool GATHER>
+template <class Kind, class D, class X, bool STAGED, bool PART, bool GATHER>
 __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uint32_t total, const BigBuffers<2>& m,
                                               int32_t* lrow, int tid, int w, int l) {
     // eight tiles in a row, which share a tile's columns of A, on one XCD
     const uint32_t v = t < total / 64 * 64 ? t / 64 * 64 + t % 8 * 8 + t / 8 % 8 : t;
     const uint32_t per = g.m_tiles * g.n_tiles, part = v / per, in = v % per;
     const int e = (int)(part / g.splits), split = (int)(part % g.splits);
-    const int64_t m0 = (int64_t)(in % g.m_tiles) * (64 * WN), n0 = (int64_t)(in / g.m_tiles) * (64 * WN);
+    const int64_t m0 = (int64_t)(in % g.m_tiles) * (X::kSize), n0 = (int64_t)(in / g.m_tiles) * (X::kSize);
     int a = 0, b = (int)g.S;
     if (g.offsets) expert_rows(g.offsets, g.E, g.S, e, a, b);
     a = __builtin_amdgcn_readfirstlane(a);
     b = __builtin_amdgcn_readfirstlane(b);
     const int each = (int)(((uint32_t)(b - a) + g.splits * 64u - 1) / (g.splits * 64u)) * 64;
     const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b), rows = min(each, b - from);
-    if (tid < 64 * WN) lrow[tid] = m0 + tid < g.M ? 0 : -1;
-    BigTransposed<WN, false> sa;
-    BigTransposed<WN, GATHER> sb;
+    for (int i = tid; i < X::kSize; i += X::kThreads) lrow[i] = m0 + i < g.M ? 0 : -1;
+    BigTransposed<X, false> sa;
+    BigTransposed<X, GATHER> sb;
     sa.template place<STAGED>(g.P + from * g.ldp, g.ldp, rows, m0, g.M, w, l);
     if constexpr (GATHER) {
         sb.template place<STAGED>(g.Q, g.ldq, rows, n0, g.N, w, l);
@@ -58,32 +58,33 @@ __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uin
         sb.template place<STAGED>(g.Q + from * g.ldq, g.ldq, (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0), n0,
                                   g.N, w, l);
     }
-    typename Kind::S16 acc[WN][2];
+    constexpr int F = X::CB;
+    typename Kind::S16 acc[F][X::U];
     const int steps = (rows + 63) >> 6;
     if constexpr (STAGED)
-        staged_sums<Kind, WN, true, true>(acc, m, sa, sb, steps, w, l);
+        staged_sums<Kind, F, true, true>(acc, m, sa, sb, steps, w, l);
     else
-        big_sums<Kind, WN, 2, WN, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
+        big_sums<Kind, X, 2, F, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
     BigOut o{(typename D::T*)g.C + e * g.stridec, g.ldc, g.N, m0, n0, nullptr, 0, 0};
     if (PART) o.C = g.part + ((int64_t)split * g.E + e) * g.M * g.N, o.ldc = g.N;
     const float* none = nullptr;
-    big_out<Kind, std::conditional_t<PART, F32, D>, WN, WN, false>(o, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, none, w, l);
+    big_out<Kind, std::conditional_t<PART, F32, D>, X, F, false>(o, acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, none, w, l);
 }
 
-template <class Kind, class D, int WN, bool STAGED, bool PART, bool GATHER>
-__global__ __launch_bounds__(128 * WN, 2) void gemm_rows_sum(GradArgs g) {
-    constexpr int kBytes = 64 * WN * kBigK;
+template <class Kind, class D, class X, bool STAGED, bool PART, bool GATHER>
+__global__ __launch_bounds__(X::kThreads, X::W == 8 || X::CB == 2 ? 2 : 1) void gemm_rows_sum(GradArgs g) {
+    constexpr int kBytes = X::kSize * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
-    __shared__ int32_t lrow[64 * WN];
+    __shared__ int32_t lrow[X::kSize];
     const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     const uint32_t total = g.m_tiles * g.n_tiles * (uint32_t)g.splits * (uint32_t)g.E;
     if constexpr (!STAGED) {  // as many workgroups as tiles
-        rows_sum_tile<Kind, D, WN, STAGED, PART, GATHER>(g, blockIdx.x, total, m, lrow, tid, w, l);
+        rows_sum_tile<Kind, D, X, STAGED, PART, GATHER>(g, blockIdx.x, total, m, lrow, tid, w, l);
     } else {
         for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
             if (t != blockIdx.x) __syncthreads();  // the tile before has been stored
-            rows_sum_tile<Kind, D, WN, STAGED, PART, GATHER>(g, t, total, m, lrow, tid, w, l);
+            rows_sum_tile<Kind, D, X, STAGED, PART, GATHER>(g, t, total, m, lrow, tid, w, l);
         }
     }
 }
@@ -192,7 +193,7 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     if constexpr (TB) {
         if (g.splits > 1) {
             const int rc = any ? launch(gemm_staged<Kind, F32, false, true, true>, 128, 128, 256)
-                               : launch(gemm_big<Kind, F32, 2, 2, false, false, true, true>, 128, 128, 256);
+                               : launch(gemm_big<Kind, F32, Tile128, 2, false, false, true, true>, 128, 128, 256);
             if (rc) return rc;
             hipLaunchKernelGGL((add_row_parts_kernel<D>), dim3((unsigned)std::min<int64_t>(g.S, 1 << 20)), dim3(256), 0, s, g);
             return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
@@ -200,11 +201,11 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     }
     if (any) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
-        return launch(gemm_big<Kind, D, 2, 4, false, GATED, TB>, 128, 128, 256);
+        return launch(gemm_big<Kind, D, Tile128, 4, false, GATED, TB>, 128, 128, 256);
     const int64_t cols = GATED ? 2 * g.N : g.N, wide = (cols + 255) / 256 * 256, narrow = (cols + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
-        return launch(gemm_big<Kind, D, 2, 2, false, GATED, TB>, 128, 128, 256);
-    return launch(gemm_big<Kind, D, 4, 2, false, GATED, TB>, 256, 256, 512);
+        return launch(gemm_big<Kind, D, Tile128, 2, false, GATED, TB>, 128, 128, 256);
+    return launch(gemm_big<Kind, D, Tile256, 2, false, GATED, TB>, 256, 256, Tile256::kThreads);
 }
 
 // Parts that the sums of dA = dC B are cut into: as many as give 512 workgroups, of 128 rows of B at least each.
@@ -236,9 +237,9 @@ int rows_sum_t(GradArgs g, hipStream_t s) {
     const int64_t mid = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.E * g.splits;
     const auto go = [&](auto part, auto gather) {
         constexpr bool P = decltype(part)::value, G = decltype(gather)::value;
-        return any || mid > kMostTiles ? launch(gemm_rows_sum<Kind, D, 2, true, P, G>, 128, 256)
-               : mid < 512             ? launch(gemm_rows_sum<Kind, D, 2, false, P, G>, 128, 256)
-                                       : launch(gemm_rows_sum<Kind, D, 4, false, P, G>, 256, 512);
+        return any || mid > kMostTiles ? launch(gemm_rows_sum<Kind, D, Tile128, true, P, G>, 128, 256)
+               : mid < 512             ? launch(gemm_rows_sum<Kind, D, Tile128, false, P, G>, 128, 256)
+                                       : launch(gemm_rows_sum<Kind, D, Tile256, false, P, G>, 256, Tile256::kThreads);
     };
     const std::true_type yes{};
     const std::false_type no{};

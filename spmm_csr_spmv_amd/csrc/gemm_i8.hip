@@ -89,18 +89,18 @@ int gemm_t(GemmArgs g, hipStream_t s) {
     // 14336 (256 rows) 222, 228, 187; 512 x 2 (128 rows) 151, 163, 170, but even
     // 165, 163, 138; shorter sums 512 x 8, 128, 2048, 1536 (32 rows) 90, 93, 94;
     // 2048 x 8 (128 rows) 144, 144, 130.
-    if (once) return launch(gemm_big<KindI8, D, 2, 4, true, GATED, false>, 128, 128, 256);
+    if (once) return launch(gemm_big<KindI8, D, Tile128, 4, true, GATED, false>, 128, 128, 256);
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
-        return launch(gemm_big<KindI8, D, 2, 4, false, GATED, false>, 128, 128, 256);
+        return launch(gemm_big<KindI8, D, Tile128, 4, false, GATED, false>, 128, 128, 256);
     // Up to two 128 x 128 tiles a CU: 2048 x 4096 x 4096 43, with four steps 47,
     // with 256 x 256 tiles 57.  Also where 256-wide tiles would be empty for a
     // fifth: 20000 x 2, 16, 512, 300 25, with 256 x 256 33.
     const int64_t cols = GATED ? 2 * g.N : g.N, wide = (cols + 255) / 256 * 256, narrow = (cols + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
-        return launch(gemm_big<KindI8, D, 2, 2, false, GATED, false>, 128, 128, 256);
+        return launch(gemm_big<KindI8, D, Tile128, 2, false, GATED, false>, 128, 128, 256);
     // 8192 x 8192 x 4096 250 against 313 with 128 x 128 tiles; 4096 x 4096 x 4096
     // 68, 82; 4096 x 8, 64, 4096, 2048 (512 rows) 341, even 335 against 415.
-    return launch(gemm_big<KindI8, D, 4, 2, false, GATED, false>, 256, 256, 512);
+    return launch(gemm_big<KindI8, D, Tile256, 2, false, GATED, false>, 256, 256, 512);
 }
 
 }  // namespace

@@ -247,7 +247,7 @@ __device__ __forceinline__ int64_t b_row(const GemmArgs& g, int64_t n0, int i) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: tiles of up to 64 WN rows x 64 WN columns by 2 WN waves, WN = 4
+// Many rows: tiles of up to 64 CB rows x 64 CB columns by W waves, CB = 4
 // (256 x 256, one workgroup a CU) or 2 (128 x 128, two).
 //
 // K advances in steps of 128 bytes, double-buffered in LDS: while the matrix
@@ -259,20 +259,20 @@ __device__ __forceinline__ int64_t b_row(const GemmArgs& g, int64_t n0, int i) {
 // cycles were conflicts).
 //
 // Operands whose rows are steps of the sum (gradients; 16 bits only) are
-// transposed on their way to the matrix cores: LDS holds 64 rows of 64 WN columns,
+// transposed on their way to the matrix cores: LDS holds 64 rows of 64 CB columns,
 // and ds_read_b64_tr_b16 gives a lane four rows of one column.  Their blocks of 32
 // columns (64 bytes) lie at block ^ (row % 4), so that the four rows that half a
 // wave reads at once lie in different banks.
 //
-// Wave (wm, wn) owns columns 64 wn .. 64 wn + 63 and every second 32-row
-// block: rows 32 (2 i + wm), i < F.  F = 1 .. WN is the tile's height in units
+// Wave (wm, wn) owns columns 32 U wn .. 32 U (wn + 1) - 1 and every second 32-row
+// block: rows 32 (2 i + wm), i < F.  F = 1 .. CB is the tile's height in units
 // of 64 rows: a short tile (an expert's last) runs fewer MFMAs and loads fewer
 // rows, instead of multiplying rows nobody stores.  An expert's rows are cut
 // into tiles of equal height rather than full ones and a rest.
 //
 // B is the first MFMA operand, so that a lane's four consecutive sums lie in
 // one row of C; the sums go through LDS once more to be stored as whole lines.
-// In a gated product a wave's 64 columns are 32 of the gate and the same 32 of the
+// In a gated product 64 of a wave's columns are 32 of the gate and the same 32 of the
 // other projection: both meet in its own part of LDS.
 constexpr int kBigK = 128;            // bytes of K a step
 constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
@@ -286,29 +286,40 @@ __device__ __forceinline__ int big_swizzle(int row) { return (row >> 1) & 7; }
 // What global_load_lds reads for rows that are not there.
 static __device__ __attribute__((aligned(16))) int8_t big_zeros[16];
 
-// Copy instructions a wave issues for a step: 2048 WN bytes each over the workgroup.
-template <int WN, int F>
+// A tile's shape: 64 CB columns, W waves, U 32-column blocks a wave.
+template <int CB_, int W_>
+struct Tile {
+    static constexpr int CB = CB_, W = W_, U = 4 * CB / W, kSize = 64 * CB, kThreads = 64 * W;
+    static constexpr int kCopied = kSize / (8 * W);  // copies of a wave for as many rows as the tile has columns
+};
+typedef Tile<2, 4> Tile128;
+typedef Tile<4, 8> Tile256;
+
+// Copy instructions a wave issues for a step: 1024 W bytes each over the workgroup.
+template <class X, int F>
 struct BigShape {
-    static constexpr int kRows = 16 * WN;            // rows of K-contiguous operands that one instruction of every wave covers
+    static constexpr int kRows = 8 * X::W;           // rows of K-contiguous operands that one instruction of every wave covers
     static constexpr int kA = 64 * F / kRows;        // for the rows of A
-    static constexpr int kB = 64 * WN / kRows;       // for the rows of B
+    static constexpr int kB = X::kSize / kRows;      // for the rows of B
     static constexpr int kCopies = kA + kB;
 };
 
 // Where a lane's copy j of a step reads a K-contiguous operand.
+template <class X>
 struct BigDirect {
-    const int8_t* p[4];
+    const int8_t* p[X::kCopied];
     int64_t chunk, last, K;  // chunks behind the last are read from there and masked
+    __device__ __forceinline__ void fetch(int) {}
     __device__ __forceinline__ const int8_t* at(int j, int step) const {
-        return p[j & 3] + min((int64_t)step * kBigK + chunk, last);
+        return p[j % X::kCopied] + min((int64_t)step * kBigK + chunk, last);
     }
     // Rows of any alignment and length, zeros behind K.  The last piece of a row that K cuts begins with bytes that
     // the piece before holds: zeroed, or with ALONE, where the other operand does not begin with the same, moved to where they belong.
     template <bool ALONE>
     __device__ __forceinline__ i32x4 load(int j, int step, bool mask) const {
         const int64_t k = (int64_t)step * kBigK + chunk;
-        if (K < 16) return load_short(p[j & 3], k, K);
-        i32x4 v = load_any(p[j & 3], k, K);
+        if (K < 16) return load_short(p[j % X::kCopied], k, K);
+        i32x4 v = load_any(p[j % X::kCopied], k, K);
         if (mask) {
             if (ALONE) return shift_down(v, (int)min(max(k - (K - 16), (int64_t)0), (int64_t)16));
 #pragma unroll
@@ -335,10 +346,11 @@ struct FastDiv {
 };
 
 // Where a lane's copy j of a step reads an operand whose rows are steps of the sum.  GATHER: row i of the sum is the
-// row of slot src[i]; the sources are read with scalar loads, which do not queue behind the copies in flight.
-template <int WN, bool GATHER>
+// row of slot src[i]; the sources of a step are read ahead of its copies (fetch), with scalar loads, which do not queue
+// behind the copies in flight.
+template <class X, bool GATHER>
 struct BigTransposed {
-    static constexpr int kWave = 8 / WN;  // rows of one copy of a wave
+    static constexpr int kWave = 8 / X::CB, kAll = X::W * kWave;  // rows of one copy of a wave, of all waves
     const int8_t* base;          // the lane's chunk in its row of copy 0 (GATHER: in row 0)
     int64_t ld;
     int rows, row0;              // rows of the sum; the lane's row of copy 0
@@ -348,34 +360,46 @@ struct BigTransposed {
     const int32_t* src;          // the rows' slots
     FastDiv slots;
     int64_t a_rows;              // rows that there are
+    int32_t f[GATHER ? X::kCopied : 1][kWave];  // sources of the step fetched last
     // first: row 0; width: the rows' elements; n0: the tile's first column; STAGED: for load(), else for at()
     template <bool STAGED>
     __device__ __forceinline__ void place(const int8_t* first, int64_t ld_, int rows_, int64_t n0, int64_t width, int w_,
                                           int l) {
-        constexpr int kChunks = 8 * WN;
+        constexpr int kChunks = 8 * X::CB;
         w = w_;
         row0 = w * kWave + l / kChunks;
         const int chunk = (l % kChunks) ^ (4 * (row0 & 3));
         cols = (int)max(min(width - n0 - chunk * 8, (int64_t)8), (int64_t)0);
-        inside = n0 + 64 * WN <= width;
+        inside = n0 + X::kSize <= width;
         narrow = width < 8;
         const int64_t at = 2 * n0 + 16 * chunk;
         base = first + (STAGED ? at : min(at, (2 * width - 1) & ~(int64_t)15)) + (GATHER ? 0 : row0 * ld_);
         ld = ld_;
         rows = rows_;
     }
+    __device__ __forceinline__ void fetch(int step) {
+        if constexpr (GATHER) {
+            const __attribute__((address_space(4))) int32_t* s = (const __attribute__((address_space(4))) int32_t*)src;
+#pragma unroll
+            for (int j = 0; j < X::kCopied; ++j)
+#pragma unroll
+                for (int i = 0; i < kWave; ++i) {
+                    const int at = step * 64 + kAll * j + w * kWave + i;
+                    f[j][i] = rows > 0 ? s[min(at, rows - 1)] : -1;
+                }
+        }
+    }
     // The lane's chunk of its row of copy j; NULL where there is no such row.
     __device__ __forceinline__ const int8_t* row(int j, int step) const {
-        const int u = step * 64 + 16 * j;
+        const int u = step * 64 + kAll * j;
         if constexpr (!GATHER) {
             return u + row0 < rows ? base + (int64_t)u * ld : nullptr;
         } else {
-            const __attribute__((address_space(4))) int32_t* s = (const __attribute__((address_space(4))) int32_t*)src;
             int64_t off = -1;
 #pragma unroll
             for (int i = 0; i < kWave; ++i) {
-                const int at = u + w * kWave + i, f = at < rows ? s[at] : -1, t = slots(max(f, 0));
-                const int64_t o = f >= 0 && t < a_rows ? t * ld : -1;
+                const int at = u + w * kWave + i, t = slots(max(f[j][i], 0));
+                const int64_t o = at < rows && f[j][i] >= 0 && t < a_rows ? t * ld : -1;
                 off = row0 == w * kWave + i ? o : off;
             }
             return off >= 0 ? base + off : nullptr;
@@ -403,9 +427,9 @@ struct BigTransposed {
 };
 
 // Copies [FROM, TO) of the step's, in the order A, B.  ONCE: no other tile reads these rows of B.
-template <int WN, int F, bool ONCE, int FROM, int TO, class SA, class SB>
+template <class X, int F, bool ONCE, int FROM, int TO, class SA, class SB>
 __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const SA& sa, const SB& sb, int step, int w) {
-    using S = BigShape<WN, F>;
+    using S = BigShape<X, F>;
 #pragma unroll
     for (int j = FROM; j < TO; ++j) {
         const int8_t* src = j < S::kA ? sa.at(j, step) : sb.at(j - S::kA, step);
@@ -418,47 +442,47 @@ __device__ __forceinline__ void big_copy(int8_t* la, int8_t* lb, const SA& sa, c
 }
 
 // An MFMA operand of 32 rows (block) and 32 bytes of K: piece ks of a step.
-template <int WN, bool T>
+template <class X, bool T>
 __device__ __forceinline__ i32x4 big_operand(const int8_t* lds, int block, int ks, int l) {
     if constexpr (!T) {
         const int r = l & 31;
         return *reinterpret_cast<const i32x4*>(lds + (32 * block + r) * kBigK + (((2 * ks + (l >> 5)) ^ big_swizzle(r)) << 4));
     } else {
         // lanes 16 q + 4 i + c name row i, columns 4 c .. 4 c + 3 of their 16; lane 16 q + i gets column i of the four rows
-        const int8_t* p = lds + (16 * ks + 8 * (l >> 5) + ((l >> 2) & 3)) * (128 * WN) + ((block ^ ((l >> 2) & 3)) << 6) +
+        const int8_t* p = lds + (16 * ks + 8 * (l >> 5) + ((l >> 2) & 3)) * (2 * X::kSize) + ((block ^ ((l >> 2) & 3)) << 6) +
                           32 * ((l >> 4) & 1) + 8 * (l & 3);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 128 * WN));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * X::kSize));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         return __builtin_bit_cast(i32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 }
 
 // MFMA operands of 32 bytes of K.  TA, TB: rows of A, of B are steps of the sum.
-template <class Kind, int WN, int F, bool TA, bool TB>
+template <class Kind, class X, int F, bool TA, bool TB>
 struct BigOps {
     typedef typename Kind::S16 S16;
-    i32x4 a[F], b[2];
+    i32x4 a[F], b[X::U];
     __device__ __forceinline__ void read(const int8_t* la, const int8_t* lb, int ks, int wm, int wn, int l) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) b[u] = big_operand<WN, TB>(lb, 2 * wn + u, ks, l);
+        for (int u = 0; u < X::U; ++u) b[u] = big_operand<X, TB>(lb, X::U * wn + u, ks, l);
 #pragma unroll
-        for (int i = 0; i < F; ++i) a[i] = big_operand<WN, TA>(la, 2 * i + wm, ks, l);
+        for (int i = 0; i < F; ++i) a[i] = big_operand<X, TA>(la, 2 * i + wm, ks, l);
     }
-    __device__ __forceinline__ void multiply(S16 (&acc)[F][2], int i0 = 0, int i1 = F) const {
+    __device__ __forceinline__ void multiply(S16 (&acc)[F][X::U], int i0 = 0, int i1 = F) const {
 #pragma unroll
         for (int i = 0; i < F; ++i)
             if (i >= i0 && i < i1)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) acc[i][u] = Kind::mfma32(b[u], a[i], acc[i][u]);
+                for (int u = 0; u < X::U; ++u) acc[i][u] = Kind::mfma32(b[u], a[i], acc[i][u]);
     }
     // The same with copies [FROM, TO) of a later step spread between the MFMAs:
     // a wave that issues them in one go waits for the memory pipeline to take them.
     template <bool ONCE, int FROM, int TO, int I = 0, class SA, class SB>
-    __device__ __forceinline__ void multiply_and_copy(S16 (&acc)[F][2], int8_t* la, int8_t* lb, const SA& sa, const SB& sb,
+    __device__ __forceinline__ void multiply_and_copy(S16 (&acc)[F][X::U], int8_t* la, int8_t* lb, const SA& sa, const SB& sb,
                                                       int step, int w) const {
         constexpr int N = TO - FROM;
-        big_copy<WN, F, ONCE, FROM + (N * I + F - 1) / F, FROM + (N * (I + 1) + F - 1) / F>(la, lb, sa, sb, step, w);
+        big_copy<X, F, ONCE, FROM + (N * I + F - 1) / F, FROM + (N * (I + 1) + F - 1) / F>(la, lb, sa, sb, step, w);
         multiply(acc, I, I + 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (I + 1 < F) multiply_and_copy<ONCE, FROM, TO, I + 1>(acc, la, lb, sa, sb, step, w);
@@ -504,12 +528,12 @@ __device__ __forceinline__ void big_barrier() {
     asm volatile("s_barrier" ::: "memory");
 }
 
-template <class S16, int F>
-__device__ __forceinline__ void big_clear(S16 (&acc)[F][2]) {
+template <class S16, int F, int U>
+__device__ __forceinline__ void big_clear(S16 (&acc)[F][U]) {
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][u][r] = 0;
 }
@@ -525,21 +549,25 @@ __device__ __forceinline__ void big_clear(S16 (&acc)[F][2]) {
 // piece's.  Before the barrier a wave waits for its own copies of step s + 1;
 // those of ST - 2 later steps stay in flight.  Copies behind the last step
 // read its last chunk again (or zeros), which keeps the counts the same.
-template <class Kind, int WN, int ST, int F, bool TA, bool TB, bool ONCE, class SA, class SB>
-__device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][2], const BigBuffers<ST>& m, const SA& sa, const SB& sb,
+template <class Kind, class X, int ST, int F, bool TA, bool TB, bool ONCE, class SA, class SB>
+__device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][X::U], const BigBuffers<ST>& m, const SA& sa, SB& sb,
                                          int steps, int left, int tid, int w, int l) {
-    using S = BigShape<WN, F>;
+    using S = BigShape<X, F>;
     const int wm = w & 1, wn = w >> 1;
     big_clear(acc);
     const auto mask = [&](int8_t* la, int8_t* lb) {
-        if (!TA) big_mask(la, 64 * F, left, tid, 128 * WN);
-        if (Kind::kFloat && !TB) big_mask(lb, 64 * WN, left, tid, 128 * WN);
+        if (!TA) big_mask(la, 64 * F, left, tid, X::kThreads);
+        if (Kind::kFloat && !TB) big_mask(lb, X::kSize, left, tid, X::kThreads);
     };
-    BigOps<Kind, WN, F, TA, TB> x0, x1;
+    BigOps<Kind, X, F, TA, TB> x0, x1;
     constexpr int kCopies = S::kCopies, kHalf = kCopies / 2;
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) big_copy<WN, F, ONCE, 0, kCopies>(m.a[i], m.b[i], sa, sb, i, w);
-    big_copy<WN, F, ONCE, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], sa, sb, ST - 1, w);
+    for (int i = 0; i < ST - 1; ++i) {
+        sb.fetch(i);
+        big_copy<X, F, ONCE, 0, kCopies>(m.a[i], m.b[i], sa, sb, i, w);
+    }
+    sb.fetch(ST - 1);
+    big_copy<X, F, ONCE, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], sa, sb, ST - 1, w);
     big_barrier<(ST - 2) * kCopies + kHalf>();
     if (steps == 1 && left < kBigK) {
         mask(m.a[0], m.b[0]);
@@ -553,6 +581,7 @@ __device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][2], const 
         x1.read(m.a[I], m.b[I], 1, wm, wn, l);                                                            \
         __builtin_amdgcn_sched_barrier(0);                                                                \
         x0.template multiply_and_copy<ONCE, kHalf, kCopies>(acc, m.a[kBack], m.b[kBack], sa, sb, (s) + ST - 1, w); \
+        sb.fetch((s) + ST);  /* B's copies of a step are in its second half */                            \
         big_operands_here();                                                                              \
         x0.read(m.a[I], m.b[I], 2, wm, wn, l);                                                            \
         __builtin_amdgcn_sched_barrier(0);                                                                \
@@ -597,12 +626,13 @@ __device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][2], const 
 // (global_load_lds wants aligned pieces): the next step's loads are in flight while this one is
 // multiplied, and go to the other LDS buffer after it.
 template <class Kind, int F, bool TA, bool TB, class SA, class SB>
-__device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, const SB& sb,
+__device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, SB& sb,
                                             int steps, int w, int l) {
-    using S = BigShape<2, F>;
+    using S = BigShape<Tile128, F>;
     const int wm = w & 1, wn = w >> 1;
     i32x4 v[S::kCopies];
     const auto load = [&](int s) {
+        sb.fetch(s);
 #pragma unroll
         for (int j = 0; j < S::kCopies; ++j)
             v[j] = j < S::kA ? sa.template load<TB>(j, s, s == steps - 1)
@@ -625,7 +655,7 @@ __device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], con
         const int8_t* la = s & 1 ? m.a[1] : m.a[0];
         const int8_t* lb = s & 1 ? m.b[1] : m.b[0];
         if (s + 1 < steps) load(s + 1);
-        BigOps<Kind, 2, F, TA, TB> x0, x1;
+        BigOps<Kind, Tile128, F, TA, TB> x0, x1;
         x0.read(la, lb, 0, wm, wn, l);
 #pragma unroll
         for (int ks = 0; ks < 4; ks += 2) {
@@ -642,17 +672,17 @@ __device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], con
 // Where the copies of K-contiguous operands read: rows kRows j + 8 w + l / 8 of the tile, chunk
 // (l % 8) ^ big_swizzle(row); the tile's rows of A (and scales) go to LDS, and behind
 // the rows a word of each wave that says whether it met a far scale.
-template <class Kind, int WN, int F>
+template <class Kind, class X, int F>
 __device__ __forceinline__ void big_rows(const GemmArgs& g, int64_t lo, int64_t hi, int32_t* lrow, float* lscale,
-                                         BigDirect& a, int w, int l) {
-    using S = BigShape<WN, F>;
+                                         BigDirect<X>& a, int w, int l) {
+    using S = BigShape<X, F>;
     const int crow = 8 * w + (l >> 3);
     a.chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
     a.last = (g.K - 1) & ~(int64_t)15;
     a.K = g.K;
     bool far = false;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < X::kCopied; ++j) {
         const int row = S::kRows * j + crow;
         const int64_t p = lo + row;
         const int64_t r = j < S::kA && p < hi ? a_row(g, p) : -1;
@@ -666,19 +696,20 @@ __device__ __forceinline__ void big_rows(const GemmArgs& g, int64_t lo, int64_t 
             }
         }
     }
-    if (!Kind::kFloat) lrow[64 * WN + w] = __any(far);
+    if (!Kind::kFloat) lrow[X::kSize + w] = __any(far);
 }
-template <class Kind, int WN, bool GATED>
-__device__ __forceinline__ void big_columns(const GemmArgs& g, int e, int64_t n0, float* lscale, BigDirect& b, int tid,
+template <class Kind, class X, bool GATED>
+__device__ __forceinline__ void big_columns(const GemmArgs& g, int e, int64_t n0, float* lscale, BigDirect<X>& b, int tid,
                                             int w, int l) {
     const int crow = 8 * w + (l >> 3);
     b.chunk = ((l & 7) ^ big_swizzle(crow)) << 4;
     b.last = (g.K - 1) & ~(int64_t)15;
     b.K = g.K;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b.p[j] = g.B + e * g.strideb + b_row<GATED>(g, n0, 16 * WN * j + crow) * g.ldb;
+    for (int j = 0; j < X::kCopied; ++j) b.p[j] = g.B + e * g.strideb + b_row<GATED>(g, n0, 8 * X::W * j + crow) * g.ldb;
     if constexpr (!Kind::kFloat) {
-        if (tid < 64 * WN) lscale[64 * WN + tid] = g.b_scale[e * (GATED ? 2 * g.N : g.N) + b_row<GATED>(g, n0, tid)];
+        for (int i = tid; i < X::kSize; i += X::kThreads)
+            lscale[X::kSize + i] = g.b_scale[e * (GATED ? 2 * g.N : g.N) + b_row<GATED>(g, n0, i)];
     }
 }
 
@@ -694,10 +725,10 @@ __device__ __forceinline__ BigOut big_out_of(const GemmArgs& g, int64_t lo, int6
     return BigOut{g.C, g.ldc, g.N, lo, n0, g.pre, g.ldp, g.act};
 }
 
-// The tile's sums scaled and stored; l0 .. l3 are LDS buffers of 64 WN x kBigK
+// The tile's sums scaled and stored; l0 .. l3 are LDS buffers of X::kSize x kBigK
 // bytes that nothing uses any more.
-template <class Kind, class D, int WN, int F, bool GATED>
-__device__ __forceinline__ void big_out(const BigOut& g, const typename Kind::S16 (&acc)[F][2], int8_t* l0, int8_t* l1,
+template <class Kind, class D, class X, int F, bool GATED>
+__device__ __forceinline__ void big_out(const BigOut& g, const typename Kind::S16 (&acc)[F][X::U], int8_t* l0, int8_t* l1,
                                         int8_t* l2, int8_t* l3, const int32_t* lrow, const float* lscale, int w, int l) {
     typedef typename D::T T;
     typedef typename Kind::S S;
@@ -708,28 +739,30 @@ __device__ __forceinline__ void big_out(const BigOut& g, const typename Kind::S1
     // projection, 16 rows).  D layout of the 32 x 32 MFMA: lane l, register r ->
     // first operand's row 8 (r/4) + 4 (l/32) + r%4 (a column of C), second operand's
     // row l%32 (a row of C).
-    constexpr int kSums = 32 * kBigRow, kPer = 64 * WN * kBigK / (4 * kSums);  // waves to a buffer
-    static_assert(4 * kPer >= 2 * WN, "the waves' sums fit the four buffers");
+    constexpr int kSums = 32 * kBigRow, kPer = X::kSize * kBigK / (4 * kSums);  // waves to a buffer
+    static_assert(4 * kPer >= X::W, "the waves' sums fit the four buffers");
     int8_t* const buffer = w / kPer == 0 ? l0 : w / kPer == 1 ? l1 : w / kPer == 2 ? l2 : l3;
     S* mine = reinterpret_cast<S*>(buffer) + (w % kPer) * kSums;
     constexpr int N = Chunk<T>::N;
     constexpr int kLanes = GATED ? 4 : 8, kRows = 64 / kLanes, kWide = GATED ? 32 : 64;  // lanes a row, rows an instruction
-    const int64_t n = g.n0 + kWide * wn + 8 * (l % kLanes);
+    const int64_t n1 = g.n0 + kWide * (X::U / 2) * wn + 8 * (l % kLanes);
     bool far = false;  // whether any row of the tile has a far scale
-    if constexpr (!Kind::kFloat) far = __any(lrow[64 * WN + (l & (2 * WN - 1))]);
-    const bool inside = g.n0 + kWide * WN <= g.N && !far;  // the whole tile's columns, and ordinary scales
-    float sb[GATED ? 16 : 8];
-    if constexpr (!Kind::kFloat)
+    if constexpr (!Kind::kFloat) far = __any(lrow[X::kSize + (l & (X::W - 1))]);
+    const bool inside = g.n0 + kWide * X::CB <= g.N && !far;  // the whole tile's columns, and ordinary scales
+    // 32 rows and 64 of the wave's columns; `whole` (a compile-time constant) where all is inside
+    const auto block = [&](int i, int y, auto whole) {
+        const int64_t n = n1 + kWide * y;
+        float sb[GATED ? 16 : 8];
+        if constexpr (!Kind::kFloat)
 #pragma unroll
-        for (int i = 0; i < (GATED ? 16 : 8); ++i)
-            sb[i] = lscale[64 * WN + 64 * wn + 8 * (l % kLanes) + (i < 8 ? i : 32 + i - 8)];
-    // one 32-row block; `whole` (a compile-time constant) where all is inside
-    const auto block = [&](int i, auto whole) {
+            for (int x = 0; x < (GATED ? 16 : 8); ++x)
+                sb[x] = lscale[X::kSize + 32 * X::U * wn + 64 * y + 8 * (l % kLanes) + (x < 8 ? x : 32 + x - 8)];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const S4 v = {acc[i][u][4 * q], acc[i][u][4 * q + 1], acc[i][u][4 * q + 2], acc[i][u][4 * q + 3]};
+                const auto& s = acc[i][2 * y + u];
+                const S4 v = {s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]};
                 *reinterpret_cast<S4*>(mine + (l & 31) * kBigRow + 32 * u + 8 * q + 4 * (l >> 5)) = v;
             }
         __builtin_amdgcn_wave_barrier();
@@ -812,10 +845,14 @@ __device__ __forceinline__ void big_out(const BigOut& g, const typename Kind::S1
     };
     if (inside) {
 #pragma unroll
-        for (int i = 0; i < F; ++i) block(i, std::true_type());
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int y = 0; y < X::U / 2; ++y) block(i, y, std::true_type());
     } else {
 #pragma unroll
-        for (int i = 0; i < F; ++i) block(i, std::false_type());
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int y = 0; y < X::U / 2; ++y) block(i, y, std::false_type());
     }
 }
 
@@ -831,24 +868,24 @@ __device__ __forceinline__ GemmArgs part_of(GemmArgs g, int split) {
 }
 
 // One tile of rows by expert.  TB: B's rows are the steps of the sum (g.K / 2 of them, g.N elements each).
-template <class Kind, class D, int WN, int ST, bool ONCE, bool GATED, bool TB, int F>
+template <class Kind, class D, class X, int ST, bool ONCE, bool GATED, bool TB, int F>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
                                          const BigBuffers<ST>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
-    BigDirect sa;
-    big_rows<Kind, WN, F>(g, lo, hi, lrow, lscale, sa, w, l);
-    typename Kind::S16 acc[F][2];
+    BigDirect<X> sa;
+    big_rows<Kind, X, F>(g, lo, hi, lrow, lscale, sa, w, l);
+    typename Kind::S16 acc[F][X::U];
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     const int left = (int)(g.K - (int64_t)(steps - 1) * kBigK);
     if constexpr (TB) {
-        BigTransposed<WN, false> sb;
+        BigTransposed<X, false> sb;
         sb.template place<false>(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
-        big_sums<Kind, WN, ST, F, false, true, ONCE>(acc, m, sa, sb, steps, left, tid, w, l);
+        big_sums<Kind, X, ST, F, false, true, ONCE>(acc, m, sa, sb, steps, left, tid, w, l);
     } else {
-        BigDirect sb;
-        big_columns<Kind, WN, GATED>(g, e, n0, lscale, sb, tid, w, l);
-        big_sums<Kind, WN, ST, F, false, false, ONCE>(acc, m, sa, sb, steps, left, tid, w, l);
+        BigDirect<X> sb;
+        big_columns<Kind, X, GATED>(g, e, n0, lscale, sb, tid, w, l);
+        big_sums<Kind, X, ST, F, false, false, ONCE>(acc, m, sa, sb, steps, left, tid, w, l);
     }
-    big_out<Kind, D, WN, F, GATED>(big_out_of(g, lo, n0), acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, w, l);
+    big_out<Kind, D, X, F, GATED>(big_out_of(g, lo, n0), acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, w, l);
 }
 
 // Tile number t of the m_tiles x n_tiles that there are.  Four row tiles to a
@@ -865,7 +902,7 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int e, int64_t lo, i
 // 515; 32768 of 64, 4096 x 2048 340, 338, 336.  The tallest tiles first gained
 // nothing on that.  RUN = 0, neighbours, where a row tile has few column tiles
 // and all matrices fit the caches: 40000 of 16, 512 x 300 26, 29, 29.
-template <int WN, int RUN, bool GATED>
+template <class X, int RUN, bool GATED>
 __device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t m_tiles, uint32_t t, int lane, int& e,
                                           int64_t& lo, int64_t& hi, int64_t& n0) {
     const uint32_t all = m_tiles * g.n_tiles;
@@ -877,25 +914,25 @@ __device__ __forceinline__ bool big_place(const GemmArgs& g, uint32_t m_tiles, u
         v = t / kRound * kRound + t % kXcds * RUN + t / kXcds % RUN;
     const uint32_t group = 4 * g.n_tiles, first = v / group * 4, in = v % group;
     const uint32_t high = min(m_tiles - first, 4u);
-    n0 = (int64_t)(in / high) * (GATED ? 32 * WN : 64 * WN);
-    return find_tile<64 * WN>(g, first + in % high, lane, e, lo, hi);
+    n0 = (int64_t)(in / high) * (GATED ? X::kSize / 2 : X::kSize);
+    return find_tile<X::kSize>(g, first + in % high, lane, e, lo, hi);
 }
 
-template <class Kind, class D, int WN, int ST, bool ONCE, bool GATED, bool TB, bool PART = false>
-__global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_big(GemmArgs args) {
+template <class Kind, class D, class X, int ST, bool ONCE, bool GATED, bool TB, bool PART = false>
+__global__ __launch_bounds__(X::kThreads, X::W == 8 || X::CB * ST <= 4 ? 2 : 1) void gemm_big(GemmArgs args) {
     const GemmArgs g = PART ? part_of(args, blockIdx.y) : args;
-    constexpr int kBytes = 64 * WN * kBigK;
+    constexpr int kBytes = X::kSize * kBigK;
     __shared__ __attribute__((aligned(1024))) int8_t a0[kBytes], a1[kBytes], b0[kBytes], b1[kBytes];
-    __shared__ int32_t lrow[64 * WN + 2 * WN];  // row of A of every row of the tile, or -1; words of the waves
-    __shared__ float lscale[Kind::kFloat ? 1 : 2 * 64 * WN];   // scales of the tile's rows, then of its columns
+    __shared__ int32_t lrow[X::kSize + X::W];  // row of A of every row of the tile, or -1; words of the waves
+    __shared__ float lscale[Kind::kFloat ? 1 : 2 * X::kSize];   // scales of the tile's rows, then of its columns
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     int e;
     int64_t lo, hi, n0;
-    const uint32_t m_tiles = count_tiles<64 * WN>(g, l);
+    const uint32_t m_tiles = count_tiles<X::kSize>(g, l);
     if (blockIdx.x >= m_tiles * g.n_tiles) return;
-    if (!big_place<WN, ST == 4 ? 1 : WN == 4 ? 8 : 0, GATED>(g, m_tiles, blockIdx.x, l, e, lo, hi, n0)) return;
+    if (!big_place<X, ST == 4 ? 1 : X::CB == 4 ? 8 : 0, GATED>(g, m_tiles, blockIdx.x, l, e, lo, hi, n0)) return;
     const int blocks = (int)((hi - lo + 63) >> 6);
-#define SPX_TILE(F) big_tile<Kind, D, WN, ST, ONCE, GATED, TB, F>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l)
+#define SPX_TILE(F) big_tile<Kind, D, X, ST, ONCE, GATED, TB, F>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l)
     if constexpr (ST == 4) {
         __shared__ __attribute__((aligned(1024))) int8_t a2[kBytes], a3[kBytes], b2[kBytes], b3[kBytes];
         const BigBuffers<4> m = {{a0, a1, a2, a3}, {b0, b1, b2, b3}};
@@ -904,7 +941,7 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_big(GemmA
     } else {
         const BigBuffers<2> m = {{a0, a1}, {b0, b1}};
         if (blocks == 1) return SPX_TILE(1);
-        if constexpr (WN == 4) {
+        if constexpr (X::CB == 4) {
             if (blocks == 3) return SPX_TILE(3);
             if (blocks == 4) return SPX_TILE(4);
         }
@@ -920,20 +957,20 @@ __global__ __launch_bounds__(128 * WN, WN * ST <= 4 ? 2 : 1) void gemm_big(GemmA
 template <class Kind, class D, bool GATED, bool TB, int F>
 __device__ __forceinline__ void staged_tile(const GemmArgs& g, int e, int64_t lo, int64_t hi, int64_t n0,
                                             const BigBuffers<2>& m, int32_t* lrow, float* lscale, int tid, int w, int l) {
-    BigDirect sa;
-    big_rows<Kind, 2, F>(g, lo, hi, lrow, lscale, sa, w, l);
+    BigDirect<Tile128> sa;
+    big_rows<Kind, Tile128, F>(g, lo, hi, lrow, lscale, sa, w, l);
     typename Kind::S16 acc[F][2];
     const int steps = (int)((g.K + kBigK - 1) / kBigK);
     if constexpr (TB) {
-        BigTransposed<2, false> sb;
+        BigTransposed<Tile128, false> sb;
         sb.template place<true>(g.B + e * g.strideb, g.ldb, (int)(g.K / 2), n0, g.N, w, l);
         staged_sums<Kind, F, false, true>(acc, m, sa, sb, steps, w, l);
     } else {
-        BigDirect sb;
-        big_columns<Kind, 2, GATED>(g, e, n0, lscale, sb, tid, w, l);
+        BigDirect<Tile128> sb;
+        big_columns<Kind, Tile128, GATED>(g, e, n0, lscale, sb, tid, w, l);
         staged_sums<Kind, F, false, false>(acc, m, sa, sb, steps, w, l);
     }
-    big_out<Kind, D, 2, F, GATED>(big_out_of(g, lo, n0), acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, w, l);
+    big_out<Kind, D, Tile128, F, GATED>(big_out_of(g, lo, n0), acc, m.b[0], m.b[1], m.a[0], m.a[1], lrow, lscale, w, l);
 }
 
 template <class Kind, class D, bool GATED, bool TB, bool PART = false>
@@ -949,7 +986,7 @@ __global__ __launch_bounds__(256, 2) void gemm_staged(GemmArgs args) {
     for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
         int e;
         int64_t lo, hi, n0;
-        if (!big_place<2, 8, GATED>(g, m_tiles, t, l, e, lo, hi, n0)) continue;
+        if (!big_place<Tile128, 8, GATED>(g, m_tiles, t, l, e, lo, hi, n0)) continue;
         __syncthreads();  // the tile before has been stored
         if (hi - lo <= 64)
             staged_tile<Kind, D, GATED, TB, 1>(g, e, lo, hi, n0, m, lrow, lscale, tid, w, l);
