@@ -51,7 +51,7 @@ __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uin
     sa.template place<STAGED>(g.P + from * g.ldp, g.ldp, rows, m0, g.M, w, l);
     if constexpr (GATHER) {
         sb.template place<STAGED>(g.Q, g.ldq, rows, n0, g.N, w, l);
-        sb.src = g.src + from;
+        sb.src = rows > 0 ? g.src + from : reinterpret_cast<const int32_t*>(big_zeros);
         sb.slots = g.slots;
         sb.a_rows = g.q_rows;
     } else {

@@ -352,12 +352,13 @@ template <class X, bool GATHER>
 struct BigTransposed {
     static constexpr int kWave = 8 / X::CB, kAll = X::W * kWave;  // rows of one copy of a wave, of all waves
     const int8_t* base;          // the lane's chunk in its row of copy 0 (GATHER: in row 0)
+    const int8_t* zeros;         // read for rows that are not there
     int64_t ld;
     int rows, row0;              // rows of the sum; the lane's row of copy 0
     int cols;                    // load: elements from the lane's chunk to the row's end, 8 at most
     bool inside, narrow;         // load: all the tile's chunks are whole; rows shorter than a chunk
     int w;                       // GATHER only, as what follows
-    const int32_t* src;          // the rows' slots
+    const int32_t* src;          // the rows' slots (readable where there are no rows too)
     FastDiv slots;
     int64_t a_rows;              // rows that there are
     int32_t f[GATHER ? X::kCopied : 1][kWave];  // sources of the step fetched last
@@ -374,6 +375,7 @@ struct BigTransposed {
         narrow = width < 8;
         const int64_t at = 2 * n0 + 16 * chunk;
         base = first + (STAGED ? at : min(at, (2 * width - 1) & ~(int64_t)15)) + (GATHER ? 0 : row0 * ld_);
+        zeros = big_zeros;
         ld = ld_;
         rows = rows_;
     }
@@ -385,43 +387,47 @@ struct BigTransposed {
 #pragma unroll
                 for (int i = 0; i < kWave; ++i) {
                     const int at = step * 64 + kAll * j + w * kWave + i;
-                    f[j][i] = rows > 0 ? s[min(at, rows - 1)] : -1;
+                    f[j][i] = s[max(min(at, rows - 1), 0)];
                 }
         }
     }
-    // The lane's chunk of its row of copy j; NULL where there is no such row.
-    __device__ __forceinline__ const int8_t* row(int j, int step) const {
+    // The lane's chunk of its row of copy j, or `none` where there is no such row.  Distances from row to row are the same
+    // for all lanes, and so is whether all rows of a copy are there.
+    __device__ __forceinline__ const int8_t* row(int j, int step, const int8_t* none) const {
         const int u = step * 64 + kAll * j;
         if constexpr (!GATHER) {
-            return u + row0 < rows ? base + (int64_t)u * ld : nullptr;
+            const int8_t* p = base + (int64_t)u * ld;
+            return u + row0 < rows ? p : none;
         } else {
-            int64_t off = -1;
+            int64_t off[kWave];
+            bool there[kWave];
 #pragma unroll
             for (int i = 0; i < kWave; ++i) {
                 const int at = u + w * kWave + i, t = slots(max(f[j][i], 0));
-                const int64_t o = at < rows && f[j][i] >= 0 && t < a_rows ? t * ld : -1;
-                off = row0 == w * kWave + i ? o : off;
+                there[i] = at < rows && f[j][i] >= 0 && t < a_rows;
+                off[i] = t * ld;
             }
-            return off >= 0 ? base + off : nullptr;
+            const int mine = row0 - w * kWave;
+            const int8_t* p = none;
+#pragma unroll
+            for (int i = 0; i < kWave; ++i) p = mine == i ? (there[i] ? base + off[i] : none) : p;
+            return p;
         }
     }
-    __device__ __forceinline__ const int8_t* at(int j, int step) const {
-        const int8_t* p = row(j, step);
-        return p ? p : big_zeros;
-    }
+    __device__ __forceinline__ const int8_t* at(int j, int step) const { return row(j, step, zeros); }
     // Branches that all lanes take alike only: loads behind others would wait for one another.  A chunk that the
     // row's end cuts is loaded with the elements before it and moved down.
     template <bool>
     __device__ __forceinline__ i32x4 load(int j, int step, bool) const {
-        const int8_t* p = row(j, step);
-        if (inside) return *reinterpret_cast<const i32x4_u*>(p ? p : big_zeros);
+        if (inside) return *reinterpret_cast<const i32x4_u*>(row(j, step, zeros));
+        const int8_t* p = row(j, step, nullptr);
         if (narrow) {
             i32x4 v = {0, 0, 0, 0};
             for (int i = 0; i < 7; ++i)
                 if (p && i < cols) v[i >> 1] |= (int32_t)((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1)));
             return v;
         }
-        const int8_t* at = p && cols > 0 ? p + 2 * cols - 16 : big_zeros;
+        const int8_t* at = p && cols > 0 ? p + 2 * cols - 16 : zeros;
         return shift_down(*reinterpret_cast<const i32x4_u*>(at), 16 - 2 * cols);
     }
 };
