@@ -89,45 +89,86 @@ __global__ __launch_bounds__(X::kThreads, X::W == 8 || X::CB == 2 ? 2 : 1) void 
     }
 }
 
-// dB = the parts' sum, in the order of the splits.
+// The parts' sums, in their order, rounded: rows of N, row i going to row i % M of matrix i / M.  With offsets (dA; one
+// matrix) only the rows that some expert has.  A workgroup does 1024 columns of a row.
+struct PartArgs {
+    const float* part;  // [splits][rows][N]
+    int32_t splits;
+    int64_t rows, N, M;
+    void* C;
+    int64_t ldc, stridec;
+    const int32_t* offsets;
+    int32_t E;
+};
 template <class D>
-__global__ __launch_bounds__(256) void add_parts_kernel(GradArgs g) {
-    const int64_t each = g.E * g.M * g.N, rows = g.E * g.M, chunks = (g.N + 3) / 4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / chunks, c = i % chunks * 4;
-        const int n = (int)min((int64_t)4, g.N - c);
-        const float* p = g.part + row * g.N + c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < g.splits; ++s)
+__global__ __launch_bounds__(256) void add_parts_kernel(PartArgs g) {
+    typedef float F4 __attribute__((ext_vector_type(4)));
+    typedef float F4U __attribute__((ext_vector_type(4), aligned(4)));
+    typedef typename D::T T;
+    typedef T V4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    const int64_t n = (int64_t)blockIdx.y * 1024 + 4 * threadIdx.x;
+    for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+        if (g.offsets) {
+            int mine = 0;
+            for (int e = threadIdx.x; e < g.E; e += 256) {
+                int a, b;
+                expert_rows(g.offsets, g.E, g.rows, e, a, b);
+                mine |= a <= row && row < b;
+            }
+            if (!__syncthreads_or(mine)) continue;
+        }
+        T* to = (T*)g.C + row / g.M * g.stridec + row % g.M * g.ldc + n;
+        const float* from = g.part + row * g.N + n;
+        const int64_t next = g.rows * g.N;
+        if (n + 4 <= g.N) {
+            F4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+            int s = 0;
+            for (; s + 4 <= g.splits; s += 4) {
+                F4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] += j < n ? p[s * each + j] : 0.0f;
-        typename D::T* o = (typename D::T*)g.C + row / g.M * g.stridec + row % g.M * g.ldc + c;
+                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const F4U*>(from + (s + i) * next);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < n) o[j] = D::down(sum[j]);
+                for (int i = 0; i < 4; ++i) sum += v[i];
+            }
+            for (; s < g.splits; ++s) sum += *reinterpret_cast<const F4U*>(from + s * next);
+            *reinterpret_cast<V4*>(to) = V4{D::down(sum[0]), D::down(sum[1]), D::down(sum[2]), D::down(sum[3])};
+        } else {
+            for (int i = 0; i < 3 && n + i < g.N; ++i) {
+                float sum = 0.0f;
+                for (int s = 0; s < g.splits; ++s) sum += from[s * next + i];
+                to[i] = D::down(sum);
+            }
+        }
     }
 }
-
-// dA = the parts' sum, in the order of the splits, for the rows that some expert has; a workgroup a row.
 template <class D>
-__global__ __launch_bounds__(256) void add_row_parts_kernel(GemmArgs g) {
-    for (int64_t p = blockIdx.x; p < g.S; p += gridDim.x) {
-        int mine = !g.offsets;
-        for (int e = threadIdx.x; e < g.E && !mine; e += 256) {
-            int a, b;
-            expert_rows(g, e, a, b);
-            mine = a <= p && p < b;
+int add_parts(const PartArgs& g, hipStream_t s) {
+    const int64_t y = (g.N + 1023) / 1024;
+    if (y > 65535) return SP_ERR_SIZE;
+    hipLaunchKernelGGL((add_parts_kernel<D>), dim3((unsigned)std::min<int64_t>(g.rows, 1 << 20), (unsigned)y), dim3(256), 0, s, g);
+    return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
+}
+
+// Into how many parts to cut the sums of `steps` steps of a product's tiles, and whether 256 x 256 tiles are better than
+// 128 x 128 ones: the least of an estimate in us.  128 x 128 tiles take 0.65 a step where there is one on a CU, 1.1 where
+// there are two; 256 x 256 ones 1.8; parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
+struct Cut {
+    bool wide;
+    int splits;
+};
+Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double outputs, bool wide_parts) {
+    Cut best{false, 1};
+    double least = 1e300;
+    for (int w = 0; w < 2; ++w)
+        for (const int n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (n > 1 && (2 * n > steps || (w && !wide_parts))) break;
+            const int64_t each = (steps + n - 1) / n, parts = n == 1 ? 1 : (steps + each - 1) / each;  // none is empty
+            const int64_t tiles = (w ? wide_tiles : narrow_tiles) * parts;
+            const double step = w ? 1.8 * ((tiles + 255) / 256) : tiles <= 256 ? 0.65 : 1.1 * ((tiles + 511) / 512);
+            const double us = step * each + (parts > 1 ? 4.0 + 2e-6 * parts * outputs : 0.0);
+            if (us < least) least = us, best = Cut{w != 0, (int)parts};
         }
-        if (!__syncthreads_or(mine)) continue;
-        const float* from = g.part + p * g.N;
-        typename D::T* to = (typename D::T*)g.C + p * g.ldc;
-        for (int64_t n = threadIdx.x; n < g.N; n += 256) {
-            float sum = from[n];
-#pragma unroll 4
-            for (int s = 1; s < g.splits; ++s) sum += from[s * g.S * g.N + n];
-            to[n] = D::down(sum);
-        }
-    }
+    return best;
 }
 
 // ---------------------------------------------------------------- the gate's gradient
@@ -166,9 +207,9 @@ int launch_thin(bool once, const GemmArgs& g, hipStream_t s) {
                 : gemm_launch(gemm_thin<Kind, D, R, C, W, false, GATED>, g, 16 * R, kWide, 64 * W, s);
 }
 
-template <class Kind, class D, bool GATED, bool TB>
+template <class Kind, class D, bool GATED>
 int gemm16_t(const GemmArgs& g, hipStream_t s) {
-    // bn rows of B (TB: columns) a tile
+    // bn rows of B a tile
     const auto tiles = [&](int64_t bm, int64_t bn) { return spx::tiles(g, bm, GATED ? bn / 2 : bn); };
     const auto launch = [&](auto kernel, int64_t bm, int64_t bn, int threads) {
         return gemm_launch(kernel, g, bm, GATED ? bn / 2 : bn, threads, s);
@@ -176,51 +217,84 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
     const int64_t mid = tiles(128, 128);
     const bool any = !aligned16(g);
-    if ((g.K < 16 && g.splits <= 1) || mid > kMostTiles) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
+    if (g.K < 16 || mid > kMostTiles) return launch(gemm_staged<Kind, D, GATED, false>, 128, 128, 256);
     const bool few = tiles(16, 32) <= kMostTiles;
     const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
     const bool deep = g.K > 2048;
     const bool once = !any && g.S <= 32 * groups;
-    if constexpr (!TB) {
-        if (tiles(16, 32) <= 128) return launch_thin<Kind, D, 1, GATED ? 2 : 1, 8, GATED>(once, g, s);
-        if (tiles(16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
-            return launch_thin<Kind, D, 1, 2, 4, GATED>(once, g, s);
-        if (tiles(32, 32) <= 256 || (experts && g.S <= 16 * groups && deep))
-            return launch_thin<Kind, D, 2, 2, 4, GATED>(once, g, s);
-        if (tiles(32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
-            return launch_thin<Kind, D, 2, 4, 4, GATED>(once, g, s);
-    }
-    if constexpr (TB) {
-        if (g.splits > 1) {
-            const int rc = any ? launch(gemm_staged<Kind, F32, false, true, true>, 128, 128, 256)
-                               : launch(gemm_big<Kind, F32, Tile128, 2, false, false, true, true>, 128, 128, 256);
-            if (rc) return rc;
-            hipLaunchKernelGGL((add_row_parts_kernel<D>), dim3((unsigned)std::min<int64_t>(g.S, 1 << 20)), dim3(256), 0, s, g);
-            return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
-        }
-    }
-    if (any) return launch(gemm_staged<Kind, D, GATED, TB>, 128, 128, 256);
+    if (tiles(16, 32) <= 128) return launch_thin<Kind, D, 1, GATED ? 2 : 1, 8, GATED>(once, g, s);
+    if (tiles(16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
+        return launch_thin<Kind, D, 1, 2, 4, GATED>(once, g, s);
+    if (tiles(32, 32) <= 256 || (experts && g.S <= 16 * groups && deep))
+        return launch_thin<Kind, D, 2, 2, 4, GATED>(once, g, s);
+    if (tiles(32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
+        return launch_thin<Kind, D, 2, 4, 4, GATED>(once, g, s);
+    if (any) return launch(gemm_staged<Kind, D, GATED, false>, 128, 128, 256);
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
-        return launch(gemm_big<Kind, D, Tile128, 4, false, GATED, TB>, 128, 128, 256);
+        return launch(gemm_big<Kind, D, Tile128, 4, false, GATED, false>, 128, 128, 256);
     const int64_t cols = GATED ? 2 * g.N : g.N, wide = (cols + 255) / 256 * 256, narrow = (cols + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
-        return launch(gemm_big<Kind, D, Tile128, 2, false, GATED, TB>, 128, 128, 256);
-    return launch(gemm_big<Kind, D, Tile256, 2, false, GATED, TB>, 256, 256, Tile256::kThreads);
+        return launch(gemm_big<Kind, D, Tile128, 2, false, GATED, false>, 128, 128, 256);
+    return launch(gemm_big<Kind, D, Tile256, 2, false, GATED, false>, 256, 256, Tile256::kThreads);
 }
 
-// Parts that the sums of dA = dC B are cut into: as many as give 512 workgroups, of 128 rows of B at least each.
-int row_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
-    const int64_t tiles = std::max<int64_t>((S / 128 + std::min<int64_t>(E, S)) * ((N + 127) / 128), 1), steps = (M + 63) / 64;
-    const int64_t want = std::min<int64_t>({512 / tiles, steps / 2, 32});
-    if (want < 2) return 1;
-    const int64_t each = (steps + want - 1) / want;
-    return (int)((steps + each - 1) / each);  // none is empty
+// dA = dC B, M rows of B a sum.  Tiles of 16 rows where a matrix has up to 16 rows on the average, of 32 up to 32, whose
+// sums are cut into as many parts as give 512 workgroups; else 128 x 128 or 256 x 256 ones.
+struct RowPlan {
+    int high;    // rows of a thin tile (16 R), or 0
+    bool wide;
+    int splits;
+};
+RowPlan row_plan(int64_t S, int32_t E, int64_t M, int64_t N) {
+    const int64_t groups = std::max<int64_t>(std::min<int64_t>(E, S), 1), rows = S / groups;
+    const int high = rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+    const int64_t steps = (M + 63) / 64;
+    const auto tiles = [&](int64_t bm, int64_t bn) {
+        return std::max<int64_t>((groups > 1 ? S / bm + groups : (S + bm - 1) / bm) * ((N + bn - 1) / bn), 1);
+    };
+    if (high && tiles(high, 64) <= kMostTiles / 2) {
+        const int64_t want = std::min<int64_t>({512 / tiles(high, 64), steps / 4, 32});  // a step for each of four waves
+        const int64_t each = (steps + want - 1) / std::max<int64_t>(want, 1);
+        return RowPlan{high, false, want < 2 ? 1 : (int)((steps + each - 1) / each)};  // none is empty
+    }
+    // an expert's last tile is half as high as the others on the average, and takes half their time
+    const auto even = [&](int64_t b) { return tiles(b, b) - (groups > 1 ? groups / 2 * ((N + b - 1) / b) : 0); };
+    const Cut c = best_cut(even(128), even(256), steps, (double)S * N, false);
+    return RowPlan{0, c.wide, c.splits};
 }
 
-// Parts that an expert's rows are cut into for dB: as many as give 512 workgroups, of 256 rows at least each on the average.
-int grad_splits(int64_t S, int32_t E, int64_t M, int64_t N) {
-    const int64_t tiles = std::max<int64_t>((M + 127) / 128 * ((N + 127) / 128) * E, 1);
-    return (int)std::max<int64_t>(std::min<int64_t>({512 / tiles, S / E / 256, 64}), 1);
+template <class Kind, class D>
+int row_gradient_t(const GemmArgs& g, const RowPlan& plan, hipStream_t s) {
+    const auto launch = [&](auto kernel, int64_t bm, int64_t bn, int threads) { return gemm_launch(kernel, g, bm, bn, threads, s); };
+    const int64_t groups = g.offsets ? std::min<int64_t>(g.E, g.S) : 1;
+    const bool any = !aligned16(g), once = !any && g.S <= 32 * groups;
+    const int64_t mid = tiles(g, 128, 128);
+    const auto thin = [&](auto part) {
+        constexpr bool P = decltype(part)::value;
+        typedef std::conditional_t<P, F32, D> O;
+        return plan.high == 16 ? (once ? launch(gemm_thin_rows<Kind, O, 1, true, P>, 16, 64, 256)
+                                  : launch(gemm_thin_rows<Kind, O, 1, false, P>, 16, 64, 256))
+                          : (once ? launch(gemm_thin_rows<Kind, O, 2, true, P>, 32, 64, 256)
+                                  : launch(gemm_thin_rows<Kind, O, 2, false, P>, 32, 64, 256));
+    };
+    if (g.splits > 1) {
+        const int rc = plan.high ? thin(std::true_type())
+                       : any ? launch(gemm_staged<Kind, F32, false, true, true>, 128, 128, 256)
+                             : launch(gemm_big<Kind, F32, Tile128, 2, false, false, true, true>, 128, 128, 256);
+        if (rc) return rc;
+        return add_parts<D>(PartArgs{g.part, g.splits, g.S, g.N, g.S, g.C, g.ldc, 0, g.offsets, g.E}, s);
+    }
+    if (plan.high) return thin(std::false_type());
+    if (any || g.K < 16 || mid > kMostTiles) return launch(gemm_staged<Kind, D, false, true>, 128, 128, 256);
+    if (plan.wide) return launch(gemm_big<Kind, D, Tile256, 2, false, false, true>, 256, 256, Tile256::kThreads);
+    if (mid <= 256 || g.S <= 128 * groups) return launch(gemm_big<Kind, D, Tile128, 4, false, false, true>, 128, 128, 256);
+    return launch(gemm_big<Kind, D, Tile128, 2, false, false, true>, 128, 128, 256);
+}
+
+// dB: the parts of an expert's rows, of 64 rows a step on the average.
+Cut grad_cut(int64_t S, int32_t E, int64_t M, int64_t N) {
+    const auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b) * E; };
+    return best_cut(tiles(128), tiles(256), (S / E + 63) / 64, (double)E * M * N, true);
 }
 
 template <class Kind, class D>
@@ -235,23 +309,18 @@ int rows_sum_t(GradArgs g, hipStream_t s) {
         return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
     };
     const int64_t mid = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.E * g.splits;
+    const bool wide = grad_cut(g.S, g.E, g.M, g.N).wide;
     const auto go = [&](auto part, auto gather) {
         constexpr bool P = decltype(part)::value, G = decltype(gather)::value;
         return any || mid > kMostTiles ? launch(gemm_rows_sum<Kind, D, Tile128, true, P, G>, 128, 256)
-               : mid < 512             ? launch(gemm_rows_sum<Kind, D, Tile128, false, P, G>, 128, 256)
-                                       : launch(gemm_rows_sum<Kind, D, Tile256, false, P, G>, 256, Tile256::kThreads);
+               : wide                  ? launch(gemm_rows_sum<Kind, D, Tile256, false, P, G>, 256, Tile256::kThreads)
+                                       : launch(gemm_rows_sum<Kind, D, Tile128, false, P, G>, 128, 256);
     };
     const std::true_type yes{};
     const std::false_type no{};
     const int rc = g.splits > 1 ? (g.src ? go(yes, yes) : go(yes, no)) : (g.src ? go(no, yes) : go(no, no));
-    if (rc) return rc;
-    if (g.splits > 1) {
-        const int64_t chunks = g.E * g.M * ((g.N + 3) / 4);
-        hipLaunchKernelGGL((add_parts_kernel<D>), dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 20)), dim3(256), 0,
-                           s, g);
-        if (hipGetLastError() != hipSuccess) return SP_ERR_HIP;
-    }
-    return SP_OK;
+    if (rc || g.splits <= 1) return rc;
+    return add_parts<D>(PartArgs{g.part, g.splits, g.E * g.M, g.N, g.M, g.C, g.ldc, g.stridec, nullptr, 0}, s);
 }
 
 // go(kind, type)
@@ -264,7 +333,7 @@ int64_t pre_stride(int64_t N) { return (2 * N + 63) / 64 * 64; }  // rows on 128
 
 // Workspace of product_backward, whose two products use it one after the other.
 size_t parts_bytes(const Products& p, int64_t M) {
-    const int rows = row_splits(p.S, p.E, M, p.K), sums = grad_splits(p.S, p.E, M, p.K);
+    const int rows = row_plan(p.S, p.E, M, p.K).splits, sums = grad_cut(p.S, p.E, M, p.K).splits;
     const size_t a = rows > 1 ? (size_t)rows * p.S * p.K : 0, b = sums > 1 ? (size_t)sums * p.E * M * p.K : 0;
     return std::max(a, b) * sizeof(float);
 }
@@ -275,14 +344,15 @@ int product_backward(const Products& p, int64_t M, const void* dC, int64_t ldc, 
     if (dA && p.S > 0 && p.K > 0) {
         GemmArgs g{p.S, p.K, 2 * M, (const int8_t*)dC, p.S, 2 * ldc, nullptr, nullptr, 1, (const int8_t*)p.B, 2 * p.ldb,
                    2 * p.strideb, nullptr, p.offsets, p.E, dA, ldda};
+        const RowPlan plan = row_plan(p.S, p.E, M, p.K);
         g.part = part;
-        g.splits = row_splits(p.S, p.E, M, p.K);
-        const int rc = by_type(p.dtype, [&](auto k, auto d) { return gemm16_t<decltype(k), decltype(d), false, true>(g, s); });
+        g.splits = plan.splits;
+        const int rc = by_type(p.dtype, [&](auto k, auto d) { return row_gradient_t<decltype(k), decltype(d)>(g, plan, s); });
         if (rc) return rc;
     }
     if (dB && M > 0 && p.K > 0) {
         GradArgs g{p.S, M, p.K, (const int8_t*)dC, 2 * ldc, (const int8_t*)p.A, p.a_rows, 2 * p.lda, p.src,
-                   FastDiv::by(p.slots), p.offsets, p.E, dB, lddb, stridedb, part, grad_splits(p.S, p.E, M, p.K)};
+                   FastDiv::by(p.slots), p.offsets, p.E, dB, lddb, stridedb, part, grad_cut(p.S, p.E, M, p.K).splits};
         return by_type(p.dtype, [&](auto k, auto d) { return rows_sum_t<decltype(k), decltype(d)>(g, s); });
     }
     return SP_OK;
@@ -295,8 +365,8 @@ int moe_gemm_device(const Products& p, int32_t gate, void* pre, int64_t ldp, voi
     GemmArgs g{p.S, p.N, 2 * p.K, (const int8_t*)p.A, p.a_rows, 2 * p.lda, nullptr, p.src, p.slots, (const int8_t*)p.B,
                2 * p.ldb, 2 * p.strideb, nullptr, p.offsets, p.E, C, ldc, pre, ldp, gate};
     return by_type(p.dtype, [&](auto k, auto d) {
-        return gate < 0 ? gemm16_t<decltype(k), decltype(d), false, false>(g, s)
-                        : gemm16_t<decltype(k), decltype(d), true, false>(g, s);
+        return gate < 0 ? gemm16_t<decltype(k), decltype(d), false>(g, s)
+                        : gemm16_t<decltype(k), decltype(d), true>(g, s);
     });
 }
 

@@ -280,6 +280,7 @@ constexpr int kBigRow = 64 + 4;       // LDS words per row of a wave's sums
 typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) const int8_t lds_int8;
 
 __device__ __forceinline__ int big_swizzle(int row) { return (row >> 1) & 7; }
 
@@ -455,10 +456,14 @@ __device__ __forceinline__ i32x4 big_operand(const int8_t* lds, int block, int k
         return *reinterpret_cast<const i32x4*>(lds + (32 * block + r) * kBigK + (((2 * ks + (l >> 5)) ^ big_swizzle(r)) << 4));
     } else {
         // lanes 16 q + 4 i + c name row i, columns 4 c .. 4 c + 3 of their 16; lane 16 q + i gets column i of the four rows
-        const int8_t* p = lds + (16 * ks + 8 * (l >> 5) + ((l >> 2) & 3)) * (2 * X::kSize) + ((block ^ ((l >> 2) & 3)) << 6) +
-                          32 * ((l >> 4) & 1) + 8 * (l & 3);
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * X::kSize));
+        int at = (8 * (l >> 5) + ((l >> 2) & 3)) * (2 * X::kSize) + ((block ^ ((l >> 2) & 3)) << 6) + 32 * ((l >> 4) & 1) +
+                 8 * (l & 3);
+        // One number for the compiler: an address few steps from the buffer's tells it which buffer is read.  Built from the
+        // terms above it loses track, and makes the read wait for the copies into all buffers.
+        asm("" : "+v"(at));
+        lds_int8* const from = (lds_int8*)lds + at;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 16 * ks * (2 * X::kSize)));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + (16 * ks + 4) * (2 * X::kSize)));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         return __builtin_bit_cast(i32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
@@ -1192,6 +1197,151 @@ __global__ __launch_bounds__(64 * W) void gemm_thin(GemmArgs g) {
             out(std::true_type());
         else
             out(std::false_type());
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows, B's rows the steps of the sum (16 bits): tiles of 16 R rows x 64 columns, four waves that share the tile
+// and split the steps; rows of any alignment.  A wave takes 64 rows of B in turn, the tile's 128 bytes of each, with its
+// next 64 in flight, and transposes them on the way from its own part of LDS to the matrix cores: LDS holds 64 rows of 64
+// columns, block c of 16 columns of row r at c ^ (r / 2 % 2 + 2 (r / 8 % 2)), so that the eight rows that half a wave reads
+// at once lie in different banks.
+template <class Kind, int R, bool ONCE>
+struct ThinRows {
+    typedef typename Kind::S4 S4;
+    static constexpr int kA = 2 * R, kLds = 64 * 128 + 16 * R * kBigK;
+    i32x4 a[kA], b[8];
+    static __device__ __forceinline__ int place(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2); }
+    // Steps s .. s + 63 of `rows`; pa: rows of A, pb: the lane's chunk of B's first row; zeros behind the last step.
+    // cols: the lane's elements inside B's rows (8: all); whole: of every lane.
+    __device__ __forceinline__ void read(const int8_t* const (&pa)[kA], const int8_t* pb, int64_t ldb, int64_t s,
+                                         int64_t rows, int cols, bool whole, bool narrow, const int8_t* zeros, int l) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t r = s + 8 * j + (l >> 3);
+            const int8_t* p = r < rows ? pb + r * ldb : zeros;
+            if (whole) {
+                b[j] = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const i32x4_u*>(p)) : *reinterpret_cast<const i32x4_u*>(p);
+            } else if (narrow) {
+                b[j] = i32x4{0, 0, 0, 0};
+                for (int i = 0; i < 7; ++i)
+                    if (r < rows && i < cols)
+                        b[j][i >> 1] |= (int32_t)((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1)));
+            } else {
+                p = r < rows && cols > 0 ? p + 2 * cols - 16 : zeros;
+                b[j] = shift_down(*reinterpret_cast<const i32x4_u*>(p), 16 - 2 * cols);
+            }
+        }
+        const int64_t k = 2 * s + 16 * (l & 7), K = 2 * rows;
+#pragma unroll
+        for (int j = 0; j < kA; ++j) a[j] = K < 16 ? load_short(pa[j], k, K) : load_any(pa[j], k, K);
+        if (s + 64 > rows && K >= 16)
+#pragma unroll
+            for (int j = 0; j < kA; ++j) a[j] = shift_down(a[j], (int)min(max(k - (K - 16), (int64_t)0), (int64_t)16));
+    }
+    // No wait for other waves: as ThinOps::multiply.
+    __device__ __forceinline__ void multiply(S4 (&acc)[R][4], int8_t* lds, int l) const {
+        int8_t* const la = lds + 64 * 128;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 8 * j + (l >> 3);
+            *reinterpret_cast<i32x4*>(lds + r * 128 + ((((l & 7) >> 1) ^ place(r)) << 5) + ((l & 1) << 4)) = b[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            const int r = 8 * j + (l >> 3);
+            *reinterpret_cast<i32x4*>(la + r * kBigK + (((l & 7) ^ big_swizzle(r)) << 4)) = a[j];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 x[4], y[R];
+            const int r = 32 * h + 8 * (l >> 4) + ((l >> 2) & 3);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int8_t* p = lds + r * 128 + 8 * (l & 3);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ((c ^ place(r)) << 5)));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 128 + ((c ^ place(r + 4)) << 5)));
+                typedef short s16x8 __attribute__((ext_vector_type(8)));
+                x[c] = __builtin_bit_cast(i32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int q = 16 * i + (l & 15);
+                y[i] = *reinterpret_cast<const i32x4*>(la + q * kBigK + (((4 * h + (l >> 4)) ^ big_swizzle(q)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][c] = Kind::mfma16(x[c], y[i], acc[i][c]);
+        }
+    }
+};
+
+template <class Kind, class D, int R, bool ONCE, bool PART>
+__global__ __launch_bounds__(256, 2) void gemm_thin_rows(GemmArgs args) {
+    typedef typename D::T T;
+    typedef typename Kind::S4 S4;
+    typedef ThinRows<Kind, R, ONCE> Ops;
+    constexpr int BM = 16 * R, W = 4, LD = 64 + 4, kSums = BM * LD * 4, kWave = Ops::kLds > kSums ? Ops::kLds : kSums;
+    const GemmArgs g = PART ? part_of(args, blockIdx.y) : args;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[W * kWave];
+    float* part = reinterpret_cast<float*>(lds);
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    // the row tiles of one column tile follow each other, as in gemm_thin
+    const uint32_t v = xcd_contiguous((int)blockIdx.x, 0, (int)gridDim.x);
+    int e;
+    int64_t lo, hi;
+    if (!find_tile<BM>(g, v % g.m_tiles, l, e, lo, hi)) return;
+    const int64_t n0 = (int64_t)(v / g.m_tiles) * 64, rows = g.K / 2;
+    const int8_t* pa[Ops::kA];
+#pragma unroll
+    for (int i = 0; i < Ops::kA; ++i) {
+        const int64_t p = lo + 8 * i + (l >> 3);
+        pa[i] = g.A + max(p < hi ? a_row(g, p) : -1, (int64_t)0) * g.lda;
+    }
+    const int8_t* pb = g.B + e * g.strideb + 2 * n0 + 16 * (l & 7);
+    const int cols = (int)max(min(g.N - n0 - 8 * (l & 7), (int64_t)8), (int64_t)0);
+    const bool whole = n0 + 64 <= g.N, narrow = g.N < 8;
+    S4 acc[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = S4{0, 0, 0, 0};
+    int8_t* const mine = lds + w * Ops::kLds;
+    Ops x, y;
+    int64_t s = 64 * w;
+    if (s < rows) x.read(pa, pb, g.ldb, s, rows, cols, whole, narrow, big_zeros, l);
+    for (; s < rows; s += 128 * W) {
+        const bool more = s + 64 * W < rows;
+        if (more) y.read(pa, pb, g.ldb, s + 64 * W, rows, cols, whole, narrow, big_zeros, l);
+        x.multiply(acc, mine, l);
+        if (!more) break;
+        if (s + 128 * W < rows) x.read(pa, pb, g.ldb, s + 128 * W, rows, cols, whole, narrow, big_zeros, l);
+        y.multiply(acc, mine, l);
+    }
+    __syncthreads();  // the sums take the same LDS
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<S4*>(part + (w * BM + 16 * i + (l & 15)) * LD + 16 * c + 4 * (l >> 4)) = acc[i][c];
+    __syncthreads();
+    for (int x4 = tid; x4 < BM * 16; x4 += 64 * W) {
+        const int row = x4 / 16, col = x4 % 16 * 4;
+        const int64_t p = lo + row, n = n0 + col;
+        if (p >= hi || n >= g.N) continue;
+        S4 sum = *reinterpret_cast<const S4*>(part + row * LD + col);
+#pragma unroll
+        for (int u = 1; u < W; ++u) sum += *reinterpret_cast<const S4*>(part + (u * BM + row) * LD + col);
+        T* c = (T*)g.C + p * g.ldc + n;
+        typedef T V4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+        if (n + 4 <= g.N)
+            *reinterpret_cast<V4*>(c) = V4{D::down(sum[0]), D::down(sum[1]), D::down(sum[2]), D::down(sum[3])};
+        else
+            for (int i = 0; i < 3; ++i)
+                if (n + i < g.N) c[i] = D::down(sum[i]);
     }
 }
 
