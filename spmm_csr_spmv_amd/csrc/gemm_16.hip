@@ -149,22 +149,25 @@ int add_parts(const PartArgs& g, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? SP_OK : SP_ERR_HIP;
 }
 
+// Rows of these lengths, laid out without gaps, are not aligned.  (The workspace's size goes by the lengths alone.)
+bool odd(int64_t M, int64_t N) { return M % 8 || N % 8; }
+
 // Into how many parts to cut the sums of `steps` steps of a product's tiles, and whether 256 x 256 tiles are better than
 // 128 x 128 ones: the least of an estimate in us.  128 x 128 tiles take 0.65 a step where there is one on a CU, 1.1 where
-// there are two; 256 x 256 ones 1.8; parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
+// there are two; 256 x 256 ones 1.8; 128 x 128 ones of unaligned rows 1.6 with up to two; parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
 struct Cut {
     bool wide;
     int splits;
 };
-Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double outputs, bool wide_parts) {
+Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double outputs, bool wide_parts, bool unaligned) {
     Cut best{false, 1};
     double least = 1e300;
-    for (int w = 0; w < 2; ++w)
+    for (int w = 0; w < (unaligned ? 1 : 2); ++w)
         for (const int n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             if (n > 1 && (2 * n > steps || (w && !wide_parts))) break;
             const int64_t each = (steps + n - 1) / n, parts = n == 1 ? 1 : (steps + each - 1) / each;  // none is empty
             const int64_t tiles = (w ? wide_tiles : narrow_tiles) * parts;
-            const double step = w ? 1.8 * ((tiles + 255) / 256) : tiles <= 256 ? 0.65 : 1.1 * ((tiles + 511) / 512);
+            const double step = unaligned ? 1.6 * ((tiles + 511) / 512) : w ? 1.8 * ((tiles + 255) / 256) : tiles <= 256 ? 0.65 : 1.1 * ((tiles + 511) / 512);
             const double us = step * each + (parts > 1 ? 4.0 + 2e-6 * parts * outputs : 0.0);
             if (us < least) least = us, best = Cut{w != 0, (int)parts};
         }
@@ -259,7 +262,7 @@ RowPlan row_plan(int64_t S, int32_t E, int64_t M, int64_t N) {
     }
     // an expert's last tile is half as high as the others on the average, and takes half their time
     const auto even = [&](int64_t b) { return tiles(b, b) - (groups > 1 ? groups / 2 * ((N + b - 1) / b) : 0); };
-    const Cut c = best_cut(even(128), even(256), steps, (double)S * N, false);
+    const Cut c = best_cut(even(128), even(256), steps, (double)S * N, false, odd(M, N));
     return RowPlan{0, c.wide, c.splits};
 }
 
@@ -294,7 +297,7 @@ int row_gradient_t(const GemmArgs& g, const RowPlan& plan, hipStream_t s) {
 // dB: the parts of an expert's rows, of 64 rows a step on the average.
 Cut grad_cut(int64_t S, int32_t E, int64_t M, int64_t N) {
     const auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b) * E; };
-    return best_cut(tiles(128), tiles(256), (S / E + 63) / 64, (double)E * M * N, true);
+    return best_cut(tiles(128), tiles(256), (S / E + 63) / 64, (double)E * M * N, true, odd(M, N));
 }
 
 template <class Kind, class D>

@@ -314,20 +314,24 @@ struct BigDirect {
     __device__ __forceinline__ const int8_t* at(int j, int step) const {
         return p[j % X::kCopied] + min((int64_t)step * kBigK + chunk, last);
     }
-    // Rows of any alignment and length, zeros behind K.  The last piece of a row that K cuts begins with bytes that
-    // the piece before holds: zeroed, or with ALONE, where the other operand does not begin with the same, moved to where they belong.
-    template <bool ALONE>
-    __device__ __forceinline__ i32x4 load(int j, int step, bool mask) const {
+    // Rows of any alignment, K >= 16 (SHORT: of any length): load(), and then finish() what it gave.  The last piece of
+    // a row that K cuts begins with bytes that the piece before holds: zeroed, or with ALONE, where the other operand does not
+    // begin with the same, moved to where they belong.
+    template <bool SHORT>
+    __device__ __forceinline__ i32x4 load(int j, int step) const {
         const int64_t k = (int64_t)step * kBigK + chunk;
-        if (K < 16) return load_short(p[j % X::kCopied], k, K);
-        i32x4 v = load_any(p[j % X::kCopied], k, K);
-        if (mask) {
-            if (ALONE) return shift_down(v, (int)min(max(k - (K - 16), (int64_t)0), (int64_t)16));
+        return SHORT && K < 16 ? load_short(p[j % X::kCopied], k, K) : load_any(p[j % X::kCopied], k, K);
+    }
+    template <bool SHORT, bool ALONE>
+    __device__ __forceinline__ i32x4 finish(i32x4 v, int step, bool last_step) const {
+        if (!last_step || (SHORT && K < 16)) return v;
+        const int64_t k = (int64_t)step * kBigK + chunk;
+        if (ALONE) return shift_down(v, (int)min(max(k - (K - 16), (int64_t)0), (int64_t)16));
 #pragma unroll
-            for (int d = 0; d < 4; ++d) v[d] &= low_mask(k, K, d);
-        }
+        for (int d = 0; d < 4; ++d) v[d] &= low_mask(k, K, d);
         return v;
     }
+    __device__ __forceinline__ bool is_short() const { return K < 16; }
 };
 
 // n / d for 0 <= n < 2^31: d = 1, or (n * m) >> 32 >> s with m = floor(2^(32 + s) / d) + 1 and 2^s < d <= 2^(s + 1):
@@ -416,21 +420,25 @@ struct BigTransposed {
         }
     }
     __device__ __forceinline__ const int8_t* at(int j, int step) const { return row(j, step, zeros); }
-    // Branches that all lanes take alike only: loads behind others would wait for one another.  A chunk that the
-    // row's end cuts is loaded with the elements before it and moved down.
-    template <bool>
-    __device__ __forceinline__ i32x4 load(int j, int step, bool) const {
-        if (inside) return *reinterpret_cast<const i32x4_u*>(row(j, step, zeros));
-        const int8_t* p = row(j, step, nullptr);
-        if (narrow) {
+    // A chunk that the row's end cuts is loaded with the elements before it and moved down; rows shorter than a chunk
+    // (SHORT) go element by element.
+    template <bool SHORT>
+    __device__ __forceinline__ i32x4 load(int j, int step) const {
+        if (SHORT && narrow) {
+            const int8_t* p = row(j, step, nullptr);
             i32x4 v = {0, 0, 0, 0};
             for (int i = 0; i < 7; ++i)
                 if (p && i < cols) v[i >> 1] |= (int32_t)((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1)));
             return v;
         }
-        const int8_t* at = p && cols > 0 ? p + 2 * cols - 16 : zeros;
-        return shift_down(*reinterpret_cast<const i32x4_u*>(at), 16 - 2 * cols);
+        const int8_t* p = row(j, step, zeros);
+        return *reinterpret_cast<const i32x4_u*>(cols == 0 ? zeros : p == zeros ? p : p + (2 * cols - 16));
     }
+    template <bool SHORT, bool>
+    __device__ __forceinline__ i32x4 finish(i32x4 v, int, bool) const {
+        return inside || (SHORT && narrow) ? v : shift_down(v, 16 - 2 * cols);
+    }
+    __device__ __forceinline__ bool is_short() const { return narrow; }
 };
 
 // Copies [FROM, TO) of the step's, in the order A, B.  ONCE: no other tile reads these rows of B.
@@ -634,50 +642,71 @@ __device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][X::U], con
 }
 
 // The same for rows of any alignment and length, with the copies through registers
-// (global_load_lds wants aligned pieces): the next step's loads are in flight while this one is
-// multiplied, and go to the other LDS buffer after it.
-template <class Kind, int F, bool TA, bool TB, class SA, class SB>
-__device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, SB& sb,
+// (global_load_lds wants aligned pieces): the loads of the next kAhead steps are in flight while a step is multiplied,
+// after which the oldest go to the other LDS buffer.  A step alone takes a quarter of a load's latency.
+constexpr int kAhead = 2;
+template <class Kind, int F, bool TA, bool TB, bool SHORT, class SA, class SB>
+__device__ __forceinline__ void staged_loop(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, SB& sb,
                                             int steps, int w, int l) {
     using S = BigShape<Tile128, F>;
+    constexpr int D = SHORT ? 1 : kAhead;
     const int wm = w & 1, wn = w >> 1;
-    i32x4 v[S::kCopies];
-    const auto load = [&](int s) {
+    i32x4 v[D][S::kCopies];
+    const auto load = [&](i32x4 (&x)[S::kCopies], int s) {
         sb.fetch(s);
 #pragma unroll
         for (int j = 0; j < S::kCopies; ++j)
-            v[j] = j < S::kA ? sa.template load<TB>(j, s, s == steps - 1)
-                             : sb.template load<TA>(j - S::kA, s, Kind::kFloat && s == steps - 1);
+            x[j] = j < S::kA ? sa.template load<SHORT>(j, s) : sb.template load<SHORT>(j - S::kA, s);
     };
-    const auto store = [&](int s) {
+    const auto store = [&](const i32x4 (&x)[S::kCopies], int s) {
         int8_t* la = (s & 1 ? m.a[1] : m.a[0]) + w * 1024 + l * 16;
         int8_t* lb = (s & 1 ? m.b[1] : m.b[0]) + w * 1024 + l * 16;
+        const bool last = s == steps - 1;
 #pragma unroll
-        for (int j = 0; j < S::kCopies; ++j)
-            *reinterpret_cast<i32x4*>(j < S::kA ? la + j * S::kRows * kBigK : lb + (j - S::kA) * S::kRows * kBigK) = v[j];
+        for (int j = 0; j < S::kCopies; ++j) {
+            if (j < S::kA)
+                *reinterpret_cast<i32x4*>(la + j * S::kRows * kBigK) = sa.template finish<SHORT, TB>(x[j], s, last);
+            else
+                *reinterpret_cast<i32x4*>(lb + (j - S::kA) * S::kRows * kBigK) =
+                    sb.template finish<SHORT, TA>(x[j], s, Kind::kFloat && last);
+        }
     };
     big_clear(acc);
-    if (steps > 0) {
-        load(0);
-        store(0);
-    }
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        const int8_t* la = s & 1 ? m.a[1] : m.a[0];
-        const int8_t* lb = s & 1 ? m.b[1] : m.b[0];
-        if (s + 1 < steps) load(s + 1);
-        BigOps<Kind, Tile128, F, TA, TB> x0, x1;
-        x0.read(la, lb, 0, wm, wn, l);
+    // steps behind the last are not loaded; set i holds steps i, i + D, ..
 #pragma unroll
-        for (int ks = 0; ks < 4; ks += 2) {
-            x1.read(la, lb, ks + 1, wm, wn, l);
-            x0.multiply(acc);
-            if (ks == 0) x0.read(la, lb, 2, wm, wn, l);
-            x1.multiply(acc);
+    for (int i = 0; i < D; ++i)
+        if (i < steps) load(v[i], i);
+    if (steps > 0) store(v[0], 0);
+    __syncthreads();
+    for (int s0 = 0; s0 < steps; s0 += D) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            const int s = s0 + i;
+            if (s >= steps) break;
+            if (s + D < steps) load(v[i], s + D);
+            const int8_t* la = s & 1 ? m.a[1] : m.a[0];
+            const int8_t* lb = s & 1 ? m.b[1] : m.b[0];
+            BigOps<Kind, Tile128, F, TA, TB> x0, x1;
+            x0.read(la, lb, 0, wm, wn, l);
+#pragma unroll
+            for (int ks = 0; ks < 4; ks += 2) {
+                x1.read(la, lb, ks + 1, wm, wn, l);
+                x0.multiply(acc);
+                if (ks == 0) x0.read(la, lb, 2, wm, wn, l);
+                x1.multiply(acc);
+            }
+            if (s + 1 < steps) store(v[(i + 1) % D], s + 1);
+            __syncthreads();
         }
-        if (s + 1 < steps) store(s + 1);
-        __syncthreads();
     }
+}
+template <class Kind, int F, bool TA, bool TB, class SA, class SB>
+__device__ __forceinline__ void staged_sums(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, SB& sb,
+                                            int steps, int w, int l) {
+    if (sa.is_short() || sb.is_short())
+        staged_loop<Kind, F, TA, TB, true>(acc, m, sa, sb, steps, w, l);
+    else
+        staged_loop<Kind, F, TA, TB, false>(acc, m, sa, sb, steps, w, l);
 }
 
 // Where the copies of K-contiguous operands read: rows kRows j + 8 w + l / 8 of the tile, chunk
