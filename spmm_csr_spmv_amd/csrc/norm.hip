@@ -153,6 +153,7 @@ __device__ __forceinline__ void norm_store(T* p, int64_t len, typename Chunk<T>:
         chunk_store(p, len, v);
 }
 
+// A workgroup goes over its rows with the next one's loads in flight, and keeps the weights of its columns.
 template <class D, class W, int TPR, bool LINES, bool I8>
 __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
     typedef typename D::T T;
@@ -161,12 +162,33 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
     __shared__ float part[2][2][Across<TPR>::kWaves];
     Across<TPR> across{part, 0};
     const int lane = threadIdx.x % TPR;
-    const int64_t chunks = (g.H + N - 1) / N;
-    for (int64_t row = first_row<TPR>(); row < g.rows; row += (int64_t)gridDim.x * kRows<TPR>) {
-        const T* x = (const T*)g.X + row * g.ldx;
-        const T* r = g.R ? (const T*)g.R + row * g.ldr : nullptr;
+    const int64_t chunks = (g.H + N - 1) / N, step = (int64_t)gridDim.x * kRows<TPR>;
+    float w[kHeld][N];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+        if (lane + h * TPR < chunks) weights_at<W, N>(g.weight, (lane + h * TPR) * N, g.H - (lane + h * TPR) * N, w[h]);
+    const auto load = [&](const void* p, int64_t ld, int64_t row, int64_t c) {
+        return norm_load<T, LINES>((const T*)p + row * ld + c * N, g.H - c * N);
+    };
+    struct Held {
+        V x[kHeld], r[kHeld];
+    };
+    const auto hold = [&](Held& b, int64_t row) {
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (lane + h * TPR < chunks) {
+                b.x[h] = load(g.X, g.ldx, row, lane + h * TPR);
+                if (g.R) b.r[h] = load(g.R, g.ldr, row, lane + h * TPR);
+            }
+    };
+    int64_t row = first_row<TPR>();
+    Held next;
+    if (row < g.rows) hold(next, row);
+    for (; row < g.rows; row += step) {
+        const Held now = next;
+        if (row + step < g.rows) hold(next, row + step);
         T* sum = g.sum ? (T*)g.sum + row * g.lds : nullptr;
-        const T* stored = sum ? sum : x;
+        const T* stored = sum ? sum : (const T*)g.X + row * g.ldx;
         float held[kHeld][N];  // s w
         float ss = 0.0f, most = 0.0f;
         const auto sums = [&](const float (&s)[N], const float (&t)[N]) {
@@ -176,16 +198,15 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 if (I8) most = Most()(fabsf(t[i]), most);
             }
         };
-        // s of chunk c, formed and stored
+        // s of chunk c, formed and stored; t: its weights, then s w
         const auto first = [&](int64_t c, V v, V q, float (&t)[N]) {
             const int64_t k = c * N, len = g.H - k;
-            if (r) {
+            if (g.R) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[i] = D::down(D::up(v[i]) + D::up(q[i]));
             }
             if (sum) norm_store<T, LINES>(sum + k, len, v);
             float s[N];
-            weights_at<W, N>(g.weight, k, len, t);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 s[i] = D::up(v[i]);
@@ -204,21 +225,18 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 t[i] *= s[i];
             }
         };
-        const auto load = [&](const T* p, int64_t c) { return norm_load<T, LINES>(p + c * N, g.H - c * N); };
-        V vx[kHeld], vr[kHeld];
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
             if (lane + h * TPR < chunks) {
-                vx[h] = load(x, lane + h * TPR);
-                if (r) vr[h] = load(r, lane + h * TPR);
-            }
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (lane + h * TPR < chunks) first(lane + h * TPR, vx[h], vr[h], held[h]);
+                for (int i = 0; i < N; ++i) held[h][i] = w[h][i];
+                first(lane + h * TPR, now.x[h], now.r[h], held[h]);
+            }
         for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
             float t[N];
-            const V v = load(x, c);
-            first(c, v, r ? load(r, c) : v, t);
+            const V v = load(g.X, g.ldx, row, c);
+            weights_at<W, N>(g.weight, c * N, g.H - c * N, t);
+            first(c, v, g.R ? load(g.R, g.ldr, row, c) : v, t);
         }
         across(ss, most, Add(), Most());
         float f = range_factor(ss, g.eps);
@@ -472,7 +490,9 @@ int chunk_of(int32_t dtype) { return dtype == SP_F32 ? 4 : 8; }
 constexpr int kMostForward = 1024, kMostBackward = 512;
 int norm_lanes(int64_t H, int32_t dtype, int most) {
     const int64_t chunks = (H + chunk_of(dtype) - 1) / chunk_of(dtype);
-    return chunks <= 16 * kHeld ? 16 : chunks <= 64 * kHeld ? 64 : chunks <= 256 * kHeld ? 256 : most;
+    for (const int lanes : {16, 64, 256, 512})
+        if (chunks <= lanes * kHeld) return lanes;
+    return most;
 }
 bool held(int64_t H, int32_t dtype) { return (H + chunk_of(dtype) - 1) / chunk_of(dtype) <= kMostBackward * kHeld; }
 // Whether rows are whole lines that no other row shares.
@@ -481,12 +501,17 @@ bool on_lines(const void* p, int64_t ld, int64_t H, int32_t dtype) {
     return ((uintptr_t)p | (uintptr_t)(ld * size) | (uintptr_t)(H * size)) % 128 == 0;
 }
 
-constexpr int64_t kMostGroups = 1 << 20;  // workgroups; more rows take several rounds
+// Workgroups; more rows take several rounds (us with 1024 and 4096: 16384 x 4096 bf16 without a residual 46.1, 46.1,
+// int8 with one 78, 80; 3000 x 16384 37.6, 46.6, int8 71, 82; 48613 x 1091 fp32 with a residual 166, 179).  Whole lines of
+// four streams, two of them written, want more: 16384 x 4096 bf16 with a residual 95, 92; 65536 x 512 46.5, 45.6.
+constexpr int64_t kMostGroups = 1024, kMostFour = 4096;
 
-// Workgroups of the gradient, and so parts of dweight.
-int64_t backward_groups(int64_t rows, int64_t H, int32_t dtype) {
+// Workgroups of the gradient, and so parts of dweight, which have to be written and read; rows that share lines
+// with their neighbours want more of them (us with 512 and 1024: 16384 x 4096 bf16 92, 108, 65536 x 512 48, 60; 48613 x 1091
+// fp32 254, 172).  lines: whether they do not; the workspace has room for either.
+int64_t backward_groups(int64_t rows, int64_t H, int32_t dtype, bool lines) {
     const int lanes = norm_lanes(H, dtype, kMostBackward), per = std::max(256, lanes) / lanes;
-    return std::min<int64_t>((rows + per - 1) / per, 1024);
+    return std::min<int64_t>((rows + per - 1) / per, lines || rows < 4096 ? 512 : 1024);
 }
 // Rows a part of norm_columns_kernel.
 int64_t column_rows(int64_t rows) { return std::max<int64_t>(16, (rows + 255) / 256); }
@@ -504,6 +529,7 @@ int norm_by(int32_t dtype, int32_t w_type, int64_t H, bool lines, Go go) {
         return n == 16    ? go(d, w, Lanes<16>(), std::false_type())
                : n == 64  ? with(Lanes<64>())
                : n == 256 ? with(Lanes<256>())
+               : n == 512 ? with(Lanes<512>())
                           : with(Lanes<MOST>());
     };
     if (dtype == SP_F32) return lanes(F32(), F32());
@@ -524,7 +550,7 @@ int rms_norm_device(const NormRows& n, void* sum, int64_t lds, void* Y, int64_t 
         typedef decltype(w) W;
         constexpr int L = decltype(l)::value;
         constexpr bool kLines = decltype(on)::value;
-        const dim3 grid((unsigned)std::min<int64_t>((g.rows + kRows<L> - 1) / kRows<L>, kMostGroups));
+        const dim3 grid((unsigned)std::min<int64_t>((g.rows + kRows<L> - 1) / kRows<L>, kLines && n.R && !scale ? kMostFour : kMostGroups));
         if (scale)
             hipLaunchKernelGGL((rms_norm_kernel<D, W, L, kLines, true>), grid, dim3(kThreads<L>), 0, s, g);
         else
@@ -534,7 +560,7 @@ int rms_norm_device(const NormRows& n, void* sum, int64_t lds, void* Y, int64_t 
 }
 
 size_t rms_norm_backward_bytes(int64_t rows, int64_t H, int32_t dtype) {
-    if (held(H, dtype)) return (size_t)backward_groups(rows, H, dtype) * part_stride(H) * sizeof(float);
+    if (held(H, dtype)) return (size_t)backward_groups(rows, H, dtype, false) * part_stride(H) * sizeof(float);
     const int64_t each = column_rows(rows);
     return ((size_t)part_stride(rows) + (size_t)((rows + each - 1) / each) * part_stride(H)) * sizeof(float);
 }
@@ -545,17 +571,17 @@ int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, vo
     g.rows = n.rows, g.H = n.H, g.X = n.X, g.ldx = n.ldx, g.R = n.R, g.ldr = n.ldr, g.weight = n.weight, g.eps = n.eps;
     g.dY = dY, g.lddy = lddy, g.Y = dX, g.ldy = lddx;
     const bool whole = held(n.H, n.dtype);
+    const bool lines = whole && on_lines(n.X, n.ldx, n.H, n.dtype) && on_lines(n.R, n.R ? n.ldr : 0, n.H, n.dtype) &&
+                       on_lines(dY, lddy, n.H, n.dtype) && on_lines(dX, lddx, n.H, n.dtype);
     const int64_t each = column_rows(n.rows);
-    const int64_t parts = n.rows == 0 ? 0 : whole ? backward_groups(n.rows, n.H, n.dtype) : (n.rows + each - 1) / each;
+    const int64_t parts = n.rows == 0 ? 0 : whole ? backward_groups(n.rows, n.H, n.dtype, lines) : (n.rows + each - 1) / each;
     float* const part = (float*)work + (whole ? 0 : part_stride(n.rows));
     if (dweight) {
         g.part = part;
         if (!whole) g.rstd = (float*)work;
     }
     if (n.rows > 0) {
-        const bool lines = on_lines(n.X, n.ldx, n.H, n.dtype) && on_lines(n.R, n.R ? n.ldr : 0, n.H, n.dtype) &&
-                           on_lines(dY, lddy, n.H, n.dtype) && on_lines(dX, lddx, n.H, n.dtype);
-        const int rc = norm_by<kMostBackward>(n.dtype, n.w_type, n.H, lines && whole, [&](auto d, auto w, auto l, auto on) {
+        const int rc = norm_by<kMostBackward>(n.dtype, n.w_type, n.H, lines, [&](auto d, auto w, auto l, auto on) {
             typedef decltype(d) D;
             typedef decltype(w) W;
             constexpr int L = decltype(l)::value;
