@@ -334,20 +334,20 @@ struct BigDirect {
     __device__ __forceinline__ bool is_short() const { return K < 16; }
 };
 
-// n / d for 0 <= n < 2^31: d = 1, or (n * m) >> 32 >> s with m = floor(2^(32 + s) / d) + 1 and 2^s < d <= 2^(s + 1):
+// n / d for 0 <= n < 2^31 as (n * m) >> 32 >> s with m = floor(2^(32 + s) / d) + 1 and 2^s < d <= 2^(s + 1):
 // m d exceeds 2^(32 + s) by at most d <= 2^(s + 1), so that the product exceeds n / d by less than (n / 2^31) / d < 1 / d.
+// d = 1: (2 n * 2^31) >> 32.
 struct FastDiv {
-    uint32_t m, s;
+    uint32_t m, s, one;
     static FastDiv by(int32_t d) {
-        FastDiv f{0, 0};
+        FastDiv f{1u << 31, 0, 1};
         if (d == 1) return f;
+        f.one = 0;
         while ((2ll << f.s) < d) ++f.s;
         f.m = (uint32_t)(((1ull << (32 + f.s)) / (uint32_t)d) + 1);
         return f;
     }
-    __device__ __forceinline__ int32_t operator()(int32_t n) const {
-        return m == 0 ? n : (int32_t)(__umulhi((uint32_t)n, m) >> s);
-    }
+    __device__ __forceinline__ int32_t operator()(int32_t n) const { return (int32_t)(__umulhi((uint32_t)n << one, m) >> s); }
 };
 
 // Where a lane's copy j of a step reads an operand whose rows are steps of the sum.  GATHER: row i of the sum is the
@@ -404,18 +404,16 @@ struct BigTransposed {
             const int8_t* p = base + (int64_t)u * ld;
             return u + row0 < rows ? p : none;
         } else {
-            int64_t off[kWave];
-            bool there[kWave];
-#pragma unroll
-            for (int i = 0; i < kWave; ++i) {
-                const int at = u + w * kWave + i, t = slots(max(f[j][i], 0));
-                there[i] = at < rows && f[j][i] >= 0 && t < a_rows;
-                off[i] = t * ld;
-            }
             const int mine = row0 - w * kWave;
             const int8_t* p = none;
 #pragma unroll
-            for (int i = 0; i < kWave; ++i) p = mine == i ? (there[i] ? base + off[i] : none) : p;
+            for (int i = 0; i < kWave; ++i) {
+                const int at = u + w * kWave + i, t = slots(f[j][i] & 0x7fffffff);
+                // the same for all lanes: one test of three signs, and no branch
+                const bool there = (f[j][i] | ((int)a_rows - 1 - t) | (rows - 1 - at)) >= 0;
+                const int8_t* q = reinterpret_cast<const int8_t*>(reinterpret_cast<uintptr_t>(base) + (uint64_t)(uint32_t)t * (uint64_t)ld);
+                p = mine == i && there ? q : p;
+            }
             return p;
         }
     }
