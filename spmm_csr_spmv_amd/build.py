@@ -19,7 +19,7 @@ PROBE_LIB = os.path.join(HERE, "libspx_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 
 SOURCES = ["api.cpp", "plan_host.cpp", "tune.cpp", "convert.hip", "spmv.hip", "pstream.hip", "spmm.hip", "bsr.hip", "bsr_convert.hip", "wcsr.hip", "xwin.hip",
-           "moe_api.cpp", "moe.hip", "quant.hip", "gemm_i8.hip", "layer_api.cpp", "norm.hip", "gemm_16.hip"]
+           "moe_api.cpp", "moe.hip", "quant.hip", "gemm_i8.hip", "layer_api.cpp", "norm.hip", "gemm_16.hip", "gemm_16_grad.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1373,6 +1373,12 @@ __global__ __launch_bounds__(256, 2) void gemm_thin_rows(GemmArgs args) {
 }
 
 // ---------------------------------------------------------------- launch
+// go(kind, type)
+template <class Go>
+inline int by_type(int32_t dtype, Go go) {
+    return dtype == SP_BF16 ? go(KindBf16(), Bf16()) : go(KindF16(), F16());
+}
+
 inline bool aligned16(const GemmArgs& g) {
     return ((uintptr_t)g.A | (uintptr_t)g.B | (uintptr_t)g.lda | (uintptr_t)g.ldb |
             (uintptr_t)(g.E > 1 ? g.strideb : 0)) % 16 == 0;
