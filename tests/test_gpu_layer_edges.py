@@ -97,6 +97,35 @@ def test_gated_int8_of_every_tile(M, N, K, aligned):
     check(sp.gated_i8(A, sa, B, sb), h, bound, (M, N, K))
 
 
+def test_gated_gradient_of_offsets_that_descend():
+    """An expert's rows may lie behind the last offset."""
+    rng = rng_for("descend")
+    S, N, K = 60, 24, 40
+    A, B, dH = rows_tensor(rng, S, K, "bf16"), rows_tensor(rng, 3 * 2 * N, K, "bf16").reshape(3, 2 * N, K), rows_tensor(rng, S, N, "bf16")
+    pre = rows_tensor(rng, S, 2 * N, "bf16")
+    o = torch.tensor([0, 50, 20, 2 ** 31 - 1], dtype=torch.int32, device="cuda")  # 0 .. 50, none, 20 .. 60
+    _, dB = sp.moe_gated_backward(dH, pre, A, B, o, dA=None)
+    for e, rows in enumerate((slice(0, 50), slice(0, 0), slice(20, 60))):
+        _, want = sp.moe_gated_backward(dH[rows].contiguous(), pre[rows].contiguous(), A[rows].contiguous(), B[e], dA=None)
+        assert torch.allclose(dB[e].float(), want.float(), rtol=4 * HALF["bf16"], atol=1e-5)  # two roundings, sums in other orders
+    o = torch.tensor([0, 50, 20, 20], dtype=torch.int32, device="cuda")
+    dA, _ = sp.moe_gated_backward(dH, pre, A, B, o, dB=None)
+    want, _ = sp.moe_gated_backward(dH[:50].contiguous(), pre[:50].contiguous(), A[:50].contiguous(), B[0], dB=None)
+    assert torch.allclose(dA[:50].float(), want.float(), rtol=4 * HALF["bf16"], atol=1e-5)
+
+
+def test_the_same_source_again():
+    """Many rows that read one token's."""
+    rng = rng_for("again")
+    S, N, K = 300, 40, 72
+    A, B, dC = rows_tensor(rng, 5, K, "bf16"), rows_tensor(rng, N, K, "bf16"), rows_tensor(rng, S, N, "bf16")
+    o, src = torch.tensor([0, S], dtype=torch.int32, device="cuda"), torch.full((S,), 7, dtype=torch.int32, device="cuda")
+    copies = A[3:4].expand(S, K).contiguous()
+    assert torch.equal(sp.moe_gemm(A, B[None], o, src=src, slots=2), sp.moe_gemm(copies, B[None], o))
+    for got, want in zip(sp.moe_gemm_backward(dC, A, B[None], o, src=src, slots=2), sp.moe_gemm_backward(dC, copies, B[None], o)):
+        assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ beyond 32 bits
 def test_rows_far_apart():
     """Rows whose distances pass 2^31 elements and 2^32 bytes from the first to the last."""
