@@ -640,14 +640,15 @@ __device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][X::U], con
 }
 
 // The same for rows of any alignment and length, with the copies through registers
-// (global_load_lds wants aligned pieces): the loads of the next kAhead steps are in flight while a step is multiplied,
-// after which the oldest go to the other LDS buffer.  A step alone takes a quarter of a load's latency.
-constexpr int kAhead = 2;
+// (global_load_lds wants aligned pieces): the loads of the next steps are in flight while a step is multiplied, after
+// which the oldest go to the other LDS buffer.  Two steps ahead in 16 bits, where a step alone takes a quarter of a load's
+// latency (dA of 1024 x 1000 x 1001 bf16 23 us, one ahead 47; three would not fit the registers); one in 8 bits
+// (8192 x 8192 x 4095 474, two ahead 485).
 template <class Kind, int F, bool TA, bool TB, bool SHORT, class SA, class SB>
 __device__ __forceinline__ void staged_loop(typename Kind::S16 (&acc)[F][2], const BigBuffers<2>& m, const SA& sa, SB& sb,
                                             int steps, int w, int l) {
     using S = BigShape<Tile128, F>;
-    constexpr int D = SHORT ? 1 : kAhead;
+    constexpr int D = SHORT || !Kind::kFloat ? 1 : 2;
     const int wm = w & 1, wn = w >> 1;
     i32x4 v[D][S::kCopies];
     const auto load = [&](i32x4 (&x)[S::kCopies], int s) {

