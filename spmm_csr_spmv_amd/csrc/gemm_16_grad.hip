@@ -29,8 +29,8 @@ struct GradArgs {
 
 // Square tiles of dB, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
 // are split and the parts' fp32 sums (PART) added afterwards in the order of the splits.
-// 4096 rows, 8192 x 8192 bf16 in 430 us, 1.28 PFLOP/s (the library 450); 8192 x 4 of 32 experts, 2816 x 2048 in 410, and
-// 437 with sources: the matrix cores and power, as for the products.
+// Matrix cores and power bound it, as they do the products: 4096 rows, 8192 x 8192 bf16 in 422 to 432 us, 1.28 PFLOP/s (the
+// library 480); 8192 x 4 of 32 experts, 2816 x 2048 420 to 431 (128 x 128 tiles 509), with sources 440.
 template <class Kind, class D, class X, bool STAGED, bool PART, bool GATHER>
 __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uint32_t total, const BigBuffers<2>& m,
                                               int32_t* lrow, int tid, int w, int l) {
@@ -153,13 +153,17 @@ int add_parts(const PartArgs& g, hipStream_t s) {
 bool odd(int64_t M, int64_t N) { return M % 8 || N % 8; }
 
 // Into how many parts to cut the sums of `steps` steps of a product's tiles, and whether 256 x 256 tiles are better than
-// 128 x 128 ones: the least of an estimate in us.  128 x 128 tiles take 0.65 a step where there is one on a CU, 1.1 where
-// there are two; 256 x 256 ones 1.8; 128 x 128 ones of unaligned rows 1.6 with up to two; parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
+// 128 x 128 ones: the least of an estimate in us.  A step (64 of the sum) of 128 x 128 tiles takes `one` where there is one
+// on a CU, 1.1 where there are two; of 256 x 256 ones 1.8; of 128 x 128 ones of unaligned rows 1.05 and 1.6.  All of it takes
+// `memory` at least.  Parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
+// dB (bf16, us): of 32768 rows, 1024 x 1024 in parts 106, whole 324; of 512 rows, 1024 x 4096 whole 10, in 4 parts 36; of
+// 2048 x 8 of 64 experts, 2816 x 2048 in 256 x 256 tiles 358, in 128 x 128 ones 433.
 struct Cut {
     bool wide;
     int splits;
 };
-Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double outputs, bool wide_parts, bool unaligned) {
+Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double one, double memory, double outputs,
+             bool wide_parts, bool unaligned) {
     Cut best{false, 1};
     double least = 1e300;
     for (int w = 0; w < (unaligned ? 1 : 2); ++w)
@@ -167,8 +171,10 @@ Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double out
             if (n > 1 && (2 * n > steps || (w && !wide_parts))) break;
             const int64_t each = (steps + n - 1) / n, parts = n == 1 ? 1 : (steps + each - 1) / each;  // none is empty
             const int64_t tiles = (w ? wide_tiles : narrow_tiles) * parts;
-            const double step = unaligned ? 1.6 * ((tiles + 511) / 512) : w ? 1.8 * ((tiles + 255) / 256) : tiles <= 256 ? 0.65 : 1.1 * ((tiles + 511) / 512);
-            const double us = step * each + (parts > 1 ? 4.0 + 2e-6 * parts * outputs : 0.0);
+            const double step = w              ? 1.8 * ((tiles + 255) / 256)
+                                : tiles <= 256 ? (unaligned ? 1.05 : one)
+                                               : (unaligned ? 1.6 : 1.1) * ((tiles + 511) / 512);
+            const double us = std::max(step * each, memory) + (parts > 1 ? 4.0 + 2e-6 * parts * outputs : 0.0);
             if (us < least) least = us, best = Cut{w != 0, (int)parts};
         }
     return best;
@@ -208,10 +214,14 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N
 }
 
 // ---------------------------------------------------------------- launch
-// dA = dC B, M rows of B a sum.  Tiles of 16 rows where a matrix has up to 16 rows on the average, of 32 up to 32, whose
-// sums are cut into as many parts as give 512 workgroups; else 128 x 128 or 256 x 256 ones.  us, bf16, thin tiles and
-// 128 x 128 ones: 16 x 14336 x 4096 29 and 41, 32 x 4096 x 4096 16 and 25, 128 x 8 of 64 experts (16 rows), 2816 x 2048 165
-// and 252 (739 MB of weights: 4.5 TB/s).  4096 x 8192 x 8192 in 256 x 256 tiles 430, 1.28 PFLOP/s (the library 386).
+// dA = dC B, M rows of B a sum.  One matrix of up to 2^23 numbers and up to 32 rows: tiles of 16 or 32 rows, whose sums are
+// cut into as many parts as give 512 workgroups; else 128 x 128 or 256 x 256 ones, in parts where best_cut says so, four
+// steps in LDS where there is a tile a CU.  bf16, us: 16 x 1024 x 4096 (rows, M, columns) thin 8.3, 128x128 10.1;
+// 16 x 2048 x 2048 8.2, 10.8; 16 x 4096 x 4096 14.9, 13.5; 16 x 14336 x 4096 32, in 8 parts 25 (4.7 TB/s of weights; two
+// steps in LDS 31), whole 84; 256 x 4096 x 4096 in 4 parts 26, whole 37.  Experts' weights take their time whatever the
+// tiles, so that parts and thin tiles only cost: 128 x 8 of 64 experts, 2816 x 2048 whole 132 to 146 (5.1 to 5.6 TB/s of
+// weights), in 4 parts 180, thin 174 to 189; rows off 16 bytes (2815 x 2047) 153, 194, 355.  4096 x 8192 x 8192 in
+// 256 x 256 tiles 435, 1.26 PFLOP/s (the library 417).
 struct RowPlan {
     int high;    // rows of a thin tile (16 R), or 0
     bool wide;
@@ -219,7 +229,7 @@ struct RowPlan {
 };
 RowPlan row_plan(int64_t S, int32_t E, int64_t M, int64_t N) {
     const int64_t groups = std::max<int64_t>(std::min<int64_t>(E, S), 1), rows = S / groups;
-    const int high = rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+    const int high = groups > 1 || M * N > (1 << 23) ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
     const int64_t steps = (M + 63) / 64;
     const auto tiles = [&](int64_t bm, int64_t bn) {
         return std::max<int64_t>((groups > 1 ? S / bm + groups : (S + bm - 1) / bm) * ((N + bn - 1) / bn), 1);
@@ -231,7 +241,8 @@ RowPlan row_plan(int64_t S, int32_t E, int64_t M, int64_t N) {
     }
     // an expert's last tile is half as high as the others on the average, and takes half their time
     const auto even = [&](int64_t b) { return tiles(b, b) - (groups > 1 ? groups / 2 * ((N + b - 1) / b) : 0); };
-    const Cut c = best_cut(even(128), even(256), steps, (double)S * N, false, odd(M, N));
+    const double memory = 2.0 * groups * M * N / 5.5e6;  // B at 5.5 TB/s
+    const Cut c = best_cut(even(128), even(256), steps, 0.45, memory, (double)S * N, false, odd(M, N));
     return RowPlan{0, c.wide, c.splits};
 }
 
@@ -252,7 +263,9 @@ int row_gradient_t(const GemmArgs& g, const RowPlan& plan, hipStream_t s) {
     if (g.splits > 1) {
         const int rc = plan.high ? thin(std::true_type())
                        : any ? launch(gemm_staged<Kind, F32, false, true, true>, 128, 128, 256)
-                             : launch(gemm_big<Kind, F32, Tile128, 2, false, false, true, true>, 128, 128, 256);
+                       : mid * g.splits <= 256
+                           ? launch(gemm_big<Kind, F32, Tile128, 4, false, false, true, true>, 128, 128, 256)
+                           : launch(gemm_big<Kind, F32, Tile128, 2, false, false, true, true>, 128, 128, 256);
         if (rc) return rc;
         return add_parts<D>(PartArgs{g.part, g.splits, g.S, g.N, g.S, g.C, g.ldc, 0, g.offsets, g.E}, s);
     }
@@ -266,7 +279,7 @@ int row_gradient_t(const GemmArgs& g, const RowPlan& plan, hipStream_t s) {
 // dB: the parts of an expert's rows, of 64 rows a step on the average.
 Cut grad_cut(int64_t S, int32_t E, int64_t M, int64_t N) {
     const auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b) * E; };
-    return best_cut(tiles(128), tiles(256), (S / E + 63) / 64, (double)E * M * N, true, odd(M, N));
+    return best_cut(tiles(128), tiles(256), (S / E + 63) / 64, 0.65, 0.0, (double)E * M * N, true, odd(M, N));
 }
 
 template <class Kind, class D>
