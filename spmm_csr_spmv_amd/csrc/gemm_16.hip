@@ -17,8 +17,9 @@ int launch_thin(bool once, const GemmArgs& g, hipStream_t s) {
 }
 
 // Which kernel.  Times are medians in us, M x N x K, or tokens x choices, experts, N, K, bf16, of calls that follow each
-// other in a graph, with at least 256 MB of weights in turn.  The tiles and the order of the tests are those of the int8
-// products, whose bytes a row are the same; the limits are of 16-bit rows.
+// other in a graph, with 1 GB of weights in turn, so that they come from memory (256 MB stay in the caches in part, and
+// favour other tiles).  The tiles and the order of the tests are those of the int8 products, whose bytes a row are the
+// same; the limits are of 16-bit rows.
 template <class Kind, class D, bool GATED>
 int gemm16_t(const GemmArgs& g, hipStream_t s) {
     // bn rows of B a tile
@@ -34,14 +35,12 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     const bool matrix = few && groups == 1, experts = few && groups > 1 && !any;
     const bool deep = g.K >= 2048;
     const bool once = !any && g.S <= 32 * groups;
-    // A matrix whose 128 x 128 tiles nearly fill the chip: 16 x 14336 x 4096 21.4, 16x32 25.0; 32 x 14336 x 4096 21.4, 32x64
-    // 28.7; not one row (21.9, 16x32 20.9), and not 32 tiles (16 x 4096 x 4096 21.8, 16x16 9.6).
-    if (matrix && !any && g.S >= 8 && g.S <= 128 && mid >= 88 && mid <= 256)
-        return launch(gemm_big<Kind, D, Tile128, 4, false, GATED, false>, 128, 128, 256);
-    // Few tiles: 1 x 4096 x 4096 16x16 7.9, 16x32 11.0; 16 x 4096 x 1024 4.7, 5.3; 32 x 4096 x 4096 16x32 11.4, 16x16 13.3,
-    // 32x32 13.4; 64 x 4096 x 4096 32x32 11.7, 16x32 13.7, 32x64 15.9, 128x128 24; 128 x 4096 x 4096 32x64 16.4, 32x32 16.9,
-    // 128x128 34.  Experts of few rows: 16 x 8, 64, 2048, 2048 16x32 55, 32x32 58, 128x128 68; 64 x 8 94, 91, 112; 128 x 8
-    // (16 rows) 32x32 113, 16x32 125, 128x128 120; 128 x 8, 128, 1024, 1024 (8 rows) 16x32 51, 32x32 51, 128x128 55.
+    // Few tiles: 1 x 4096 x 4096 16x16 7.7, 16x32 10.8; 16 x 4096 x 1024 4.5, 5.1; 32 x 4096 x 4096 16x32 11.0, 16x16 12.9,
+    // 32x32 13.0; 64 x 4096 x 4096 32x32 13.2, 16x32 15.7, 32x64 17.5, 128x128 31; 128 x 4096 x 4096 32x64 16.9, 32x32 19.2,
+    // 128x128 40.  Few rows of one matrix in any number: 16 x 14336 x 4096 16x32 22.2, 16x16 25.4, 128x128 30; 32 x 14336 x
+    // 4096 32x64 22.6, 32x32 25.0, 16x32 33.8, 128x128 32.  Experts of few rows: 16 x 8, 64, 2048, 2048 16x32 53, 32x32 56, 128x128
+    // 79; 64 x 8 82, 80, 106; 128 x 8 (16 rows) 32x32 104, 16x32 113, 128x128 113; 128 x 8, 128, 1024, 1024 (8 rows) 16x32 46,
+    // 32x32 48, 128x128 52.
     if (tiles(16, 32) <= 128) return launch_thin<Kind, D, 1, GATED ? 2 : 1, 8, GATED>(once, g, s);
     if (tiles(16, 32) <= 256 || (matrix && g.S <= 16) || (experts && g.S <= (deep ? 8 : 6) * groups))
         return launch_thin<Kind, D, 1, 2, 4, GATED>(once, g, s);
@@ -50,16 +49,16 @@ int gemm16_t(const GemmArgs& g, hipStream_t s) {
     if (tiles(32, 64) <= (any ? 512 : 256) || (matrix && g.S <= 32 && deep))
         return launch_thin<Kind, D, 2, 4, 4, GATED>(once, g, s);
     if (any) return launch(gemm_staged<Kind, D, GATED, false>, 128, 128, 256);
-    // One 128 x 128 tile a CU at most, or tiles that mostly wait for memory: four steps in LDS.  512 x 4096 x 4096 35, two
-    // steps 51, 256x256 87; 1024 x 4096 x 4096 39, 58, 89; 512 x 8, 64, 2048, 2048 (64 rows) 135, 165, 182; 1024 x 8 (128
-    // rows) 163, 191, 188; 512 x 2, 8, 4096, 4096 (128 rows) 85, 97, 109.
+    // One 128 x 128 tile a CU at most, or tiles that mostly wait for memory: four steps in LDS.  512 x 4096 x 4096 38, two
+    // steps 60, 256x256 98; 1024 x 4096 x 4096 40, 59, 96; 512 x 8, 64, 2048, 2048 (64 rows) 127, 153, 168; 1024 x 8 (128
+    // rows) 157, 186, 179; 512 x 2, 8, 4096, 4096 (128 rows) 84, 91, 107.
     if (mid <= 256 || (few && g.S <= (deep ? 128 : 64) * groups))
         return launch(gemm_big<Kind, D, Tile128, 4, false, GATED, false>, 128, 128, 256);
-    // Up to two 128 x 128 tiles a CU: 512 x 14336 x 4096 68, four steps 71, 256x256 82.
+    // Up to two 128 x 128 tiles a CU: 512 x 14336 x 4096 77, four steps 82, 256x256 101.
     const int64_t cols = GATED ? 2 * g.N : g.N, wide = (cols + 255) / 256 * 256, narrow = (cols + 127) / 128 * 128;
     if (mid <= 512 || (few && 5 * wide >= 6 * narrow))
         return launch(gemm_big<Kind, D, Tile128, 2, false, GATED, false>, 128, 128, 256);
-    // 1024 x 14336 x 4096 114, 128x128 136; 8192 x 8192 x 4096 428.
+    // 1024 x 14336 x 4096 113, 128x128 140; 8192 x 8192 x 4096 452, 559; 8192 x 4, 32, 2048, 1408 217, 260.
     return launch(gemm_big<Kind, D, Tile256, 2, false, GATED, false>, 256, 256, Tile256::kThreads);
 }
 

@@ -154,7 +154,7 @@ bool odd(int64_t M, int64_t N) { return M % 8 || N % 8; }
 
 // Into how many parts to cut the sums of `steps` steps of a product's tiles, and whether 256 x 256 tiles are better than
 // 128 x 128 ones: the least of an estimate in us.  A step (64 of the sum) of 128 x 128 tiles takes `one` where there is one
-// on a CU, 1.1 where there are two; of 256 x 256 ones 1.8; of 128 x 128 ones of unaligned rows 1.05 and 1.6.  All of it takes
+// on a CU (dA's, of rows from memory, 0.4 to 0.65 measured; dB's 0.65), 1.1 where there are two; of 256 x 256 ones 1.8; of 128 x 128 ones of unaligned rows 1.05 and 1.6.  All of it takes
 // `memory` at least.  Parts are `outputs` fp32 numbers each, written and read at 4 TB/s, and a launch.
 // dB (bf16, us): of 32768 rows, 1024 x 1024 in parts 106, whole 324; of 512 rows, 1024 x 4096 whole 10, in 4 parts 36; of
 // 2048 x 8 of 64 experts, 2816 x 2048 in 256 x 256 tiles 358, in 128 x 128 ones 433.
@@ -216,12 +216,13 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N
 // ---------------------------------------------------------------- launch
 // dA = dC B, M rows of B a sum.  One matrix of up to 2^23 numbers and up to 32 rows: tiles of 16 or 32 rows, whose sums are
 // cut into as many parts as give 512 workgroups; else 128 x 128 or 256 x 256 ones, in parts where best_cut says so, four
-// steps in LDS where there is a tile a CU.  bf16, us: 16 x 1024 x 4096 (rows, M, columns) thin 8.3, 128x128 10.1;
-// 16 x 2048 x 2048 8.2, 10.8; 16 x 4096 x 4096 14.9, 13.5; 16 x 14336 x 4096 32, in 8 parts 25 (4.7 TB/s of weights; two
-// steps in LDS 31), whole 84; 256 x 4096 x 4096 in 4 parts 26, whole 37.  Experts' weights take their time whatever the
-// tiles, so that parts and thin tiles only cost: 128 x 8 of 64 experts, 2816 x 2048 whole 132 to 146 (5.1 to 5.6 TB/s of
-// weights), in 4 parts 180, thin 174 to 189; rows off 16 bytes (2815 x 2047) 153, 194, 355.  4096 x 8192 x 8192 in
-// 256 x 256 tiles 435, 1.26 PFLOP/s (the library 417).
+// steps in LDS where there is a tile a CU.  bf16, weights from memory, us (rows, M, columns): 16 x 4096 x 1024 thin 8.8,
+// 128 x 128 tiles in 8 parts 11.1; 16 x 3840 x 2048 11.1, 11.7; from there on alike, and thin ones lose with more rows: 16 x
+// 14336 x 4096 29.1, 29.2 (4.0 TB/s of weights; whole 92), 32 x 28672 x 4096 53.6, 49.2; 64 x 4096 x 14336 in 2 parts 31,
+// whole 41.  Experts' weights take their time whatever the tiles, so that parts and thin tiles only cost: 128 x 8 of 64
+// experts, 2816 x 2048 whole 134 (5.5 TB/s of weights), in 2 parts 156, thin 165; 64 x 2 of 8, 4096 x 4096 49, 58, 67; rows
+// off 16 bytes (128 x 8 of 64, 2815 x 2047) 150, 168, 334.  4096 x 8192 x 8192 in 256 x 256 tiles 435, 1.26 PFLOP/s (the
+// library 417).
 struct RowPlan {
     int high;    // rows of a thin tile (16 R), or 0
     bool wide;
@@ -242,7 +243,7 @@ RowPlan row_plan(int64_t S, int32_t E, int64_t M, int64_t N) {
     // an expert's last tile is half as high as the others on the average, and takes half their time
     const auto even = [&](int64_t b) { return tiles(b, b) - (groups > 1 ? groups / 2 * ((N + b - 1) / b) : 0); };
     const double memory = 2.0 * groups * M * N / 5.5e6;  // B at 5.5 TB/s
-    const Cut c = best_cut(even(128), even(256), steps, 0.45, memory, (double)S * N, false, odd(M, N));
+    const Cut c = best_cut(even(128), even(256), steps, 0.55, memory, (double)S * N, false, odd(M, N));
     return RowPlan{0, c.wide, c.splits};
 }
 
