@@ -219,7 +219,8 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N
 // steps in LDS where there is a tile a CU.  bf16, weights from memory, us (rows, M, columns): 16 x 4096 x 1024 thin 8.8,
 // 128 x 128 tiles in 8 parts 11.1; 16 x 3840 x 2048 11.1, 11.7; from there on alike, and thin ones lose with more rows: 16 x
 // 14336 x 4096 29.1, 29.2 (4.0 TB/s of weights; whole 92), 32 x 28672 x 4096 53.6, 49.2; 64 x 4096 x 14336 in 2 parts 31,
-// whole 41.  Experts' weights take their time whatever the tiles, so that parts and thin tiles only cost: 128 x 8 of 64
+// whole 41; two tiles a CU 1536 x 6528 x 1536 in 3 parts 52 (with four steps 58), whole 58, 1536 x 16384 x 1536 103 (112),
+// 137.  Experts' weights take their time whatever the tiles, so that parts and thin tiles only cost: 128 x 8 of 64
 // experts, 2816 x 2048 whole 134 (5.5 TB/s of weights), in 2 parts 156, thin 165; 64 x 2 of 8, 4096 x 4096 49, 58, 67; rows
 // off 16 bytes (128 x 8 of 64, 2815 x 2047) 150, 168, 334.  4096 x 8192 x 8192 in 256 x 256 tiles 435, 1.26 PFLOP/s (the
 // library 417).

@@ -21,12 +21,14 @@ LARGE = [(16, 1, 0, 4400, 136, 0, "random"), (16, 1, 0, 11400, 72, 0, "random"),
          (4000, 1, 0, 40, 72, 0, "random"), (20, 1, 0, 1400, 304, 0, "random"), (28, 1, 0, 2100, 1104, 0, "random"),
          (2600, 1, 0, 136, 2600, 0, "random"), (700, 2, 5, 520, 264, 0.1, "skew"), (1500, 4, 6, 1100, 200, 0.05, "random"),
          (64, 8, 32, 704, 160, 0, "random"), (1500, 1, 3, 264, 1032, 0.1, "random"), (3000, 1, 2, 72, 136, 0, "skew")]
+# long sums of dA in parts: of experts, and of so many tiles that there are two parts' a CU
+CUTS = [(100, 2, 3, 2400, 136, 0, "random"), (1152, 1, 0, 7040, 1920, 0, "random")]
 PLACES = [(0, 0), (8, 0), (13, 5)]  # gap between rows, first element's offset
 
 
 @pytest.mark.parametrize("layout", PLACES)
 @pytest.mark.parametrize("dtype", SIXTEEN)
-@pytest.mark.parametrize("case", LARGE)
+@pytest.mark.parametrize("case", LARGE + CUTS)
 def test_products_of_every_tile(case, dtype, layout):
     say("large", case, dtype, layout)
     rng, S, A, B, offsets, token, args = products_inputs(case, dtype, layout, False, bool(case[2]))
