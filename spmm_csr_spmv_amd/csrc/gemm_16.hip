@@ -1,8 +1,9 @@
 // Products of 16-bit rows (bf16, fp16; fp32 sums) sorted by expert, over one matrix or one per expert:
 //   C = A B_e^T           rows of expert e; gated: a(A G_e^T) (A U_e^T) with B_e = [G_e; U_e]
-// in the tiles of gemm_tiles.h.  8192 x 8192 x 8192 bf16 takes 840 us, 1.31 PFLOP/s (8192 x 8192 x 4096 420; the library's
-// 680 and 367): the MFMAs fill 65 % of the cycles at 1.8 GHz, and the clock falls as they fill more (79 % at 1.72 GHz where
-// copies read the caches only), so that power bounds it.  A gated product of as many columns takes 4 % more.
+// in the tiles of gemm_tiles.h.  8192 x 8192 x 8192 bf16 takes 840 us, 1.31 PFLOP/s (8192 x 8192 x 4096 420 to 452 on
+// several cards; the library's 680 and 367): the MFMAs fill 65 % of the cycles at 1.6 to 1.8 GHz, and the clock falls as they
+// fill more (79 % at 1.72 GHz where copies read the caches only), so that power bounds it.  A gated product of as many
+// columns takes 4 % more.
 #include "gemm_tiles.h"
 
 namespace spx {

@@ -182,7 +182,7 @@ Cut best_cut(int64_t narrow_tiles, int64_t wide_tiles, int64_t steps, double one
 
 // ---------------------------------------------------------------- the gate's gradient
 // dpre[p] = [dg du] of the rows up to the last that some expert has (offsets need not ascend), rows ldd elements apart;
-// rounded to the operands' type, which the matrix cores want.  Memory bounds it: 32768 x 1408 bf16 in 75 us, 6.1 TB/s.
+// rounded to the operands' type, which the matrix cores want.  Memory bounds it: 32768 x 1408 bf16 in 75 to 84 us, 5.4 to 6.1 TB/s.
 template <class D>
 __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t S, int64_t N, int32_t E, const int32_t* offsets, int act,
                                                             const typename D::T* __restrict__ dH, int64_t ldh,
