@@ -27,12 +27,15 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
 }
 
 // The gradients of a(g) u, given its own: dg = dh u a'(g) with a' = sig + g sig (1 - sig) p', and du = dh a(g).
+// Where sig is 0 so are a and a', where it is 1 so is a': g p' may be beyond fp32's range there, and g and u Infs (sums
+// that the operands' type cannot hold), which would make NaN of a limit.
 __device__ __forceinline__ void gated_backward(float dh, float g, float u, int act, float& dg, float& du) {
 #pragma clang fp contract(off)
     const float s = gate_sig(g, act);
     const float dp = act == SP_ACT_SILU ? 1.0f : fmaf(3.0f * kGelu3, g * g, kGelu);
-    du = dh * (g * s);
-    dg = dh * u * (s * fmaf(g * dp, 1.0f - s, 1.0f));
+    const auto held = [](float v) { return fabsf(v) == __builtin_inff() ? 0.0f : v; };
+    du = dh * (s == 0.0f ? s * held(g) : g * s);
+    dg = s == 0.0f ? dh * s * held(u) : dh * u * (s == 1.0f ? s : s * fmaf(g * dp, 1.0f - s, 1.0f));
 }
 
 }  // namespace spx

@@ -1,0 +1,85 @@
+"""The norm and the gated gradient at the ends of their types' ranges on the GPU, against their definitions in 64 bits.
+
+Tolerances as in test_gpu_layer.py: u = 2^-24 is fp32's rounding, half a step of the output's type, and steps_of(H) of a sum.
+"""
+import numpy as np
+import pytest
+import torch
+
+import spmm_csr_spmv_amd as sp
+from gpu_util import say
+from test_gpu_layer import SIXTEEN, check
+from test_gpu_moe import HALF, LEAST, TYPES, U, f64, rng_for
+
+pytestmark = pytest.mark.gpu
+
+
+def tensor(a, dtype):
+    return torch.from_numpy(np.asarray(a)).to(TYPES[dtype]).cuda()
+
+
+# ------------------------------------------------------------------ gated gradient
+def saturated(g, act):
+    """a(g) and a'(g) of |g| up to the type's largest: their limits where exp(-|p|) is below 2^-1000."""
+    c = 2 * np.sqrt(2 / np.pi)
+    m = np.clip(g, -800, 800) if act == "silu" else np.clip(g, -100, 100)
+    p, dp = (m, np.ones_like(m)) if act == "silu" else (c * (m + 0.044715 * m ** 3), c * (1 + 3 * 0.044715 * m * m))
+    with np.errstate(over="ignore"):
+        sig = 1 / (1 + np.exp(-p))
+    far = np.abs(p) > 700
+    a = np.where(far, np.where(g > 0, g, 0), m * sig)
+    da = np.where(far, g > 0, sig * (1 + m * dp * (1 - sig)))
+    rough = np.where(far, da, sig * (1 + np.abs(m * dp)))  # without the cancellation in a'
+    return a, da, rough, np.where(far, 0, np.abs(p))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", SIXTEEN)
+def test_gated_backward_of_far_pre_activations(dtype, act):
+    """Up to the type's largest, where the derivative's factors leave fp32's range though the derivative does not."""
+    say("far pre-activations", dtype, act)
+    far = [2e4, 6e4] if dtype == "f16" else [1e13, 2e13, 1e14, 1.8e19, 1e20, 1e30, 3e38]
+    values = np.array([0, 0.5, 3, 9, 15, 40, 88, 90, 120, 1e3] + far)
+    values = np.concatenate([values, -values])
+    N = values.size
+    rng = rng_for("far pre", dtype, act)
+    S = 9
+    pre = tensor(np.concatenate([np.tile(values, (S, 1)), rng.standard_normal((S, N))], 1), dtype)
+    dH = tensor(rng.uniform(0.25, 0.5, (S, N)) * rng.choice([-1, 1], (S, N)), dtype)
+    one = torch.eye(2 * N, dtype=TYPES[dtype], device="cuda")
+    dA, dB = sp.moe_gated_backward(dH, pre, one[:S], one, act=act)
+    g, u, d = f64(pre)[:, :N], f64(pre)[:, N:], f64(dH)
+    a, da, rough, p = saturated(g, act)
+    want = np.concatenate([d * u * da, d * a], 1)
+    rough = np.concatenate([np.abs(d * u) * rough, np.abs(d * a)], 1)
+    # sig is off by u (4 + 4 |p|) of itself, as is 1 - sig; products with the unit matrix are exact.  Below fp32's normal
+    # range exp may be 0: at most 2^-126 times the other factors, which are below 2^8 there
+    off = rough * U * (16 + 8 * np.concatenate([p, p], 1)) + 2.0 ** -110
+    check(dA, want, off + HALF[dtype] * (np.abs(want) + off) + LEAST[dtype], (dtype, act))
+    assert torch.equal(dB.t()[:S], dA)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_gated_backward_of_pre_activations_beyond_fp16(act):
+    """A gate's sum that fp16 cannot hold is kept as an Inf; below, the product and its gradient are 0."""
+    S, N, K = 5, 8, 64
+    A = torch.full((S, K), 64.0, dtype=torch.float16, device="cuda")
+    B = torch.full((2 * N, K), 1 / 64, dtype=torch.float16, device="cuda")
+    B[:3] = -64.0  # sums of -2^18
+    B[5] = 64.0  # and 2^18
+    B[N + 5] = 2.0 ** -14
+    pre = torch.empty(S, 2 * N, dtype=torch.float16, device="cuda")
+    out = sp.moe_gated(A, B, act=act, pre=pre)
+    assert bool((pre[:, :3] == -float("inf")).all()) and bool((pre[:, 5] == float("inf")).all())
+    assert bool((out[:, :3] == 0).all())
+    dH = torch.full((S, N), 0.5, dtype=torch.float16, device="cuda")
+    for columns in (slice(0, 5), slice(6, 8)):
+        rows = list(range(N))[columns] + list(range(N, 2 * N))[columns]
+        dA, dB = sp.moe_gated_backward(dH[:, columns].contiguous(), pre[:, rows].contiguous(), A, B[rows].contiguous(), act=act)
+        assert bool(torch.isfinite(dA).all()) and bool(torch.isfinite(dB).all())
+        if columns.start == 0:
+            assert not dB[:3].any() and not dB[5:8].any()
+    # a'(Inf) = 1: the gate's own gradient is dH u
+    dP = sp.moe_gated_backward(dH[:, 5:6].contiguous(), pre[:, [5, 13]].contiguous(), torch.ones(S, 1, dtype=torch.float16, device="cuda"),
+                               torch.ones(2, 1, dtype=torch.float16, device="cuda"), act=act, dA=None)[1]
+    assert float(dP[0, 0]) == S * 0.5 * float(pre[0, 13]) and float(dP[1, 0]) == float("inf")
