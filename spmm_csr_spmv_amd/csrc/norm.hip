@@ -49,7 +49,7 @@ struct NormArgs {
 
 __host__ __device__ constexpr int64_t part_stride(int64_t n) { return (n + 3) / 4 * 4; }
 
-// The TPR lanes that share a row reduce two values at a time, in a fixed order, every lane getting both results.
+// The TPR lanes that share a row reduce one or two values at a time, in a fixed order, every lane getting both results.
 // Two places in LDS take turns, so that one barrier a call suffices.
 template <int TPR>
 struct Across {
@@ -91,6 +91,18 @@ struct Across {
             __syncthreads();
             a = waves(p[0], f);
             b = waves(p[1], g);
+        }
+    }
+    // One value.
+    template <class F>
+    __device__ __forceinline__ void operator()(float& a, F f) {
+        a = wave(a, f);
+        if (kWaves > 1) {
+            auto& p = part[turn];
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) p[0][threadIdx.x >> 6] = a;
+            __syncthreads();
+            a = waves(p[0], f);
         }
     }
 };
@@ -193,7 +205,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
         if (row + step < g.rows) hold(next, row + step);
         T* sum = g.sum ? (T*)g.sum + row * g.lds : nullptr;
         const T* stored = sum ? sum : (const T*)g.X + row * g.ldx;
-        float held[kHeld][N];  // s w
+        float held[kHeld][N];  // s, for codes s w
         float ss = 0.0f, most = 0.0f;
         const auto sums = [&](const float (&s)[N], const float (&t)[N]) {
 #pragma unroll
@@ -202,8 +214,14 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 if (I8) most = Most()(fabsf(t[i]), most);
             }
         };
-        // s of chunk c, formed and stored; t: its weights, then s w
-        const auto first = [&](int64_t c, V v, V q, float (&t)[N]) {
+        const auto reduce = [&] {
+            if constexpr (I8)
+                across(ss, most, Add(), Most());
+            else
+                across(ss, Add());
+        };
+        // s of chunk c, formed and stored; u: its weights; t: s, for codes s w
+        const auto first = [&](int64_t c, V v, V q, const float (&u)[N], float (&t)[N]) {
             const int64_t k = c * N, len = g.H - k;
             if (g.R) {
 #pragma unroll
@@ -214,11 +232,11 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 s[i] = D::up(v[i]);
-                t[i] *= s[i];
+                t[i] = I8 ? s[i] * u[i] : s[i];
             }
             sums(s, t);
         };
-        // s w of chunk c times f, from the stored sum
+        // s f and s f w of chunk c, from the stored sum
         const auto again = [&](int64_t c, float f, float (&s)[N], float (&t)[N]) {
             const int64_t k = c * N, len = g.H - k;
             const V v = chunk_load(stored + k, len);
@@ -231,18 +249,14 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
         };
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
-            if (lane + h * TPR < chunks) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) held[h][i] = w[h][i];
-                first(lane + h * TPR, now.x[h], now.r[h], held[h]);
-            }
+            if (lane + h * TPR < chunks) first(lane + h * TPR, now.x[h], now.r[h], w[h], held[h]);
         for (int64_t c = lane + kHeld * TPR; c < chunks; c += TPR) {
-            float t[N];
+            float u[N], t[N];
             const V v = load(g.X, g.ldx, row, c);
-            weights_at<W, N>(g.weight, c * N, g.H - c * N, t);
-            first(c, v, g.R ? load(g.R, g.ldr, row, c) : v, t);
+            if (I8) weights_at<W, N>(g.weight, c * N, g.H - c * N, u);
+            first(c, v, g.R ? load(g.R, g.ldr, row, c) : v, u, t);
         }
-        across(ss, most, Add(), Most());
+        reduce();
         float f = range_factor(ss, g.eps);
         if (I8 && !(most < 0x1p120f)) f = 0x1p-96f;
         if (f != 1.0f) {  // rare: the same for all lanes of the row
@@ -252,7 +266,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 again(c, f, s, t);
                 sums(s, t);
             }
-            across(ss, most, Add(), Most());
+            reduce();
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
         float top = 1.0f, by = 1.0f;
@@ -265,13 +279,13 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             by = 1.0f / top;
             if (lane == 0) g.scale[row] = live ? a / 127.0f : a < kTiny ? 0.0f : __builtin_nanf("");
         }
-        // chunk c of the result, t times `times` (or its codes)
-        const auto out = [&](int64_t c, const float (&t)[N], float times) {
+        // chunk c of the result: t, or its codes
+        const auto out = [&](int64_t c, const float (&t)[N]) {
             const int64_t k = c * N, len = g.H - k;
             if constexpr (!I8) {
                 V o;
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = D::down(t[i] * times);
+                for (int i = 0; i < N; ++i) o[i] = D::down(t[i]);
                 norm_store<T, LINES>((T*)g.Y + row * g.ldy + k, len, o);
             } else {
                 // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits;
@@ -304,16 +318,22 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 }
             }
         };
-        const bool plain = f == 1.0f;
-        // scaled rows: s i first, as s w may be out of range where s i w is not
-        const float before = plain ? 1.0f : I8 ? f : inv, times = plain ? inv : 1.0f;
+        // 1 / rms comes before the weight: s w may be out of range where s i w is not.  The codes of rows in range are
+        // those of s w.
+        const bool whole = !I8 || f == 1.0f;
+        const float before = !I8 ? inv : f;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
-            if (plain && lane + h * TPR < chunks) out(lane + h * TPR, held[h], inv);
-        for (int64_t c = lane + (plain ? kHeld * TPR : 0); c < chunks; c += TPR) {
+            if (whole && lane + h * TPR < chunks) {
+                if constexpr (!I8)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) held[h][i] = held[h][i] * inv * w[h][i];
+                out(lane + h * TPR, held[h]);
+            }
+        for (int64_t c = lane + (whole ? kHeld * TPR : 0); c < chunks; c += TPR) {
             float s[N], t[N];
             again(c, before, s, t);
-            out(c, t, times);
+            out(c, t);
         }
     }
 }

@@ -8,10 +8,12 @@ import torch
 
 import spmm_csr_spmv_amd as sp
 from gpu_util import say
-from test_gpu_layer import SIXTEEN, check
+from test_gpu_layer import SIXTEEN, check, norm_ref, steps_of
 from test_gpu_moe import HALF, LEAST, TYPES, U, f64, rng_for
 
 pytestmark = pytest.mark.gpu
+
+LENGTHS = [40, 600, 2500, 9001]
 
 
 def tensor(a, dtype):
@@ -83,3 +85,25 @@ def test_gated_backward_of_pre_activations_beyond_fp16(act):
     dP = sp.moe_gated_backward(dH[:, 5:6].contiguous(), pre[:, [5, 13]].contiguous(), torch.ones(S, 1, dtype=torch.float16, device="cuda"),
                                torch.ones(2, 1, dtype=torch.float16, device="cuda"), act=act, dA=None)[1]
     assert float(dP[0, 0]) == S * 0.5 * float(pre[0, 13]) and float(dP[1, 0]) == float("inf")
+
+
+# ------------------------------------------------------------------ norm
+def weights_of(rng, H, scale):
+    return tensor((1 + 0.2 * rng.standard_normal(H)) * scale, "f32")
+
+
+def check_norm(x, w, eps, dtype, what):
+    s64, w64, i = norm_ref(x, w, eps)
+    y = s64 * i * w64
+    check(sp.rms_norm(x, w, eps=eps), y, np.abs(y) * (HALF[dtype] + (0.5 * steps_of(x.shape[1]) + 8) * U) + LEAST[dtype], what)
+
+
+@pytest.mark.parametrize("H", LENGTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_large_rows_under_large_weights(dtype, H):
+    """s weight leaves the range, the norm does not."""
+    say("norm, large rows and weights", dtype, H)
+    rng = rng_for("large", dtype, H)
+    x = tensor(rng.standard_normal((5, H)) * np.array([2.0 ** 55, 1, 2.0 ** 100, 2.0 ** -40, 2.0 ** 57])[:, None], dtype)
+    for scale in (2.0 ** 75, 2.0 ** 110, 2.0 ** -100):
+        check_norm(x, weights_of(rng, H, scale), 1e-6, dtype, (dtype, H, scale))
