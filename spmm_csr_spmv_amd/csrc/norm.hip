@@ -257,23 +257,38 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             first(c, v, g.R ? load(g.R, g.ldr, row, c) : v, u, t);
         }
         reduce();
-        float f = range_factor(ss, g.eps);
-        if (I8 && !(most < 0x1p120f)) f = 0x1p-96f;
+        const float f = range_factor(ss, g.eps);
         if (f != 1.0f) {  // rare: the same for all lanes of the row
-            ss = most = 0.0f;
+            ss = 0.0f;
             for (int64_t c = lane; c < chunks; c += TPR) {
                 float s[N], t[N];
                 again(c, f, s, t);
-                sums(s, t);
+#pragma unroll
+                for (int i = 0; i < N; ++i) ss = fmaf(s[i], s[i], ss);
             }
-            reduce();
+            across(ss, Add());
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
-        float top = 1.0f, by = 1.0f;
+        // The codes are those of s w, as the row's i cancels, or of s i w where s w may be out of range.
+        const bool ranged = f == 1.0f && most < 0x1p120f;
+        float before = I8 ? 1.0f : inv, top = 1.0f, by = 1.0f;
         bool live = false;
         if constexpr (I8) {
-            // the codes are those of t = s w f: the row's factor cancels
-            const float a = most * unit;
+            float a = most * unit;
+            if (!ranged) {  // rare as well
+                most = 0.0f;
+                for (int64_t c = lane; c < chunks; c += TPR) {
+                    float s[N], t[N];
+                    again(c, inv, s, t);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) most = Most()(fabsf(t[i]), most);
+                }
+                across(most, Most());
+                a = most;
+                const float down = most < 0x1p120f ? 1.0f : 0x1p-8f;  // 127 times a value stays in range
+                before = inv * down;
+                most *= down;
+            }
             live = a >= kTiny && a < __builtin_inff();
             top = live ? most : 1.0f;
             by = 1.0f / top;
@@ -318,10 +333,8 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 }
             }
         };
-        // 1 / rms comes before the weight: s w may be out of range where s i w is not.  The codes of rows in range are
-        // those of s w.
-        const bool whole = !I8 || f == 1.0f;
-        const float before = !I8 ? inv : f;
+        // 1 / rms comes before the weight: s w may be out of range where s i w is not
+        const bool whole = !I8 || ranged;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
             if (whole && lane + h * TPR < chunks) {

@@ -9,7 +9,7 @@ import torch
 import spmm_csr_spmv_amd as sp
 from gpu_util import say
 from test_gpu_layer import SIXTEEN, check, norm_ref, steps_of
-from test_gpu_moe import HALF, LEAST, TYPES, U, f64, rng_for
+from test_gpu_moe import HALF, LEAST, TYPES, U, f64, i64, rng_for
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,28 @@ def test_norm_of_large_rows_under_large_weights(dtype, H):
     x = tensor(rng.standard_normal((5, H)) * np.array([2.0 ** 55, 1, 2.0 ** 100, 2.0 ** -40, 2.0 ** 57])[:, None], dtype)
     for scale in (2.0 ** 75, 2.0 ** 110, 2.0 ** -100):
         check_norm(x, weights_of(rng, H, scale), 1e-6, dtype, (dtype, H, scale))
+
+
+def check_codes(x, w, eps, what):
+    """The codes are those of y = s i weight: four roundings and a sum's, a quotient and a product, then half a code."""
+    say("norm int8", what)
+    q, scale = sp.rms_norm_i8(x, w, eps=eps)
+    s64, w64, i = norm_ref(x, w, eps)
+    y = s64 * i * w64
+    a = np.abs(y).max(1)
+    off = (0.5 * steps_of(x.shape[1]) + 10) * U
+    assert (np.abs(f64(scale) * 127 / a - 1) <= off).all(), (what, f64(scale), a / 127)
+    # a row's i is in all its values alike
+    assert (np.abs(i64(q) - 127 * y / a[:, None]) <= 0.5 + 127 * 8 * U).all(), what
+
+
+@pytest.mark.parametrize("H", LENGTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_into_int8_under_large_weights(dtype, H):
+    """s weight is beyond 2^120 where the sum of squares is an ordinary one, and the other way round."""
+    rng = rng_for("codes, large", dtype, H)
+    x = tensor(rng.standard_normal((5, H)) * np.array([1, 2.0 ** 55, 2.0 ** -20, 2.0 ** 100, 30])[:, None], dtype)
+    for scale in (2.0 ** 119, 2.0 ** 121, 2.0 ** 123, 2.0 ** 75, 2.0 ** -60):
+        check_codes(x, weights_of(rng, H, scale), 1e-6 if scale > 1e36 else 0.0, (dtype, H, scale))
+    y, scale = sp.rms_norm_i8(torch.ones(3, H, device="cuda"), torch.full((H,), 2.0 ** 121, device="cuda"), eps=0.0)
+    assert bool((y == 127).all()) and torch.allclose(scale, torch.full_like(scale, 2.0 ** 121 / 127), rtol=4 * U)
