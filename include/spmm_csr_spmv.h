@@ -718,7 +718,8 @@ int moe_gated_backward(int64_t S, int32_t num_experts, int64_t N, int64_t K, int
  *
  * rms_norm_i8: Y as int8 codes q with a scale per row, as quantize_rows_i8 makes them of the
  * unrounded Y (same rules for tiny rows, Inf and NaN, same layout): what gemm_i8, gated_i8 and
- * moe_gated_i8 read.  The codes are those of s weight (rounded to fp32), from which Y differs by the row's i.
+ * moe_gated_i8 read.  The codes are those of s weight (rounded to fp32), from which Y differs by the row's i,
+ * and those of Y itself where a row's largest s weight is not between 2^-100 and 2^120.
  *
  * rms_norm_backward: from dY and the stored sum (X without a residual), with n = s i:
  *   dX = i (dY weight - n mean(dY weight n)) + dsum    (dsum, the sum's own gradient, may be NULL)

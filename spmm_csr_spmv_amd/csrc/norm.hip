@@ -267,15 +267,17 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 for (int i = 0; i < N; ++i) ss = fmaf(s[i], s[i], ss);
             }
             across(ss, Add());
+            most = __builtin_nanf("");
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
-        // The codes are those of s w, as the row's i cancels, or of s i w where s w may be out of range.
-        const bool ranged = f == 1.0f && most < 0x1p120f;
         float before = I8 ? 1.0f : inv, top = 1.0f, by = 1.0f;
-        bool live = false;
+        bool whole = true, live = false;  // whole: what is held is what the results are made of
         if constexpr (I8) {
+            // The codes are those of s w, as the row's i cancels, or of s i w where s w may be out of range: beyond it, or
+            // so far below that its bits or its reciprocal are lost though the scale is not 0 (s w is off by 2^-150 then).
             float a = most * unit;
-            if (!ranged) {  // rare as well
+            const uint32_t low = __float_as_uint(0x1p-100f), high = __float_as_uint(0x1p120f);
+            if (__float_as_uint(most) - low >= high - low && !((most + 0x1p-149f) * unit < 0.5f * kTiny)) {  // rare as well
                 most = 0.0f;
                 for (int64_t c = lane; c < chunks; c += TPR) {
                     float s[N], t[N];
@@ -288,6 +290,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 const float down = most < 0x1p120f ? 1.0f : 0x1p-8f;  // 127 times a value stays in range
                 before = inv * down;
                 most *= down;
+                whole = false;
             }
             live = a >= kTiny && a < __builtin_inff();
             top = live ? most : 1.0f;
@@ -334,7 +337,6 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             }
         };
         // 1 / rms comes before the weight: s w may be out of range where s i w is not
-        const bool whole = !I8 || ranged;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
             if (whole && lane + h * TPR < chunks) {

@@ -110,16 +110,18 @@ def test_norm_of_large_rows_under_large_weights(dtype, H):
 
 
 def check_codes(x, w, eps, what):
-    """The codes are those of y = s i weight: four roundings and a sum's, a quotient and a product, then half a code."""
+    """The codes are those of y = s i weight: four roundings and a sum's, a quotient and a product, then half a code; a row
+    below 2^-119 is zeros."""
     say("norm int8", what)
     q, scale = sp.rms_norm_i8(x, w, eps=eps)
     s64, w64, i = norm_ref(x, w, eps)
     y = s64 * i * w64
     a = np.abs(y).max(1)
     off = (0.5 * steps_of(x.shape[1]) + 10) * U
-    assert (np.abs(f64(scale) * 127 / a - 1) <= off).all(), (what, f64(scale), a / 127)
+    live = a >= 2.0 ** -119
+    assert (np.abs(f64(scale) - np.where(live, a / 127, 0)) <= off * a / 127).all(), (what, f64(scale), a / 127)
     # a row's i is in all its values alike
-    assert (np.abs(i64(q) - 127 * y / a[:, None]) <= 0.5 + 127 * 8 * U).all(), what
+    assert (np.abs(i64(q) - 127 * y / np.where(live, a, np.inf)[:, None]) <= np.where(live, 0.5 + 127 * 8 * U, 0)[:, None]).all(), what
 
 
 @pytest.mark.parametrize("H", LENGTHS)
@@ -132,3 +134,19 @@ def test_norm_into_int8_under_large_weights(dtype, H):
         check_codes(x, weights_of(rng, H, scale), 1e-6 if scale > 1e36 else 0.0, (dtype, H, scale))
     y, scale = sp.rms_norm_i8(torch.ones(3, H, device="cuda"), torch.full((H,), 2.0 ** 121, device="cuda"), eps=0.0)
     assert bool((y == 127).all()) and torch.allclose(scale, torch.full_like(scale, 2.0 ** 121 / 127), rtol=4 * U)
+
+
+@pytest.mark.parametrize("H", LENGTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_into_int8_of_tiny_rows(dtype, H):
+    """s weight is below fp32's normal range, or its reciprocal above it; the norm is ordinary."""
+    rng = rng_for("codes, tiny", dtype, H)
+    base = rng.uniform(1, 2, (4, H)) * rng.choice([-1, 1], (4, H))
+    for eps, size, scale in ((1e-6, 9e-40, 1), (1e-12, 9e-40, 1), (1e-12, 2.0 ** -135, 1), (1e-9, 4e-39, 1), (1e-6, 1e-10, 2.0 ** -95),
+                             (1e-6, 2.0 ** -60, 2.0 ** -66)):
+        check_codes(tensor(base * size, dtype), tensor(rng.uniform(0.9, 1.1, H) * scale, "f32"), eps, (dtype, H, eps, size, scale))
+    x = tensor(base, dtype)
+    x[1] = 0
+    x[2] = tensor(base[2] * 1e-38, dtype)
+    q, scale = sp.rms_norm_i8(x, eps=1.0)  # a row whose scale would be denormal is zeros
+    assert not scale[1:3].any() and not q[1:3].any() and bool((scale[[0, 3]] > 0).all())
