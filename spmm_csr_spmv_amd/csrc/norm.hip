@@ -9,7 +9,7 @@
 // A row's lanes hold it in registers between the sums and the results, so that each
 // byte is read and written once; longer rows are read again (from L2).  Sums are fp32, added
 // across lanes in a fixed order.  Squares beyond fp32's range: a row whose sum of squares is
-// not below 2^120 (or, with an eps near zero, not above 2^-60) is summed again scaled by 2^-96 (2^96).
+// not below 2^120 (or, with an eps near zero, not above 2^-60) is summed again scaled by 2^-96 (2^92).
 //
 // Memory bounds all of it from some thousand rows on: 16384 x 4096 bf16 with a residual in 92 us (5.8 TB/s, half of
 // it writes), without 46, into int8 with a residual 78 (6.0), the gradient with the sum's own 92; rows that share lines with
@@ -114,9 +114,10 @@ struct Most {
     __device__ __forceinline__ float operator()(float a, float b) const { return a >= b || a != a ? a : b; }
 };
 
-// The factor that brings a row's sum of squares into range; 1 where it is there.
+// The factor that brings a row's sum of squares into range; 1 where it is there.  2^-60 becomes 2^124, and a row whose
+// largest value is 2^-126 2^-68.
 __device__ __forceinline__ float range_factor(float ss, float eps) {
-    return !(ss < 0x1p120f) ? 0x1p-96f : ss < 0x1p-60f && eps < 0x1p-100f ? 0x1p96f : 1.0f;
+    return !(ss < 0x1p120f) ? 0x1p-96f : ss < 0x1p-60f && eps < 0x1p-100f ? 0x1p92f : 1.0f;
 }
 // i / f for a sum of squares of values that were multiplied by f.
 __device__ __forceinline__ float inverse_rms(float ss, float H, float eps, float f) {

@@ -8,7 +8,7 @@ import torch
 
 import spmm_csr_spmv_amd as sp
 from gpu_util import say
-from test_gpu_layer import SIXTEEN, check, norm_ref, steps_of
+from test_gpu_layer import SIXTEEN, check, norm_backward_ref, norm_ref, steps_of
 from test_gpu_moe import HALF, LEAST, TYPES, U, f64, i64, rng_for
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +150,21 @@ def test_norm_into_int8_of_tiny_rows(dtype, H):
     x[2] = tensor(base[2] * 1e-38, dtype)
     q, scale = sp.rms_norm_i8(x, eps=1.0)  # a row whose scale would be denormal is zeros
     assert not scale[1:3].any() and not q[1:3].any() and bool((scale[[0, 3]] > 0).all())
+
+
+@pytest.mark.parametrize("H", LENGTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_small_rows_without_eps(dtype, H):
+    """Sums of squares on both sides of where a row is summed again from scaled values."""
+    rng = rng_for("small", dtype, H)
+    logs = np.array([-50, -59.5, -60.5, -61, -62, -63, -63.9, -64.5, -66, -80, -120, -200])  # of the sum of squares
+    x = rng.standard_normal((logs.size, H))
+    x = tensor(x * np.sqrt(2.0 ** logs / (x * x).sum(1))[:, None], dtype)
+    w, dy = weights_of(rng, H, 1), tensor(rng.standard_normal(x.shape), dtype)
+    for eps in (0.0, 1e-35):
+        check_norm(x, w, eps, dtype, (dtype, H, eps))
+        check_codes(x, w, eps, (dtype, H, eps))
+        dx, dw = sp.rms_norm_backward(dy, x, w, eps=eps)
+        d, bound, dwr, dwb = norm_backward_ref(x, w, dy, None, dtype, eps)
+        check(dx, d, bound, (dtype, H, eps))
+        check(dw, dwr, dwb, (dtype, H, eps))
