@@ -723,7 +723,7 @@ int moe_gated_backward(int64_t S, int32_t num_experts, int64_t N, int64_t K, int
  *
  * rms_norm_backward: from dY and the stored sum (X without a residual), with n = s i:
  *   dX = i (dY weight - n mean(dY weight n)) + dsum    (dsum, the sum's own gradient, may be NULL)
- * the gradient of X and of residual alike, in fp32, rounded once; and dweight[h] = sum over rows of
+ * the gradient of X and of residual alike, in fp32 (dY weight has to fit), rounded once; and dweight[h] = sum over rows of
  * dY n (H fp32 values, in a fixed order; NULL: not wanted; zeros when rows is 0).  work: as
  * rms_norm_backward_bufsize() says where dweight is wanted, 16-byte aligned; calls that share it must not overlap.
  *

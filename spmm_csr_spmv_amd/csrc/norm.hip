@@ -398,7 +398,7 @@ __global__ __launch_bounds__(kThreads<TPR>, 3) void rms_norm_backward_kernel(Nor
     for (; row < g.rows; row += step) {
         const Held now = next;
         if (PARTS && row + step < g.rows) hold(next, row + step);
-        float ss = 0.0f, dot = 0.0f;  // of s^2 and of dn s
+        float ss = 0.0f, dot = 0.0f;  // of (s f)^2 and of dn s f
         const auto sums = [&](const V& vx, const V& vy, const float (&u)[N], float f) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -407,8 +407,8 @@ __global__ __launch_bounds__(kThreads<TPR>, 3) void rms_norm_backward_kernel(Nor
                 dot = fmaf(D::up(vy[i]) * u[i], s, dot);
             }
         };
-        const auto rest = [&](int64_t from, float f) {
-            for (int64_t c = from; c < chunks; c += TPR) {
+        const auto rest = [&](float f) {
+            for (int64_t c = lane; c < chunks; c += TPR) {
                 float u[N];
                 weights(c, u);
                 sums(chunk_load(at(g.X, g.ldx, row, c), g.H - c * N), chunk_load(at(g.dY, g.lddy, row, c), g.H - c * N), u, f);
@@ -419,17 +419,25 @@ __global__ __launch_bounds__(kThreads<TPR>, 3) void rms_norm_backward_kernel(Nor
             for (int h = 0; h < (PARTS ? kHeld : 1); ++h)
                 if (lane + h * TPR < chunks) sums(now.x[h], now.y[h], w[h], 1.0f);
         } else {
-            rest(lane, 1.0f);
+            rest(1.0f);
         }
         across(ss, dot, Add(), Add());
         const float f = range_factor(ss, g.eps);
-        if (f != 1.0f) {
-            ss = dot = 0.0f;
-            rest(lane, f);
-            across(ss, dot, Add(), Add());
+        const bool ranged = f == 1.0f && fabsf(dot) < 0x1p120f;
+        if (!ranged) {  // rare: dn s may be out of range where dn n is not
+            if (f != 1.0f) {
+                ss = 0.0f;
+                rest(f);
+                across(ss, Add());
+            }
+            const float all = ss;
+            dot = 0.0f;
+            rest(inverse_rms(ss, (float)g.H, g.eps, f) * f);
+            across(dot, Add());
+            ss = all;
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
-        const float mean = dot * unit / (float)g.H;  // of dn n
+        const float mean = dot * (ranged ? unit : 1.0f) / (float)g.H;  // of dn n
         if (!PARTS && g.rstd && lane == 0) g.rstd[row] = inv;
         const auto out = [&](int64_t c, const V& vx, const V& vy, const V& vd, const float (&u)[N], float (&sum)[N]) {
             V o;

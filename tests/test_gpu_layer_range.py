@@ -168,3 +168,17 @@ def test_norm_of_small_rows_without_eps(dtype, H):
         d, bound, dwr, dwb = norm_backward_ref(x, w, dy, None, dtype, eps)
         check(dx, d, bound, (dtype, H, eps))
         check(dw, dwr, dwb, (dtype, H, eps))
+
+
+@pytest.mark.parametrize("H", LENGTHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_backward_of_large_rows(dtype, H):
+    """dy weight s leaves the range, and so does its sum; the gradient does not."""
+    rng = rng_for("large gradient", dtype, H)
+    s = tensor(rng.standard_normal((5, H)) * np.array([2.0 ** 55, 1, 2.0 ** 57, 2.0 ** 30, 2.0 ** 100])[:, None], dtype)
+    dy = tensor(rng.standard_normal((5, H)) * np.array([2.0 ** 75, 2.0 ** 100, 2.0 ** 80, 2.0 ** 112, 2.0 ** 60])[:, None], dtype)
+    w = weights_of(rng, H, 1)
+    dx, dw = sp.rms_norm_backward(dy, s, w, eps=1e-6)
+    want, bound, dwr, dwb = norm_backward_ref(s, w, dy, None, dtype, 1e-6)
+    check(dx, want, bound, (dtype, H))
+    check(dw, dwr, dwb, (dtype, H))
