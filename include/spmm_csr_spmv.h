@@ -673,8 +673,9 @@ int moe_gated_i8(int64_t S, int32_t num_experts, int64_t N, int64_t K, const int
  * moe_gemm_backward: from dC (S x N): dA[p] = sum_n dC[p, n] B[e, n] (S x K, by sorted row: with
  * sources, moe_combine adds up a token's) and dB[e] = sum over e's rows p of dC[p]^T A[r] (N x K a
  * matrix, zeros for an expert without rows).  Either may be NULL and is then not formed (nor is B, or
- * A, read).  dA has a row for every p below offsets[num_experts]; rows behind keep their contents.
- * A row whose source is outside [0, a_rows) counts as a row of zeros in dB.
+ * A, read).  dA has a row for every p that an expert has; other rows keep their contents.
+ * A row whose source is outside [0, a_rows) (without sources: a row from a_rows on) counts as a row of zeros in
+ * dB, whatever dC (dH and pre) hold there.
  *
  * moe_gated_backward: the same from dH (S x N) and pre (S x 2 N, as moe_gated left it):
  * dpre = [dH u a'(g)  dH a(g)], formed in fp32 and rounded to dtype for the matrix cores; dA and dB

@@ -18,6 +18,7 @@ struct GradArgs {
     int64_t q_rows, ldq;
     const int32_t* src;       // or NULL: row p goes with row p of A
     FastDiv slots;
+    uint32_t sources;         // slots of A's rows, 2^31 at most
     const int32_t* offsets;   // or NULL: one matrix, rows 0 .. S
     int32_t E;
     void* C;                  // dB, rows ldc and experts stridec elements apart
@@ -44,7 +45,10 @@ __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uin
     a = __builtin_amdgcn_readfirstlane(a);
     b = __builtin_amdgcn_readfirstlane(b);
     const int each = (int)(((uint32_t)(b - a) + g.splits * 64u - 1) / (g.splits * 64u)) * 64;
-    const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b), rows = min(each, b - from);
+    const int from = (int)min((int64_t)a + (int64_t)split * each, (int64_t)b);
+    int rows = min(each, b - from);
+    // A row of dC whose row of A is not there counts as zeros too: what it holds may be an Inf or a NaN.
+    if (!GATHER) rows = (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0);
     for (int i = tid; i < X::kSize; i += X::kThreads) lrow[i] = m0 + i < g.M ? 0 : -1;
     BigTransposed<X, false> sa;
     BigTransposed<X, GATHER> sb;
@@ -53,18 +57,24 @@ __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uin
         sb.template place<STAGED>(g.Q, g.ldq, rows, n0, g.N, w, l);
         sb.src = rows > 0 ? g.src + from : reinterpret_cast<const int32_t*>(big_zeros);
         sb.slots = g.slots;
-        sb.a_rows = g.q_rows;
+        sb.sources = g.sources;
     } else {
-        sb.template place<STAGED>(g.Q + from * g.ldq, g.ldq, (int)max(min((int64_t)rows, g.q_rows - from), (int64_t)0), n0,
-                                  g.N, w, l);
+        sb.template place<STAGED>(g.Q + from * g.ldq, g.ldq, rows, n0, g.N, w, l);
     }
     constexpr int F = X::CB;
     typename Kind::S16 acc[F][X::U];
     const int steps = (rows + 63) >> 6;
-    if constexpr (STAGED)
-        staged_sums<Kind, F, true, true>(acc, m, sa, sb, steps, w, l);
+    static_assert(BigShape<X, F>::kA == BigShape<X, F>::kB, "a step's copies of dC come after the fetch of its sources");
+    const auto sums = [&](const auto& p) {
+        if constexpr (STAGED)
+            staged_sums<Kind, F, true, true>(acc, m, p, sb, steps, w, l);
+        else
+            big_sums<Kind, X, 2, F, true, true, false>(acc, m, p, sb, steps, kBigK, tid, w, l);
+    };
+    if constexpr (GATHER)
+        sums(BigPartner<X>{sa, sb});
     else
-        big_sums<Kind, X, 2, F, true, true, false>(acc, m, sa, sb, steps, kBigK, tid, w, l);
+        sums(sa);
     BigOut o{(typename D::T*)g.C + e * g.stridec, g.ldc, g.N, m0, n0, nullptr, 0, 0};
     if (PART) o.C = g.part + ((int64_t)split * g.E + e) * g.M * g.N, o.ldc = g.N;
     const float* none = nullptr;
@@ -333,7 +343,8 @@ int product_backward(const Products& p, int64_t M, const void* dC, int64_t ldc, 
     }
     if (dB && M > 0 && p.K > 0) {
         GradArgs g{p.S, M, p.K, (const int8_t*)dC, 2 * ldc, (const int8_t*)p.A, p.a_rows, 2 * p.lda, p.src,
-                   FastDiv::by(p.slots), p.offsets, p.E, dB, lddb, stridedb, part, grad_cut(p.S, p.E, M, p.K).splits};
+                   FastDiv::by(p.slots), (uint32_t)std::min<int64_t>(p.a_rows * p.slots, (int64_t)1 << 31), p.offsets, p.E,
+                   dB, lddb, stridedb, part, grad_cut(p.S, p.E, M, p.K).splits};
         return by_type(p.dtype, [&](auto k, auto d) { return rows_sum_t<decltype(k), decltype(d)>(g, s); });
     }
     return SP_OK;
