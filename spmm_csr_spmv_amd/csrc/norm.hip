@@ -640,9 +640,10 @@ int rms_norm_backward_device(const NormRows& n, const void* dY, int64_t lddy, vo
             } else if constexpr (L == kMostBackward && !kLines) {
                 hipLaunchKernelGGL((rms_norm_backward_kernel<D, W, L, false, false>),
                                    dim3((unsigned)std::min<int64_t>(g.rows, kMostGroups)), dim3(kThreads<L>), 0, s, g);
-                if (g.rstd && hipGetLastError() == hipSuccess)
-                    hipLaunchKernelGGL((norm_columns_kernel<D>), dim3((unsigned)((g.H + 255) / 256), (unsigned)parts),
-                                       dim3(256), 0, s, g, each);
+                const int rc = status(hipGetLastError());
+                if (rc || !g.rstd) return rc;
+                hipLaunchKernelGGL((norm_columns_kernel<D>), dim3((unsigned)((g.H + 255) / 256), (unsigned)parts), dim3(256), 0, s,
+                                   g, each);
             }
             return status(hipGetLastError());
         });
