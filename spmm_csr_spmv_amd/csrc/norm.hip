@@ -124,6 +124,14 @@ __device__ __forceinline__ float inverse_rms(float ss, float H, float eps, float
     return 1.0f / sqrtf(ss / fmaxf(H, 1.0f) + eps * f * f);
 }
 
+// v rounded to D's type; to fp16 on its own, as the compiler fuses a product with the rounding of some of a lane's values
+// only (to fp32 and bf16 it cannot).
+template <class D>
+__device__ __forceinline__ typename D::T rounded(float v) {
+    if constexpr (std::is_same<D, F16>::value) return round_alone<D>(v);
+    return D::down(v);
+}
+
 // N weights from column k on, len of them inside the row.
 template <class W, int N>
 __device__ __forceinline__ void weights_at(const void* weight, int64_t k, int64_t len, float (&w)[N]) {
@@ -226,7 +234,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             const int64_t k = c * N, len = g.H - k;
             if (g.R) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = D::down(D::up(v[i]) + D::up(q[i]));
+                for (int i = 0; i < N; ++i) v[i] = rounded<D>(D::up(v[i]) + D::up(q[i]));
             }
             if (sum) norm_store<T, LINES>(sum + k, len, v);
             float s[N];
@@ -304,7 +312,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             if constexpr (!I8) {
                 V o;
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = D::down(t[i]);
+                for (int i = 0; i < N; ++i) o[i] = rounded<D>(t[i]);
                 norm_store<T, LINES>((T*)g.Y + row * g.ldy + k, len, o);
             } else {
                 // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits;
@@ -446,7 +454,7 @@ __global__ __launch_bounds__(kThreads<TPR>, 3) void rms_norm_backward_kernel(Nor
                 const float n = D::up(vx[i]) * inv, dy = D::up(vy[i]);
                 float v = inv * fmaf(-n, mean, dy * u[i]);
                 if (g.R) v += D::up(vd[i]);
-                o[i] = D::down(v);
+                o[i] = rounded<D>(v);
                 sum[i] = fmaf(dy, n, sum[i]);
             }
             norm_store<T, LINES>((T*)g.Y + row * g.ldy + c * N, g.H - c * N, o);

@@ -182,3 +182,19 @@ def test_norm_backward_of_large_rows(dtype, H):
     want, bound, dwr, dwb = norm_backward_ref(s, w, dy, None, dtype, 1e-6)
     check(dx, want, bound, (dtype, H))
     check(dw, dwr, dwb, (dtype, H))
+
+
+@pytest.mark.parametrize("H", [8, 40, 128, 600, 2500, 9001])
+def test_equal_values_of_a_row_have_equal_norms(H):
+    """Wherever in a row a value stands, and wherever the row: one rounding to fp32, then one to fp16."""
+    say("equal values", H)
+    rows = 40000 if H < 1000 else 8000
+    v = tensor(rng_for("equal", H).standard_normal(rows), "f16")
+    x = v[:, None].expand(rows, H).contiguous()
+    beside = torch.empty(rows, H + 1, dtype=torch.float16, device="cuda")[:, :H]  # rows that do not lie on lines
+    beside.copy_(x)
+    for w in (None, torch.full((H,), 1.2345, device="cuda"), torch.full((H,), 1.2345, dtype=torch.float16, device="cuda")):
+        for call in (lambda x: sp.rms_norm(x, w, eps=1.0), lambda x: sp.rms_norm(x, w, residual=x, eps=1.0)[0],
+                     lambda x: sp.rms_norm_backward(x, x, w, eps=1.0)[0], lambda x: sp.rms_norm_backward(x, x, w, dsum=x, eps=1.0)[0]):
+            y = call(x)
+            assert torch.equal(y, y[:, :1].expand(rows, H)) and torch.equal(call(beside), y)
