@@ -308,6 +308,7 @@ struct BigShape {
 // Where a lane's copy j of a step reads a K-contiguous operand.
 template <class X>
 struct BigDirect {
+    static constexpr bool kGather = false;
     const int8_t* p[X::kCopied];
     int64_t chunk, last, K;  // chunks behind the last are read from there and masked
     __device__ __forceinline__ void fetch(int) {}
@@ -355,6 +356,7 @@ struct FastDiv {
 // behind the copies in flight.
 template <class X, bool GATHER>
 struct BigTransposed {
+    static constexpr bool kGather = GATHER;
     static constexpr int kWave = 8 / X::CB, kAll = X::W * kWave;  // rows of one copy of a wave, of all waves
     const int8_t* base;          // the lane's chunk in its row of copy 0 (GATHER: in row 0)
     const int8_t* zeros;         // read for rows that are not there
@@ -614,14 +616,17 @@ __device__ __forceinline__ void big_sums(typename Kind::S16 (&acc)[F][X::U], con
     };
     BigOps<Kind, X, F, TA, TB> x0, x1;
     constexpr int kCopies = S::kCopies, kHalf = kCopies / 2;
-    SB last = sb;
-    last.fetch(ST - 1);  // with the first step's: one wait for both
+    if constexpr (SB::kGather) {
+        SB last = sb;
+        last.fetch(ST - 1);  // with the first step's: one wait for both
+        sb.fetch(0);
+        big_copy<X, F, ONCE, 0, kCopies>(m.a[0], m.b[0], sa, sb, 0, w);
+        sb = last;
+        static_assert(ST == 2, "sources are fetched for two steps");
+    } else {
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) {
-        sb.fetch(i);
-        big_copy<X, F, ONCE, 0, kCopies>(m.a[i], m.b[i], sa, sb, i, w);
+        for (int i = 0; i < ST - 1; ++i) big_copy<X, F, ONCE, 0, kCopies>(m.a[i], m.b[i], sa, sb, i, w);
     }
-    sb = last;
     big_copy<X, F, ONCE, 0, kHalf>(m.a[ST - 1], m.b[ST - 1], sa, sb, ST - 1, w);
     big_barrier<(ST - 2) * kCopies + kHalf>();
     if (steps == 1 && left < kBigK) {
