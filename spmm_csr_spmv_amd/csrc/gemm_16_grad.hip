@@ -30,8 +30,9 @@ struct GradArgs {
 
 // Square tiles of dB, steps of 64 rows.  Where an expert has many rows and the tiles are few, its rows
 // are split and the parts' fp32 sums (PART) added afterwards in the order of the splits.
-// Matrix cores and power bound it, as they do the products: 4096 rows, 8192 x 8192 bf16 in 422 to 432 us, 1.28 PFLOP/s (the
-// library 480); 8192 x 4 of 32 experts, 2816 x 2048 420 to 431 (128 x 128 tiles 509), with sources 440.
+// Bound as the products are: 4096 rows, 8192 x 8192 bf16 in 420 to 440 us, 1.28 PFLOP/s (the library 480); 8192 x 4 of 32
+// experts, 2816 x 2048 405 to 430 (128 x 128 tiles 509), with sources 440 to 465, of rows off 16 bytes 1060.  512 x 8 of 64
+// experts, 1024 x 1024, one step a tile: 45 with sources.
 template <class Kind, class D, class X, bool STAGED, bool PART, bool GATHER>
 __device__ __forceinline__ void rows_sum_tile(const GradArgs& g, uint32_t t, uint32_t total, const BigBuffers<2>& m,
                                               int32_t* lrow, int tid, int w, int l) {

@@ -13,7 +13,8 @@
 //
 // Memory bounds all of it from some thousand rows on: 16384 x 4096 bf16 with a residual in 92 us (5.8 TB/s, half of
 // it writes), without 46, into int8 with a residual 78 (6.0), the gradient with the sum's own 92; rows that share lines with
-// their neighbours take longer (48613 x 1091 fp32 with a residual 166, 5.1 TB/s).  One row of 4096 takes 3.2 us.
+// their neighbours take longer (48613 x 1091 fp32 with a residual 166, 5.1 TB/s).  One row of 4096 takes 3.2 us.  What rows
+// out of range need (sums formed again, codes of s i w, a mean of dy w n) stands in branches that others pass by: at most 2 %.
 #include <algorithm>
 #include <type_traits>
 
@@ -542,7 +543,11 @@ __global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict
 // ---------------------------------------------------------------- launch
 int status(hipError_t e) { return e == hipSuccess ? SP_OK : SP_ERR_HIP; }
 int chunk_of(int32_t dtype) { return dtype == SP_F32 ? 4 : 8; }
-// Lanes a row: the fewest whose registers hold it, up to 1024; the gradient's, which hold more, up to 512.
+// Lanes a row: the fewest whose registers hold it, up to 1024; the gradient's, which hold more, up to 512.  us with 16, 64,
+// 256, 512 and 1024, bf16: 65536 x 128 9.8, 21, 70, 129, 274; 32768 x 1024 28, 24, 45, 75, 142; 16384 x 2048 32, 31, 26, 42, 75;
+// 8192 x 8192 71, 71, 56, 44, 64; 4096 x 16384 125, 68, 60, 57, 46; one row of 4096 18, 5.5, 3.2, 3.2, 3.3.  A row that is a
+// little longer than what some lanes hold leaves the next ones half idle: 65536 x 264 16, 23; 4096 x 8200 27 with 512, 33 with 1024.
+// The gradient: 32768 x 1024 39 with 64, 91 with 256; 16384 x 4096 76 with 256, 111 with 512.
 constexpr int kMostForward = 1024, kMostBackward = 512;
 int norm_lanes(int64_t H, int32_t dtype, int most) {
     const int64_t chunks = (H + chunk_of(dtype) - 1) / chunk_of(dtype);
@@ -550,6 +555,10 @@ int norm_lanes(int64_t H, int32_t dtype, int most) {
         if (chunks <= lanes * kHeld) return lanes;
     return most;
 }
+// Whether the gradient's lanes hold a row.  Longer ones, above 8192 in 16 bits and 4096 in fp32, are read twice by their
+// workgroup, the second time from the caches in part, and dweight's sums read both operands once more, a thread a column: 4096 x 16384 bf16 152 us,
+// without dweight 100 (1.6 times the time of one read of each and one write at 5.6 TB/s, 72); 8192 x 8192 fp32 298, 191 (144).
+// Held rows read again so: 8192 x 8192 bf16 144 us instead of 91, without dweight 90 instead of 76; 8192 x 4096 fp32 136 instead of 72.
 bool held(int64_t H, int32_t dtype) { return (H + chunk_of(dtype) - 1) / chunk_of(dtype) <= kMostBackward * kHeld; }
 // Whether rows are whole lines that no other row shares.
 bool on_lines(const void* p, int64_t ld, int64_t H, int32_t dtype) {
