@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
             most = __builtin_nanf("");
         }
         const float unit = inverse_rms(ss, (float)g.H, g.eps, f), inv = unit * f;
-        float before = I8 ? 1.0f : inv, top = 1.0f, by = 1.0f;
+        float before = I8 ? 1.0f : inv, top = 1.0f, by = 1.0f, down = 1.0f;
         bool whole = true, live = false;  // whole: what is held is what the results are made of
         if constexpr (I8) {
             // The codes are those of s w, as the row's i cancels, or of s i w where s w may be out of range: beyond it, or
@@ -297,9 +297,9 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
                 }
                 across(most, Most());
                 a = most;
-                const float down = most < 0x1p120f ? 1.0f : 0x1p-8f;  // 127 times a value stays in range
-                before = inv * down;
+                down = most < 0x1p120f ? 1.0f : 0x1p-8f;  // 127 times a value stays in range
                 most *= down;
+                before = inv;
                 whole = false;
             }
             live = a >= kTiny && a < __builtin_inff();
@@ -358,6 +358,9 @@ __global__ __launch_bounds__(kThreads<TPR>) void rms_norm_kernel(NormArgs g) {
         for (int64_t c = lane + (whole ? kHeld * TPR : 0); c < chunks; c += TPR) {
             float s[N], t[N];
             again(c, before, s, t);
+            if (I8 && !whole)
+#pragma unroll
+                for (int i = 0; i < N; ++i) t[i] *= down;
             out(c, t);
         }
     }

@@ -198,3 +198,13 @@ def test_equal_values_of_a_row_have_equal_norms(H):
                      lambda x: sp.rms_norm_backward(x, x, w, eps=1.0)[0], lambda x: sp.rms_norm_backward(x, x, w, dsum=x, eps=1.0)[0]):
             y = call(x)
             assert torch.equal(y, y[:, :1].expand(rows, H)) and torch.equal(call(beside), y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_into_int8_of_the_largest_rows_under_large_weights(dtype):
+    """1 / rms is near fp32's smallest normal numbers, and the norm near the largest."""
+    for H in LENGTHS:
+        rng = rng_for("codes, largest", dtype, H)
+        x = tensor(rng.uniform(0.25, 1, (6, H)) * rng.choice([-1, 1], (6, H)) * 2.0 ** np.array([127, 126, 125, 120, 118, 110])[:, None], dtype)
+        for scale in (2.0 ** 118, 2.0 ** 121, 2.0 ** 125):
+            check_codes(x, tensor(rng.uniform(0.9, 1.1, H) * scale, "f32"), 0.0, (dtype, H, scale))
