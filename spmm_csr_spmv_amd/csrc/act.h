@@ -13,7 +13,7 @@ namespace spx {
 constexpr float kGelu = 1.5957691216057308f;            // 2 sqrt(2 / pi)
 constexpr float kGelu3 = 1.5957691216057308f * 0.044715f;
 
-// Where exp(-p) overflows sig is 0, and so is a (its limit), not NaN.
+// Where exp(-p) overflows sig is 0, and so is a of a finite g (its limit), not NaN.
 __device__ __forceinline__ float gate_sig(float g, int act) {
 #pragma clang fp contract(off)
     const float p = act == SP_ACT_SILU ? g : g * fmaf(kGelu3, g * g, kGelu);
