@@ -12,8 +12,9 @@ from test_gpu_moe import TYPES, rng_for, rows_tensor
 
 pytestmark = pytest.mark.gpu
 
-# S, tokens, slots, E, N, K: few tiles, sums in parts, tiles of 256 x 256, short rows
-CASES = [(90, 30, 3, 4, 40, 72), (70, 70, 1, 3, 5, 7), (9000, 4500, 2, 1, 136, 136), (6000, 6000, 1, 16, 1024, 1024)]
+# S, tokens, slots, E, N, K: few tiles, short rows, sums in parts, tiles of 256 x 256, those in parts, one step a tile
+CASES = [(90, 30, 3, 4, 40, 72), (70, 70, 1, 3, 5, 7), (9000, 4500, 2, 1, 136, 136), (6000, 6000, 1, 16, 1024, 1024),
+         (20000, 10000, 2, 1, 264, 1848), (400, 50, 8, 40, 64, 64)]
 
 
 def inputs(case, dtype, layout, gated):
